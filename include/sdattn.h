@@ -47,7 +47,8 @@ typedef enum {
     SDA_DTYPE_UINT8 = 3,      /* raw bytes; an FP8 cache may be passed as uint8        */
     SDA_DTYPE_INT32 = 4,
     SDA_DTYPE_BOOL = 5,       /* one byte, nonzero = true                              */
-    SDA_DTYPE_FP32 = 6
+    SDA_DTYPE_FP32 = 6,
+    SDA_DTYPE_INT64 = 7
 } sda_dtype;
 
 /* A strided view of device memory.  Unused trailing shape/stride entries are
@@ -64,6 +65,8 @@ typedef struct {
 #define SDA_FLAG_BOUNDS  0x1u  /* a region id < -1, a table column past the table width, or a
                                   table entry outside [0, pages) was met; that piece was skipped */
 #define SDA_FLAG_TIMEOUT 0x2u  /* a pipeline wait exceeded its limit; the row's output is invalid */
+#define SDA_FLAG_FULL    0x4u  /* sparse_decode_plan_step: free pages or token rows ran out, some
+                                  requests got nothing this step */
 
 /*
  * Split count per row: start at 1 and double while below 32 and
@@ -257,6 +260,157 @@ sda_status sparse_decode_summary_scores(const sda_tensor *query, const sda_tenso
                                         const sda_tensor *scores, const sda_tensor *current,
                                         const sda_tensor *lengths, void *workspace,
                                         size_t workspace_bytes, void *stream);
+
+/*
+ * Tables of a step, built on the GPU from request lengths: which pages the new
+ * tokens take, the block table with them, and each new token's slot, position
+ * and request - what sparse_decode_rope_append writes by and the attention
+ * entry points read by.  No counterpart on the pages, whose serving engine
+ * builds these on the host.
+ *
+ *   context_lens  [Q] int32: tokens of each request already in the cache.
+ *   new_lens      [Q] int32: tokens the step adds; 0 leaves the request out;
+ *                 -1 releases it: its ceil(context / B) pages go back and its
+ *                 length becomes 0 (its table entries stay as they were).
+ *   block_size    B, tokens per page.
+ *   free_pages    [F] int32, a ring of free page ids (read and written).
+ *   free_state    [2] int32: the ring's first free entry and how many are free.
+ *   free_next     [2] int32 (written): the same after the step; may be
+ *                 free_state itself.
+ *   block_table   [Q, W] int32, stride[1] == 1, rows that do not overlap (read
+ *                 and written): the columns of the pages taken are written.
+ *   seq_lens      [Q] int32 (written): lengths after the step; may be
+ *                 context_lens itself (same stride).
+ *   token_starts  [Q + 1] int32 (written): the first token row of each request,
+ *                 and the number of token rows used.
+ *   slots         [T] int64 (written): page * B + offset of each token row.
+ *   positions     [T] int32 (written): the token's position in its request.
+ *   requests      [T] int32 (written): the token's request.
+ *                 Rows past the last token get -1 in all three.
+ *   workspace     >= 256 bytes, 256-byte aligned, zeroed once before first use;
+ *                 receives the flags below.  Calls that overlap on the GPU
+ *                 must not share one.
+ * Pages are taken from the ring in the order of the requests and of their
+ * columns, token rows likewise, so the result is a function of the inputs
+ * alone.  A request whose pages or rows do not fit gets nothing and keeps its
+ * length, as do those after it that need what ran out (SDA_FLAG_FULL).
+ * Pages released in a step go behind the ring's last free entry and can be
+ * taken by the next step.  A request outside the contract (a negative context,
+ * new_lens below -1, more pages than W, a ring with no room for what it
+ * returns) is left out with SDA_FLAG_BOUNDS, as is a whole ring whose
+ * free_state is out of range; a table entry below 0 under a partly filled page
+ * gives slot -1 with the same flag.
+ * All but the per-request vectors have stride 1.  Returns SDA_ERR_INVALID for
+ * shapes, dtypes or strides outside this contract, SDA_ERR_UNSUPPORTED for
+ * Q > 8192 or F or T above 2^30, SDA_ERR_WORKSPACE for a bad workspace,
+ * SDA_ERR_CUDA if the launch failed.
+ */
+sda_status sparse_decode_plan_step(const sda_tensor *context_lens, const sda_tensor *new_lens,
+                                   int block_size, const sda_tensor *free_pages,
+                                   const sda_tensor *free_state, const sda_tensor *free_next,
+                                   const sda_tensor *block_table, const sda_tensor *seq_lens,
+                                   const sda_tensor *token_starts, const sda_tensor *slots,
+                                   const sda_tensor *positions, const sda_tensor *requests,
+                                   void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Rotary positions with one to four axes (text; time, height and width of
+ * images and video), and the new keys and values written to their slots of the
+ * packed cache.  The pages' model does both before it calls the attention
+ * above; they print neither.
+ *
+ * Frequency pair i of a head, elements (a, b), turns by the angle
+ * t = positions[axis(i), token] * inv_freq[i]:
+ *     a' = amplitude * (a cos t - b sin t),  b' = amplitude * (b cos t + a sin t)
+ * over the first 2 * len(inv_freq) dims; the others pass through.  The angle
+ * is reduced exactly (in 64-bit fixed point), so far positions lose nothing;
+ * the products are fp32, each output is rounded once.
+ *
+ *   query       [T, Hq, D] bf16 or NULL; query_out (written) the same shape;
+ *               query_out may be query itself, else they must not overlap.
+ *   key, value  [T, G, D] bf16, or both NULL (then cache and slots may be
+ *               NULL; slots, when given, still mark padding).
+ *   positions   [A, T] int32, A in 1..4, any strides (0 included); or NULL: no
+ *               rotation, inv_freq is ignored.  Negative positions turn
+ *               backwards.
+ *   inv_freq    [R] fp32, stride 1, finite; 2R a multiple of 16, 2R <= D.
+ *   sections    A ints whose sum is R, or NULL with A == 1: pairs per axis.
+ *   interleaved_axes  zero: the first sections[0] pairs turn by axis 0, the
+ *               next sections[1] by axis 1, ...  Nonzero: pair i turns by axis
+ *               a = i % A while i / A < sections[a], a > 0; the others by axis 0
+ *               (sections[a] <= ceil((R - a) / A) for a > 0).
+ *   adjacent_pairs    zero: pair i is dims (i, i + R); nonzero: dims (2i, 2i + 1).
+ *   amplitude   factor on the turned dims (1 for plain rotary positions).
+ *   slots       [T] int64, stride 1: page * B + offset; -1 marks a padding row:
+ *               nothing of it is read, and its query_out row is left as it was.
+ *               A slot outside the cache leaves its row out with
+ *               SDA_FLAG_BOUNDS.  Two rows must not name the same slot (its
+ *               contents would be a mix of the two).
+ *   cache       [pages, G, B, 2D] bf16, FP8_E4M3 or UINT8, K first then V
+ *               (written at the slots only): K turned, V as it is.  FP8:
+ *               e4m3(x / scale), rounded to nearest even, saturated at 448.
+ *   k_scale, v_scale  device fp32 scalars; required for an FP8 cache.
+ *   workspace   NULL, or >= 256 bytes, 256-byte aligned: receives the flag.
+ * D is a multiple of 16 up to 512.  stride[2] == 1 (cache: stride[3] == 1);
+ * the bases and the other byte strides are multiples of 16, else
+ * SDA_ERR_UNSUPPORTED.  Returns SDA_ERR_INVALID for shapes, dtypes or strides
+ * outside this contract, SDA_ERR_WORKSPACE for a bad workspace, SDA_ERR_CUDA if
+ * the launch failed; T == 0 returns SDA_OK with no launch.
+ */
+sda_status sparse_decode_rope_append(const sda_tensor *query, const sda_tensor *query_out,
+                                     const sda_tensor *key, const sda_tensor *value,
+                                     const sda_tensor *positions, const sda_tensor *inv_freq,
+                                     const int32_t *sections, int interleaved_axes, int adjacent_pairs,
+                                     float amplitude, const sda_tensor *slots, const sda_tensor *cache,
+                                     const float *k_scale, const float *v_scale, void *workspace,
+                                     size_t workspace_bytes, void *stream);
+
+/*
+ * Bytes of workspace sparse_decode_paged_attention needs for query rows of
+ * `heads` heads, `query_len` tokens a request and head size `head_dim`: a
+ * 256-byte header (device error flags), the join tasks, and fp32 partial
+ * outputs and log-sum-exps of the pieces of requests that CTAs share.  It
+ * depends on no batch size or length.  Returns 0 for arguments out of range.
+ */
+size_t sparse_decode_paged_workspace_bytes(int heads, int query_len, int head_dim);
+
+/*
+ * Attention of each request's newest query_len tokens over its whole paged
+ * cache (the layers that neither select regions nor slide a window).
+ *
+ *   query        [rows, H, D] bf16, stride[2] == 1; rows = tokens * G, row r is
+ *                KV group r % G of token r / G; D in {64, 128, 192, 256};
+ *                H * query_len <= 64.
+ *   cache        [pages, G, B, 2D] bf16, FP8_E4M3 or UINT8: K then V; as in
+ *                sparse_decode_attention.  B a multiple of 8.
+ *   block_table  [requests, W] int32, stride[1] == 1.
+ *   seq_lens     [requests] int32: tokens of each request, the query_len being
+ *                decoded included.  Token j sits at seq_lens - query_len + j and
+ *                sees tokens 0..that position; a token below position 0 sees
+ *                nothing: its output is +0.0 and its lse -inf.  seq_lens < 0
+ *                marks a padding request: its rows are left as they were.
+ *   output       [rows, H, D] bf16, stride[2] == 1 (written).
+ *   lse          NULL, or [rows, H] fp32 (written): natural log-sum-exp of the
+ *                row's scaled logits, for joining with attention over other keys.
+ *   scale, query_len, k_scale, v_scale, gate, stream: as in
+ *                sparse_decode_attention (the gate does not enter lse).
+ *   workspace    >= sparse_decode_paged_workspace_bytes(H, query_len, D) bytes,
+ *                256-byte aligned, its header zeroed once before first use.
+ *                Calls that overlap on the GPU must not share one.
+ * The cache tiles of all requests are dealt out evenly over the GPU whatever
+ * the lengths, on the device, so the call can be captured in a graph; the
+ * pieces of a request are joined by their log-sum-exps in a fixed order, so
+ * equal inputs give equal bits.  What masked or unused cache places hold (NaN
+ * included) does not reach the output.  A length past the table (W * B) or a
+ * table entry outside the cache raises SDA_FLAG_BOUNDS and is left out.
+ * Errors as for sparse_decode_attention.
+ */
+sda_status sparse_decode_paged_attention(const sda_tensor *query, const sda_tensor *cache,
+                                         const sda_tensor *block_table, const sda_tensor *seq_lens,
+                                         const sda_tensor *output, const sda_tensor *lse, float scale,
+                                         int query_len, const float *k_scale, const float *v_scale,
+                                         const sda_tensor *gate, void *workspace, size_t workspace_bytes,
+                                         void *stream);
 
 /*
  * Reads the device error flags (SDA_FLAG_*) from a workspace into *flags,

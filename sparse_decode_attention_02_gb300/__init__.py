@@ -7,16 +7,21 @@ load the library; the first call does, and raises if it is not built.
 """
 from ._binding import (  # noqa: F401
     FLAG_BOUNDS,
+    FLAG_FULL,
     FLAG_TIMEOUT,
     SdaError,
     declared_functions,
     default_workspace,
     load,
     no_alloc_read_errors,
+    paged_workspace_bytes,
     read_errors,
     set_wait_limit_ns,
     sparse_decode_attention,
     sparse_decode_attention_no_alloc,
+    sparse_decode_paged_attention,
+    sparse_decode_plan_step,
+    sparse_decode_rope_append,
     sparse_decode_select_regions,
     sparse_decode_splits,
     sparse_decode_summary_scores,

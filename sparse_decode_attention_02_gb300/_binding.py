@@ -11,6 +11,7 @@ import contextlib
 import ctypes
 import os
 import re
+import struct
 import threading
 
 import torch
@@ -22,6 +23,7 @@ HEADER = os.path.join(os.path.dirname(_HERE), "include", "sdattn.h")
 SDA_OK, SDA_ERR_INVALID, SDA_ERR_UNSUPPORTED, SDA_ERR_WORKSPACE, SDA_ERR_CUDA, SDA_ERR_TIMEOUT, SDA_ERR_BOUNDS = range(7)
 FLAG_BOUNDS = 0x1
 FLAG_TIMEOUT = 0x2
+FLAG_FULL = 0x4
 
 _DTYPES = {
     torch.bfloat16: 1,
@@ -30,6 +32,7 @@ _DTYPES = {
     torch.int32: 4,
     torch.bool: 5,
     torch.float32: 6,
+    torch.int64: 7,
 }
 
 
@@ -70,6 +73,15 @@ def _declare(lib):
     lib.sparse_decode_summary_scores.argtypes = [P, P, P, P, P, ctypes.c_int, ctypes.c_int, P, P, P,
                                                  ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
     lib.sparse_decode_summary_scores.restype = ctypes.c_int
+    V, I, F, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+    lib.sparse_decode_plan_step.argtypes = [V, V, I] + 9 * [V] + [V, Z, V]
+    lib.sparse_decode_plan_step.restype = I
+    lib.sparse_decode_rope_append.argtypes = 7 * [V] + [I, I, F] + 5 * [V] + [Z, V]
+    lib.sparse_decode_rope_append.restype = I
+    lib.sparse_decode_paged_workspace_bytes.argtypes = [I, I, I]
+    lib.sparse_decode_paged_workspace_bytes.restype = Z
+    lib.sparse_decode_paged_attention.argtypes = 6 * [V] + [F, I] + 4 * [V] + [Z, V]
+    lib.sparse_decode_paged_attention.restype = I
     lib.sparse_decode_read_errors.argtypes = [ctypes.c_void_p, ctypes.POINTER(ctypes.c_uint32),
                                               ctypes.c_int, ctypes.c_void_p]
     lib.sparse_decode_read_errors.restype = ctypes.c_int
@@ -135,6 +147,48 @@ def describe(t: torch.Tensor | None) -> SdaTensor | None:
         d.shape[i] = t.shape[i]
         d.stride[i] = t.stride(i)
     return d
+
+
+_DESCRIPTOR_BYTES = ctypes.sizeof(SdaTensor)
+_PACKERS = (None,) + tuple(struct.Struct(f"=Qii{n}q{32 - 8 * n}x{n}q{32 - 8 * n}x") for n in range(1, 5))
+
+
+def _pack(*tensors):
+    """Descriptors of `tensors` side by side in one buffer, written without a
+    ctypes object each: (the buffer, to be kept until the call has returned; an
+    address per tensor, None for None).  Raises as `describe` and `_device_of`."""
+    raw = bytearray(_DESCRIPTOR_BYTES * len(tensors))
+    at = ctypes.addressof((ctypes.c_char * len(raw)).from_buffer(raw))
+    where = []
+    offset = 0
+    for t in tensors:
+        if t is None:
+            where.append(None)
+        else:
+            n = t.dim()
+            code = _DTYPES.get(t.dtype)
+            if code is None:
+                raise TypeError(f"unsupported dtype {t.dtype}")
+            if not 1 <= n <= 4:
+                raise ValueError("1 to 4 dimensions")
+            _PACKERS[n].pack_into(raw, offset, t.data_ptr(), code, n, *t.shape, *t.stride())
+            where.append(at + offset)
+        offset += _DESCRIPTOR_BYTES
+    return raw, where
+
+
+def _same_device(tensors, stream) -> torch.device:
+    """`_device_of`, quick where all is well."""
+    index = -1
+    for t in tensors:
+        if t is not None:
+            i = t.get_device()
+            if i < 0 or (index >= 0 and i != index):
+                return _device_of(*tensors, stream=stream)
+            index = i
+    if index < 0 or stream is not None:
+        return _device_of(*tensors, stream=stream)
+    return torch.device("cuda", index)
 
 
 def _ref(d):
@@ -313,6 +367,122 @@ def sparse_decode_summary_scores(query, weights, summaries, block_table, seq_len
     if rc != SDA_OK:
         raise SdaError(rc, lib.sparse_decode_status_string(rc).decode())
     return scores
+
+
+_step_workspaces: dict = {}
+
+
+def _step_workspace(device: torch.device, handle: int, nbytes: int) -> torch.Tensor:
+    """The serving-step entries' default workspace, on the current stream: kept per
+    (device, stream) like `default_workspace`, but a capture gets one of its own,
+    zeroed in the graph, that no other graph or eager call shares."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+    key = (device, handle)
+    ws = _step_workspaces.get(key)
+    if ws is None or ws.numel() < nbytes:
+        ws = _step_workspaces[key] = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+    return ws
+
+
+def _enter(tensors, workspace, need: int, stream):
+    """What the serving-step entries share: (what the call needs kept, addresses
+    of the descriptors, device, stream handle, workspace address and bytes).  Where
+    no workspace is given, the stream's default one of at least `need` bytes."""
+    dev = _same_device((*tensors, workspace), stream)
+    keep, where = _pack(*tensors)
+    handle = (stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream
+    if workspace is None:
+        with torch.cuda.stream(stream) if stream is not None else _current(dev):
+            workspace = _step_workspace(dev, handle, need)
+    return (keep, workspace), where, dev, handle, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _check(lib, rc: int) -> None:
+    if rc != SDA_OK:
+        raise SdaError(rc, lib.sparse_decode_status_string(rc).decode())
+
+
+def sparse_decode_plan_step(context_lens, new_lens, free_pages, free_state, block_table, *, block_size: int,
+                            slots, positions=None, requests=None, seq_lens=None, token_starts=None,
+                            free_next=None, workspace: torch.Tensor | None = None,
+                            stream: torch.cuda.Stream | None = None):
+    """The tables of a step from request lengths, on the GPU: pages from the free
+    ring into `block_table`, and a slot, position and request for each row of
+    `slots`; see include/sdattn.h for the contract.
+
+    `new_lens[q]` tokens are added to request q (-1 releases it).  `slots` ([T]
+    int64) sets how many token rows there are; the other outputs are allocated if
+    None.  For a step in place pass `seq_lens=context_lens` and
+    `free_next=free_state`.  Returns (seq_lens, token_starts, slots, positions,
+    requests, free_next)."""
+    lib = load()
+    new = lambda t, n: torch.empty(n, dtype=torch.int32, device=slots.device) if t is None else t
+    positions, requests = new(positions, slots.shape[0]), new(requests, slots.shape[0])
+    seq_lens, token_starts = new(seq_lens, context_lens.shape[0]), new(token_starts, context_lens.shape[0] + 1)
+    free_next = new(free_next, 2)
+    keep, d, dev, handle, ws, wsb = _enter((context_lens, new_lens, free_pages, free_state, free_next, block_table,
+                                            seq_lens, token_starts, slots, positions, requests), workspace, 256, stream)
+    with _current(dev):
+        rc = lib.sparse_decode_plan_step(d[0], d[1], int(block_size), *d[2:], ws, wsb, handle)
+    _check(lib, rc)
+    return seq_lens, token_starts, slots, positions, requests, free_next
+
+
+def sparse_decode_rope_append(query, key, value, positions, inv_freq, slots, cache, query_out=None, *,
+                              sections=None, interleaved_axes: bool = False, adjacent_pairs: bool = False,
+                              amplitude: float = 1.0, k_scale=None, v_scale=None,
+                              workspace: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None):
+    """Rotary positions (one to four axes) on `query` into `query_out` and on `key`
+    into its slots of the paged `cache`, with `value` beside it; see
+    include/sdattn.h for the contract.
+
+    `query` may be None (keys and values only), `key` and `value` may be None
+    (queries only; `cache` is then ignored), `positions` may be None (no rotation).
+    `query_out` is allocated if None and may be `query`.  `sections`: frequency
+    pairs of each axis.  `k_scale` / `v_scale`: as in sparse_decode_attention.
+    Returns `query_out`."""
+    lib = load()
+    if query is not None and query_out is None:
+        query_out = torch.zeros_like(query) if slots is not None else torch.empty_like(query)
+    if key is None:
+        cache = None
+    keep, d, dev, handle, ws, wsb = _enter((query, query_out, key, value, positions, inv_freq, slots, cache),
+                                           workspace, 256, stream)
+    ks, _keep_k = _scale_ptr(k_scale, dev)
+    vs, _keep_v = _scale_ptr(v_scale, dev)
+    parts = None
+    if sections is not None:
+        if positions is None or len(sections) != positions.shape[0]:
+            raise ValueError("sparse_decode: a section for each axis of positions")
+        parts = (ctypes.c_int32 * len(sections))(*sections)
+    with _current(dev):
+        rc = lib.sparse_decode_rope_append(*d[:6], parts, bool(interleaved_axes), bool(adjacent_pairs),
+                                           float(amplitude), d[6], d[7], ks, vs, ws, wsb, handle)
+    _check(lib, rc)
+    return query_out
+
+
+def paged_workspace_bytes(heads: int, query_len: int = 1, head_dim: int = 192) -> int:
+    return load().sparse_decode_paged_workspace_bytes(int(heads), int(query_len), int(head_dim))
+
+
+def sparse_decode_paged_attention(query, cache, block_table, seq_lens, output, *, scale: float,
+                                  query_len: int = 1, k_scale=None, v_scale=None, gate=None, lse=None,
+                                  workspace: torch.Tensor | None = None,
+                                  stream: torch.cuda.Stream | None = None) -> None:
+    """Attention of each request's newest `query_len` tokens over its whole paged
+    cache into `output`, and the rows' log-sum-exps into `lse` if given; see
+    include/sdattn.h for the contract."""
+    lib = load()
+    need = lib.sparse_decode_paged_workspace_bytes(query.shape[1], int(query_len), query.shape[-1]) or 256
+    keep, d, dev, handle, ws, wsb = _enter((query, cache, block_table, seq_lens, output, lse, gate), workspace, need,
+                                           stream)
+    ks, _keep_k = _scale_ptr(k_scale, dev)
+    vs, _keep_v = _scale_ptr(v_scale, dev)
+    with _current(dev):
+        rc = lib.sparse_decode_paged_attention(*d[:6], float(scale), int(query_len), ks, vs, d[6], ws, wsb, handle)
+    _check(lib, rc)
 
 
 def read_errors(workspace: torch.Tensor, clear: bool = False,

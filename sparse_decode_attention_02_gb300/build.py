@@ -7,7 +7,10 @@ import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SOURCES = [os.path.join(HERE, "csrc", name) for name in ("sdattn.cu", "sda_select.cu", "sda_index.cu")]
+SOURCES = [os.path.join(HERE, "csrc", name) for name in (
+    "sdattn.cu", "sda_select.cu", "sda_index.cu", "sda_plan.cu", "sda_rope.cu", "sda_paged.cu",
+    "sda_paged_64.cu", "sda_paged_128.cu", "sda_paged_192.cu", "sda_paged_256.cu")]
+INCLUDES = [os.path.join(HERE, "csrc", name) for name in ("sda_common.cuh", "sda_paged.cuh")]
 HEADER = os.path.join(ROOT, "include", "sdattn.h")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libsdattn.so")
@@ -23,7 +26,7 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
           out: str = LIB) -> str:
     """Compile the library unless it is newer than its sources; returns its path."""
     if (not force and not extra and os.path.exists(out)
-            and os.path.getmtime(out) >= max(os.path.getmtime(x) for x in [*SOURCES, HEADER])):
+            and os.path.getmtime(out) >= max(os.path.getmtime(x) for x in [*SOURCES, *INCLUDES, HEADER])):
         return out
     os.makedirs(os.path.dirname(out), exist_ok=True)
     tmp = out + f".tmp{os.getpid()}"

@@ -1,0 +1,337 @@
+// Host side of the paged attention, and the kernel that joins the pieces of a
+// request that several CTAs computed.
+#include "sda_paged.cuh"
+
+#include <cmath>
+#include <cstring>
+#include <mutex>
+
+namespace {
+
+using namespace sda;
+using namespace sda::paged;
+
+// ---------------------------------------------------------------------------
+// Join kernel: a CTA a (task, query row).  With partial outputs O_k and their
+// log-sum-exps L_k, o = sum_k e^(L_k - M) O_k / sum_k e^(L_k - M), L = M + log of
+// that sum.  A request alone on the GPU leaves one piece per CTA, so the
+// pieces are dealt over the block's thread groups, which add up through shared
+// memory in a fixed order.
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ float warp_max(float v)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        v = fmaxf(v, __shfl_xor_sync(~0u, v, o));
+    return v;
+}
+
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        v += __shfl_xor_sync(~0u, v, o);
+    return v;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) sda_paged_join_kernel(const __grid_constant__ Params p)
+{
+    constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes, kUnroll = 4;
+    __shared__ float4 sums[kGroups][kLanes];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int4 task = p.tasks[blockIdx.x];
+    const int n = task.x, r = blockIdx.y;
+    if (n == 0)
+        return;
+    const int H = p.heads, j = r / H, h = r - j * H;
+    const int64_t row = (static_cast<int64_t>(task.y) * p.query_len + j) * p.groups + task.z;
+    // piece k: the first CTA's part goes on, the others' continues it
+    auto piece = [&](int k) { return (static_cast<int64_t>(task.w) + k) * 2 + (k == 0 ? 1 : 0); };
+    auto lse_of = [&](int k) { return p.part_lse[piece(k) * p.rows + r]; };
+
+    const int lane = threadIdx.x & 31;
+    float M = -INFINITY;
+    for (int k = lane; k < n; k += 32)
+        M = fmaxf(M, lse_of(k));
+    M = warp_max(M);
+    const float ref = M == -INFINITY ? 0.0f : M;
+    float W = 0.0f;
+    for (int k = lane; k < n; k += 32)
+        W += exp2f(lse_of(k) - ref);
+    W = warp_sum(W);
+
+    const int grp = threadIdx.x / kLanes, d = threadIdx.x % kLanes;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (grp < kGroups) {
+        for (int k0 = grp; k0 < n; k0 += kGroups * kUnroll) {
+            float4 v[kUnroll];
+            float w[kUnroll];
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const int k = k0 + u * kGroups;
+                w[u] = k < n ? lse_of(k) : -INFINITY;
+                v[u] = k < n ? *reinterpret_cast<const float4 *>(p.partial + (piece(k) * p.rows + r) * D + 4 * d)
+                             : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const float f = exp2f(w[u] - ref);
+                acc.x += f * v[u].x;
+                acc.y += f * v[u].y;
+                acc.z += f * v[u].z;
+                acc.w += f * v[u].w;
+            }
+        }
+        sums[grp][d] = acc;
+    }
+    __syncthreads();
+    if (grp != 0)
+        return;
+#pragma unroll
+    for (int k = 1; k < kGroups; ++k) {
+        const float4 v = sums[k][d];
+        acc.x += v.x;
+        acc.y += v.y;
+        acc.z += v.z;
+        acc.w += v.w;
+    }
+    const bool empty = M == -INFINITY && W == 0.0f;   // a row that saw no token; NaN goes through
+    float f = empty ? 0.0f : 1.0f / W;
+    if (!empty && p.v_scale)
+        f *= *p.v_scale;
+    if (p.gate)
+        f *= gate_factor(p.gate[(static_cast<int64_t>(task.y) * p.query_len + j) * p.g_s0 +
+                                static_cast<int64_t>(task.z * H + h) * p.g_s1]);
+    uint16_t *dst = p.output + row * p.o_s0 + h * p.o_s1 + 4 * d;
+    const uint2 w = make_uint2(pack_bf16(acc.x * f, acc.y * f), pack_bf16(acc.z * f, acc.w * f));
+    if (p.o_vec) {
+        *reinterpret_cast<uint2 *>(dst) = w;
+    } else {
+        dst[0] = static_cast<uint16_t>(w.x);
+        dst[1] = static_cast<uint16_t>(w.x >> 16);
+        dst[2] = static_cast<uint16_t>(w.y);
+        dst[3] = static_cast<uint16_t>(w.y >> 16);
+    }
+    if (p.lse && d == 0)
+        p.lse[row * p.l_s0 + h * p.l_s1] = empty ? -INFINITY : (M + log2f(W)) * kLn2;
+}
+
+// ---------------------------------------------------------------------------
+// Host
+// ---------------------------------------------------------------------------
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
+                                   CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                                   CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn()
+{
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(ptr);
+    });
+    return fn;
+}
+
+bool dim_ok(int64_t d)
+{
+    return d == 64 || d == 128 || d == 192 || d == 256;
+}
+
+size_t align256(size_t n)
+{
+    return (n + 255) & ~static_cast<size_t>(255);
+}
+
+// A CTA takes at least this many tiles before the line is cut finer.
+constexpr int kMinTiles = 2;
+// Units of at most this many tiles (by the table's width) are never cut.
+constexpr int kWholeTiles = 8;
+
+}  // namespace
+
+extern "C" size_t sparse_decode_paged_workspace_bytes(int heads, int query_len, int head_dim)
+{
+    if (heads < 1 || query_len < 1 || heads > kMaxRows || query_len > kMaxRows || heads * query_len > kMaxRows ||
+        !dim_ok(head_dim))
+        return 0;
+    const size_t rows = static_cast<size_t>(kMaxCtas) * 2 * heads * query_len;
+    return kHeaderBytes + align256(kTaskBytes) + rows * head_dim * sizeof(float) + align256(rows * sizeof(float));
+}
+
+extern "C" sda_status sparse_decode_paged_attention(const sda_tensor *query, const sda_tensor *cache,
+                                                    const sda_tensor *block_table, const sda_tensor *seq_lens,
+                                                    const sda_tensor *output, const sda_tensor *lse, float scale,
+                                                    int query_len, const float *k_scale, const float *v_scale,
+                                                    const sda_tensor *gate, void *workspace,
+                                                    size_t workspace_bytes, void *stream)
+{
+    // ---- Contract.
+    if (!dims_ok(query, 3) || !dims_ok(cache, 4) || !dims_ok(block_table, 2) || !dims_ok(seq_lens, 1) ||
+        !dims_ok(output, 3))
+        return SDA_ERR_INVALID;
+    const int64_t rows = query->shape[0], heads = query->shape[1], dim = query->shape[2];
+    if (query->dtype != SDA_DTYPE_BF16 || output->dtype != SDA_DTYPE_BF16 ||
+        block_table->dtype != SDA_DTYPE_INT32 || seq_lens->dtype != SDA_DTYPE_INT32)
+        return SDA_ERR_INVALID;
+    const bool fp8 = is_fp8(cache);
+    if (!fp8 && cache->dtype != SDA_DTYPE_BF16)
+        return SDA_ERR_INVALID;
+    if (cache->shape[3] != 2 * dim || output->shape[0] != rows || output->shape[1] != heads ||
+        output->shape[2] != dim)
+        return SDA_ERR_INVALID;
+    if (query->stride[2] != 1 || output->stride[2] != 1 || cache->stride[3] != 1 || block_table->stride[1] != 1)
+        return SDA_ERR_INVALID;
+    if (!dim_ok(dim) || heads < 1 || heads > kMaxRows)
+        return SDA_ERR_UNSUPPORTED;
+    if (query_len < 1 || !std::isfinite(scale) || (fp8 && (!k_scale || !v_scale)))
+        return SDA_ERR_INVALID;
+    if (heads * query_len > kMaxRows)
+        return SDA_ERR_UNSUPPORTED;
+    const int64_t pages = cache->shape[0], groups = cache->shape[1], block = cache->shape[2];
+    const int64_t requests = seq_lens->shape[0];
+    if (groups < 1 || block < 1 || pages < 1 || rows % (groups * query_len) != 0 ||
+        rows / (groups * query_len) != requests || block_table->shape[0] < requests)
+        return SDA_ERR_INVALID;
+    const bool gated = given(gate);
+    if (gated && (!dims_ok(gate, 2) || gate->dtype != SDA_DTYPE_BF16 || gate->shape[0] != rows / groups ||
+                  gate->shape[1] != groups * heads))
+        return SDA_ERR_INVALID;
+    const bool with_lse = given(lse);
+    if (with_lse && (!dims_ok(lse, 2) || lse->dtype != SDA_DTYPE_FP32 || lse->shape[0] != rows ||
+                     lse->shape[1] != heads || (rows > 1 && lse->stride[0] == 0) ||
+                     (heads > 1 && lse->stride[1] == 0)))
+        return SDA_ERR_INVALID;
+    if ((rows > 1 && output->stride[0] == 0) || (heads > 1 && output->stride[1] == 0))
+        return SDA_ERR_INVALID;
+    if (pages > INT32_MAX || rows > INT32_MAX / kMaxRows || block_table->shape[1] > INT32_MAX ||
+        block > (1 << 24) || groups > (1 << 16))
+        return SDA_ERR_UNSUPPORTED;
+    // A TMA box holds the longest run of tokens that fits a stage and divides the page.
+    const int elt = fp8 ? 1 : 2, row_bytes = static_cast<int>(2 * dim) * elt;
+    const int slots = stage_slots(row_bytes);
+    int piece = static_cast<int>(std::min<int64_t>(block, slots)) / 8 * 8;
+    while (piece > 0 && block % piece != 0)
+        piece -= 8;
+    if (piece == 0)
+        return SDA_ERR_UNSUPPORTED;
+    if (!aligned(cache->data, 16))
+        return SDA_ERR_UNSUPPORTED;
+    for (int i = 0; i < 3; ++i)
+        if (cache->stride[i] <= 0 || (cache->stride[i] * elt) % 16 != 0)
+            return SDA_ERR_UNSUPPORTED;
+    const size_t need = sparse_decode_paged_workspace_bytes(static_cast<int>(heads), query_len, static_cast<int>(dim));
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < need)
+        return SDA_ERR_WORKSPACE;
+    if (rows == 0)
+        return SDA_OK;
+    if (!query->data || !cache->data || !seq_lens->data || !output->data ||
+        (!block_table->data && block_table->shape[1] > 0))
+        return SDA_ERR_INVALID;
+
+    // ---- The cache as (128 bytes, token, band, group, page): a box is a piece
+    // of all bands, landing as [band][token][128 bytes], swizzled.
+    EncodeTiledFn encode = encode_fn();
+    if (!encode)
+        return SDA_ERR_CUDA;
+    CUtensorMap tmap;
+    const int bands = row_bytes / 128;
+    const cuuint64_t gdim[5] = {static_cast<cuuint64_t>(128 / elt), static_cast<cuuint64_t>(block),
+                                static_cast<cuuint64_t>(bands), static_cast<cuuint64_t>(groups),
+                                static_cast<cuuint64_t>(pages)};
+    const cuuint64_t gstride[4] = {static_cast<cuuint64_t>(cache->stride[2] * elt), 128u,
+                                   static_cast<cuuint64_t>(cache->stride[1] * elt),
+                                   static_cast<cuuint64_t>(cache->stride[0] * elt)};
+    const cuuint32_t box[5] = {static_cast<cuuint32_t>(128 / elt), static_cast<cuuint32_t>(piece),
+                               static_cast<cuuint32_t>(bands), 1, 1};
+    const cuuint32_t estride[5] = {1, 1, 1, 1, 1};
+    if (encode(&tmap, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
+               const_cast<void *>(cache->data), gdim, gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return SDA_ERR_UNSUPPORTED;
+
+    Params p = {};
+    p.query = static_cast<const uint16_t *>(query->data);
+    p.q_s0 = query->stride[0];
+    p.q_s1 = query->stride[1];
+    p.block_table = static_cast<const int32_t *>(block_table->data);
+    p.bt_s0 = block_table->stride[0];
+    p.seq_lens = static_cast<const int32_t *>(seq_lens->data);
+    p.len_s = seq_lens->stride[0];
+    p.output = static_cast<uint16_t *>(const_cast<void *>(output->data));
+    p.o_s0 = output->stride[0];
+    p.o_s1 = output->stride[1];
+    if (with_lse) {
+        p.lse = static_cast<float *>(const_cast<void *>(lse->data));
+        p.l_s0 = lse->stride[0];
+        p.l_s1 = lse->stride[1];
+    }
+    if (gated) {
+        p.gate = static_cast<const uint16_t *>(gate->data);
+        p.g_s0 = gate->stride[0];
+        p.g_s1 = gate->stride[1];
+    }
+    p.k_scale = fp8 ? k_scale : nullptr;
+    p.v_scale = fp8 ? v_scale : nullptr;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const size_t parts = static_cast<size_t>(kMaxCtas) * 2 * heads * query_len;
+    p.flags = reinterpret_cast<unsigned int *>(ws);
+    p.tasks = reinterpret_cast<int4 *>(ws + kHeaderBytes);
+    p.partial = reinterpret_cast<float *>(ws + kHeaderBytes + align256(kTaskBytes));
+    p.part_lse = p.partial + parts * dim;
+    p.pages = pages;
+    p.wait_ns = sda_wait_limit_ns();
+    p.scale = scale;
+    p.requests = static_cast<int>(requests);
+    p.groups = static_cast<int>(groups);
+    p.heads = static_cast<int>(heads);
+    p.query_len = query_len;
+    p.rows = static_cast<int>(heads) * query_len;
+    p.table_cols = static_cast<int>(block_table->shape[1]);
+    p.block = static_cast<int>(block);
+    p.cap = static_cast<int>(std::min<int64_t>(block_table->shape[1] * block, INT32_MAX));
+    p.piece = piece;
+    p.tile = slots / piece * piece;
+    auto runs_of_4 = [](const sda_tensor *t) {
+        return aligned(t->data, 8) && t->stride[0] % 4 == 0 && t->stride[1] % 4 == 0;
+    };
+    p.q_vec = runs_of_4(query);
+    p.o_vec = runs_of_4(output);
+
+    const int sms = sm_count();
+    if (sms < 1)
+        return SDA_ERR_CUDA;
+    // Tiles a request can have at most, by the table's width.
+    const int64_t units = requests * groups;
+    const int64_t widest = (p.cap + static_cast<int64_t>(p.tile) - 1) / p.tile;
+    const int most = std::min(kMaxCtas, 2 * sms);
+    p.min_tiles = kMinTiles;
+    p.whole_units = widest <= kWholeTiles;
+    const int64_t want = p.whole_units ? units : (units * widest + kMinTiles - 1) / kMinTiles;
+    p.ctas = static_cast<int>(std::min<int64_t>(most, std::max<int64_t>(1, want)));
+    p.by_unit = units <= p.ctas;
+
+    const sda_status st = dim == 64    ? launch_64(fp8, tmap, p, stream)
+                          : dim == 128 ? launch_128(fp8, tmap, p, stream)
+                          : dim == 192 ? launch_192(fp8, tmap, p, stream)
+                                       : launch_256(fp8, tmap, p, stream);
+    if (st != SDA_OK || p.whole_units)
+        return st;
+    const dim3 grid(static_cast<unsigned>(p.by_unit ? units : p.ctas), static_cast<unsigned>(p.rows));
+    auto join = dim == 64    ? sda_paged_join_kernel<64>
+                : dim == 128 ? sda_paged_join_kernel<128>
+                : dim == 192 ? sda_paged_join_kernel<192>
+                             : sda_paged_join_kernel<256>;
+    return launch_pdl(join, grid, dim3(kJoinThreads), 0, stream, p);
+}

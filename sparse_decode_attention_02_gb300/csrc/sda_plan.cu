@@ -1,0 +1,393 @@
+// A step's tables from request lengths: which pages the new tokens take, the
+// block table with them, and each new token's slot, position and request.
+//
+// With c, n the context and new length of request q and B the page size,
+//     need = ceil((c + n) / B) - ceil(c / B)
+// pages come from the free ring in the order of the requests (an exclusive
+// prefix sum of need), token rows likewise (a prefix sum of n).  Every CTA
+// computes both sums over all requests (they are small: 8 bytes a request) and
+// keeps them in shared memory; the token rows and the page entries are then
+// dealt out over the grid and find their request by binary search.  The work
+// is bound by latency for a decode step (one CTA) and by the 16 bytes written
+// per token row for prompts.
+#include "sda_common.cuh"
+
+namespace {
+
+using namespace sda;
+
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxRequests = 8192;              // five int32 arrays of them in shared memory: 160 KB
+constexpr int kQuad = 4;                        // token rows a thread writes at a time
+constexpr int kRowsPerCta = 2 * kThreads * kQuad;
+constexpr int kTicketWord = 16;                 // of the workspace header: CTAs past their reads
+
+struct PlanParams {
+    const int32_t *context, *added;
+    int64_t context_s, added_s;
+    int32_t *ring;
+    const int32_t *state;
+    int32_t *next, *table;
+    int64_t table_s0;
+    int32_t *seq_lens;
+    int64_t seq_s;
+    int32_t *starts;
+    int64_t *slots;
+    int32_t *positions, *owners;
+    unsigned int *header;
+    int requests, width, block, ring_size, rows;
+    int vec;                                    // the row outputs take 16-byte stores
+};
+
+// Sums of up to three values over the block, exclusive, in thread order.
+struct Sums {
+    long long need, back, add;
+};
+
+__device__ __forceinline__ Sums warp_inclusive(Sums v, int lane)
+{
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long a = __shfl_up_sync(~0u, v.need, o), b = __shfl_up_sync(~0u, v.back, o),
+                        c = __shfl_up_sync(~0u, v.add, o);
+        if (lane >= o) {
+            v.need += a;
+            v.back += b;
+            v.add += c;
+        }
+    }
+    return v;
+}
+
+__device__ __forceinline__ Sums block_exclusive(const Sums mine, Sums *warp_sums, Sums &total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Sums inc = warp_inclusive(mine, lane);
+    __syncthreads();                            // warp_sums may still be read from the last call
+    if (lane == 31)
+        warp_sums[warp] = inc;
+    __syncthreads();
+    const Sums w = warp_inclusive(warp_sums[lane], lane);   // kWarps == 32: a lane a warp
+    auto at = [&](long long x, int l) { return __shfl_sync(~0u, x, l); };
+    total = {at(w.need, 31), at(w.back, 31), at(w.add, 31)};
+    const int before = warp > 0 ? warp - 1 : 0;
+    Sums e = {at(w.need, before), at(w.back, before), at(w.add, before)};
+    if (warp == 0)
+        e = {0, 0, 0};
+    return {e.need + inc.need - mine.need, e.back + inc.back - mine.back, e.add + inc.add - mine.add};
+}
+
+// The last index whose value is at most x (a[0] <= x; a ascends).
+__device__ __forceinline__ int last_at_most(const int32_t *a, int n, int x)
+{
+    int lo = 0, len = n;
+    while (len > 1) {
+        const int half = len >> 1;
+        lo = a[lo + half] <= x ? lo + half : lo;
+        len -= half;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ int32_t clip32(long long x)
+{
+    return static_cast<int32_t>(min(x, static_cast<long long>(INT32_MAX)));
+}
+
+__global__ void __launch_bounds__(kThreads) sda_plan_kernel(const __grid_constant__ PlanParams p)
+{
+    extern __shared__ int32_t smem[];
+    int32_t *ctx = smem;                        // context length
+    int32_t *len = ctx + p.requests;            // new length, then the length after the step
+    int32_t *tok = len + p.requests;            // token rows before the request
+    int32_t *pag = tok + p.requests;            // pages taken before it
+    int32_t *rel = pag + p.requests;            // pages returned before it
+    __shared__ Sums warp_sums[kWarps];
+    __shared__ int granted[3];                  // token rows, pages taken, pages returned
+    __shared__ int is_last;
+
+    pdl_launch_dependents();
+    pdl_wait();
+
+    const int Q = p.requests, B = p.block;
+    const int per = (Q + kThreads - 1) / kThreads;
+    const int q0 = min(Q, static_cast<int>(threadIdx.x) * per), q1 = min(Q, q0 + per);
+    int start = p.state[0], count = p.state[1];
+    bool bad = start < 0 || start >= p.ring_size || count < 0 || count > p.ring_size;
+    if (bad)
+        start = count = 0;
+    const bool ring_ok = !bad;
+    if (threadIdx.x < 3)
+        granted[threadIdx.x] = 0;
+
+    // What request q asks for: pages it needs, pages it returns, rows it adds.
+    // Requests outside the contract ask for nothing and raise the flag.
+    auto asks = [&](int c, int n, Sums &s) {
+        s = {0, 0, 0};
+        const long long have = (static_cast<long long>(max(c, 0)) + B - 1) / B;
+        if (n == 0 && c >= 0)
+            return true;
+        if (c < 0 || n < -1 || have > p.width)
+            return false;
+        if (n == -1) {
+            s.back = have;
+            return true;
+        }
+        const long long end = (static_cast<long long>(c) + n + B - 1) / B;
+        if (end > p.width || static_cast<long long>(c) + n > INT32_MAX)
+            return false;
+        s.need = end - have;
+        s.add = n;
+        return true;
+    };
+
+    Sums mine = {0, 0, 0};
+    for (int q = q0; q < q1; ++q) {
+        const int c = p.context[q * p.context_s], n = p.added[q * p.added_s];
+        Sums s;
+        bad = !asks(c, n, s) || bad;
+        ctx[q] = c;
+        len[q] = n;
+        mine.need += s.need;
+        mine.back += s.back;
+        mine.add += s.add;
+    }
+    Sums total;
+    Sums run = block_exclusive(mine, warp_sums, total);
+    if (total.need > count) {
+        // Not all pages are there: rows count only for requests whose pages are.
+        long long need = run.need, add = 0;
+        for (int q = q0; q < q1; ++q) {
+            Sums s;
+            asks(ctx[q], len[q], s);
+            need += s.need;
+            add += s.need == 0 || need <= count ? s.add : 0;
+        }
+        Sums t2;
+        run.add = block_exclusive({0, 0, add}, warp_sums, t2).add;
+    }
+
+    // Grants, in the order of the requests: pages and rows both have to fit.
+    // Refusals close a sum's tail, so the granted parts are its beginning.
+    bool full = false;
+    int top[3] = {0, 0, 0};
+    for (int q = q0; q < q1; ++q) {
+        const int c = ctx[q], n = len[q];
+        Sums s;
+        asks(c, n, s);
+        tok[q] = clip32(run.add);
+        pag[q] = clip32(run.need);
+        rel[q] = clip32(run.back);
+        run.need += s.need;
+        run.back += s.back;
+        int after = c;
+        if (s.add > 0) {
+            bool ok = s.need == 0 || run.need <= count;
+            run.add += ok ? s.add : 0;
+            ok = ok && run.add <= p.rows;
+            if (ok) {
+                after = c + n;
+                top[0] = static_cast<int>(run.add);
+                top[1] = s.need > 0 ? static_cast<int>(run.need) : top[1];
+            }
+            full = full || !ok;
+        } else if (n == -1 && c >= 0 && (s.back > 0 || c == 0)) {
+            const bool ok = ring_ok && count + run.back <= p.ring_size;
+            if (ok) {
+                after = 0;
+                top[2] = static_cast<int>(run.back);
+            }
+            bad = bad || !ok;
+        }
+        len[q] = after;
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        const int m = __reduce_max_sync(~0u, top[k]);
+        if ((threadIdx.x & 31) == 0 && m > 0)
+            atomicMax(&granted[k], m);
+    }
+    const unsigned flags = (bad ? SDA_FLAG_BOUNDS : 0u) | (full ? SDA_FLAG_FULL : 0u);
+    const unsigned any = __reduce_or_sync(~0u, flags);
+    if ((threadIdx.x & 31) == 0 && any)
+        atomicOr(p.header, any);
+    __syncthreads();
+    const int rows = granted[0], taken = granted[1], returned = granted[2];
+
+    // The lengths and the ring's state may be updated in place, so they are
+    // written by whichever CTA is the last to have read them.
+    if (gridDim.x > 1) {
+        if (threadIdx.x == 0) {
+            const unsigned t = atomicAdd(p.header + kTicketWord, 1u);
+            is_last = t == gridDim.x - 1;
+            if (is_last)
+                p.header[kTicketWord] = 0;
+        }
+        __syncthreads();
+    }
+    if (gridDim.x == 1 || is_last) {
+        for (int q = threadIdx.x; q < Q; q += kThreads) {
+            p.seq_lens[q * p.seq_s] = len[q];
+            p.starts[q] = min(tok[q], rows);
+        }
+        if (threadIdx.x == 0) {
+            p.starts[Q] = rows;
+            if (ring_ok) {
+                p.next[0] = static_cast<int>((static_cast<long long>(start) + taken) % p.ring_size);
+                p.next[1] = count - taken + returned;
+            } else {
+                const int s0 = p.state[0], s1 = p.state[1];
+                p.next[0] = s0;
+                p.next[1] = s1;
+            }
+        }
+    }
+
+    const int first = blockIdx.x * kThreads + threadIdx.x, step = gridDim.x * kThreads;
+    // index into the ring: i < 2 * ring_size
+    auto ring_at = [&](long long i) { return i >= p.ring_size ? i - p.ring_size : i; };
+
+    // ---- Token rows, four at a time: one search, then a walk.
+    for (int r0 = first * kQuad; r0 < p.rows && r0 >= 0; r0 += step * kQuad) {
+        long long slot[kQuad];
+        int pos[kQuad], own[kQuad];
+        int q = r0 < rows ? last_at_most(tok, Q, r0) : 0;
+        int page = -1, column = -1;
+#pragma unroll
+        for (int k = 0; k < kQuad; ++k) {
+            const int r = r0 + k;
+            slot[k] = -1;
+            pos[k] = own[k] = -1;
+            if (r < rows) {
+                while (q + 1 < Q && tok[q + 1] <= r) {
+                    ++q;
+                    column = -1;
+                }
+                const int c = ctx[q];
+                pos[k] = c + (r - tok[q]);
+                own[k] = q;
+                const int col = pos[k] / B;
+                if (col != column) {
+                    const int have = static_cast<int>((static_cast<long long>(c) + B - 1) / B);
+                    page = col < have ? p.table[q * p.table_s0 + col]
+                                      : p.ring[ring_at(static_cast<long long>(start) + pag[q] + (col - have))];
+                    column = col;
+                }
+                if (page >= 0)
+                    slot[k] = static_cast<long long>(page) * B + (pos[k] - col * B);
+                else
+                    atomicOr(p.header, SDA_FLAG_BOUNDS);
+            }
+        }
+        if (p.vec && r0 + kQuad <= p.rows) {
+            longlong2 *s2 = reinterpret_cast<longlong2 *>(p.slots + r0);
+            s2[0] = make_longlong2(slot[0], slot[1]);
+            s2[1] = make_longlong2(slot[2], slot[3]);
+            *reinterpret_cast<int4 *>(p.positions + r0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+            *reinterpret_cast<int4 *>(p.owners + r0) = make_int4(own[0], own[1], own[2], own[3]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kQuad; ++k)
+                if (r0 + k < p.rows) {
+                    p.slots[r0 + k] = slot[k];
+                    p.positions[r0 + k] = pos[k];
+                    p.owners[r0 + k] = own[k];
+                }
+        }
+    }
+
+    // ---- Pages taken: their table columns.
+    for (int i = first; i < taken; i += step) {
+        const int q = last_at_most(pag, Q, i);
+        const int have = static_cast<int>((static_cast<long long>(ctx[q]) + B - 1) / B);
+        p.table[q * p.table_s0 + have + (i - pag[q])] = p.ring[ring_at(static_cast<long long>(start) + i)];
+    }
+    // ---- Pages returned: behind the ring's last free page.
+    for (int i = first; i < returned; i += step) {
+        const int q = last_at_most(rel, Q, i);
+        const long long at = static_cast<long long>(start) + count + i;       // < 2 * ring_size: they fit
+        p.ring[ring_at(at)] = p.table[q * p.table_s0 + (i - rel[q])];
+    }
+}
+
+}  // namespace
+
+extern "C" sda_status sparse_decode_plan_step(const sda_tensor *context_lens, const sda_tensor *new_lens,
+                                              int block_size, const sda_tensor *free_pages,
+                                              const sda_tensor *free_state, const sda_tensor *free_next,
+                                              const sda_tensor *block_table, const sda_tensor *seq_lens,
+                                              const sda_tensor *token_starts, const sda_tensor *slots,
+                                              const sda_tensor *positions, const sda_tensor *requests,
+                                              void *workspace, size_t workspace_bytes, void *stream)
+{
+    const sda_tensor *vec[] = {context_lens, new_lens, free_pages, free_state, free_next, seq_lens,
+                               token_starts, positions, requests};
+    for (const sda_tensor *t : vec)
+        if (!dims_ok(t, 1) || t->dtype != SDA_DTYPE_INT32)
+            return SDA_ERR_INVALID;
+    if (!dims_ok(block_table, 2) || block_table->dtype != SDA_DTYPE_INT32 || !dims_ok(slots, 1) ||
+        slots->dtype != SDA_DTYPE_INT64)
+        return SDA_ERR_INVALID;
+    const int64_t Q = context_lens->shape[0], rows = slots->shape[0], ring = free_pages->shape[0];
+    if (new_lens->shape[0] != Q || block_table->shape[0] != Q || seq_lens->shape[0] != Q ||
+        token_starts->shape[0] != Q + 1 || positions->shape[0] != rows || requests->shape[0] != rows ||
+        free_state->shape[0] != 2 || free_next->shape[0] != 2 || ring < 1 || block_size < 1)
+        return SDA_ERR_INVALID;
+    const sda_tensor *dense[] = {free_pages, free_state, free_next, token_starts, slots, positions, requests};
+    for (const sda_tensor *t : dense)
+        if (t->shape[0] > 1 && t->stride[0] != 1)
+            return SDA_ERR_INVALID;
+    if (block_table->shape[1] > 1 && block_table->stride[1] != 1)
+        return SDA_ERR_INVALID;
+    // Written tensors must not be broadcast over requests.
+    if (Q > 1 && (seq_lens->stride[0] == 0 || block_table->stride[0] < block_table->shape[1]))
+        return SDA_ERR_INVALID;
+    if (Q > kMaxRequests || ring > (1 << 30) || rows > (1 << 30) || block_table->shape[1] > INT32_MAX)
+        return SDA_ERR_UNSUPPORTED;
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < kHeaderBytes)
+        return SDA_ERR_WORKSPACE;
+    for (const sda_tensor *t : dense)
+        if (t->shape[0] > 0 && !t->data)
+            return SDA_ERR_INVALID;
+    if (Q > 0 && (!context_lens->data || !new_lens->data || !seq_lens->data ||
+                  (block_table->shape[1] > 0 && !block_table->data)))
+        return SDA_ERR_INVALID;
+
+    PlanParams p = {};
+    p.context = static_cast<const int32_t *>(context_lens->data);
+    p.context_s = context_lens->stride[0];
+    p.added = static_cast<const int32_t *>(new_lens->data);
+    p.added_s = new_lens->stride[0];
+    auto out32 = [](const sda_tensor *t) { return static_cast<int32_t *>(const_cast<void *>(t->data)); };
+    p.ring = out32(free_pages);
+    p.state = static_cast<const int32_t *>(free_state->data);
+    p.next = out32(free_next);
+    p.table = out32(block_table);
+    p.table_s0 = block_table->stride[0];
+    p.seq_lens = out32(seq_lens);
+    p.seq_s = seq_lens->stride[0];
+    p.starts = out32(token_starts);
+    p.slots = static_cast<int64_t *>(const_cast<void *>(slots->data));
+    p.positions = out32(positions);
+    p.owners = out32(requests);
+    p.header = static_cast<unsigned int *>(workspace);
+    p.requests = static_cast<int>(Q);
+    p.width = static_cast<int>(block_table->shape[1]);
+    p.block = block_size;
+    p.ring_size = static_cast<int>(ring);
+    p.rows = static_cast<int>(rows);
+    p.vec = aligned(p.slots, 16) && aligned(p.positions, 16) && aligned(p.owners, 16);
+
+    const size_t smem = 5 * sizeof(int32_t) * static_cast<size_t>(Q);
+    static size_t raised[64] = {};
+    if (smem > 48 * 1024 && !raise_smem(sda_plan_kernel, 5 * sizeof(int32_t) * kMaxRequests, raised))
+        return SDA_ERR_CUDA;
+    const int sms = sm_count();
+    if (sms < 1)
+        return SDA_ERR_CUDA;
+    // One CTA while it can write the rows in two turns; else as many as have two turns to do.
+    const int64_t want = (rows + kRowsPerCta - 1) / kRowsPerCta;
+    const int grid = static_cast<int>(want < 1 ? 1 : want < sms ? want : sms);
+    return launch_pdl(sda_plan_kernel, dim3(grid), dim3(kThreads), smem, stream, p);
+}
