@@ -50,6 +50,21 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar)
     asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(bar) : "memory");
 }
 
+// Whether the phase is over, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// As mbar_test, but the hardware may suspend the thread for a while first.
 __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity)
 {
     uint32_t ok;
@@ -70,11 +85,14 @@ __device__ __forceinline__ uint64_t global_timer_ns()
     return t;
 }
 
-// Waits for the phase of `bar` with the given parity; false after limit_ns.
+// Waits for the phase of `bar` with the given parity; false after limit_ns (at
+// once for 0).
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns)
 {
-    if (mbar_try_wait(bar, parity))
+    if (mbar_test(bar, parity))
         return true;
+    if (limit_ns == 0)
+        return false;
     const uint64_t t0 = global_timer_ns();
     for (;;) {
         if (mbar_try_wait(bar, parity))

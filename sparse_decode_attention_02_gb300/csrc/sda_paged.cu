@@ -300,7 +300,7 @@ extern "C" sda_status sparse_decode_paged_attention(const sda_tensor *query, con
     p.rows = static_cast<int>(heads) * query_len;
     p.table_cols = static_cast<int>(block_table->shape[1]);
     p.block = static_cast<int>(block);
-    p.cap = static_cast<int>(std::min<int64_t>(block_table->shape[1] * block, INT32_MAX));
+    p.cap = static_cast<int>(std::min<int64_t>(block_table->shape[1] * block, INT32_MAX - 4096));
     p.piece = piece;
     p.tile = slots / piece * piece;
     auto runs_of_4 = [](const sda_tensor *t) {

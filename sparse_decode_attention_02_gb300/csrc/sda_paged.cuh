@@ -14,26 +14,28 @@
 //     sum over seq_lens.  A unit that crosses a CTA boundary leaves a partial
 //     output and log-sum-exp per piece (at most two per CTA, so the workspace
 //     does not grow with the batch); the join kernel merges them in order.
-//   * A producer warp resolves pages (a lane a piece, the next batch's table
-//     entries in flight) and streams pieces with TMA boxes into a ring; it runs
-//     ahead over unit boundaries while the consumers finish a unit.
-//   * Four consumer warps.  Query rows (query_len x heads) are the M dimension
-//     of mma.sync in MT tiles of 16; the 4 / MT warps of a tile take alternate
-//     stages, each with its own running softmax, merged through shared memory
-//     when the unit's tiles are done.
-// Two CTAs an SM: one's prologue and unit ends hide behind the other's stream.
+//   * Four warps, each its own producer and consumer: query rows (query_len x
+//     heads) are the M dimension of mma.sync in MT tiles of 16, and the 4 / MT
+//     warps of a tile take alternate stages of a shared ring, each with its own
+//     running softmax, merged through shared memory when the unit's tiles are
+//     done.  A warp that has used up a stage issues the TMA boxes of the stage
+//     that comes into its place; it looks pages up a lane a piece, a batch
+//     ahead, and runs ahead over unit boundaries.
+// Two CTAs an SM: one's prologue and unit ends hide behind the other's stream,
+// and eight warps leave each thread the registers for a whole output row tile
+// (a producer warp apart would make it nine or ten, 168 registers, and spills).
 #pragma once
 
 #include "sda_common.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace sda {
 namespace paged {
 
-constexpr int kConsumerWarps = 4;
-constexpr int kConsumers = kConsumerWarps * 32;
-constexpr int kThreads = kConsumers + 32;
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
 constexpr int kMaxRows = 64;                    // query_len * heads
 constexpr int kMaxCtas = 304;                   // two CTAs on each of 152 SMs
 constexpr int kJoinThreads = 256;
@@ -70,19 +72,25 @@ struct Params {
     int q_vec, o_vec;                           // 8-byte loads of q and stores of the output
 };
 
+// Tokens of a stage for a cache row of `row_bytes`.
+constexpr int stage_slots(int row_bytes)
+{
+    return row_bytes <= 128 ? 64 : row_bytes <= 384 ? 32 : 16;
+}
+
 template <bool FP8, int D, int MT>
 struct Shape {
     static constexpr int kElt = FP8 ? 1 : 2;
     static constexpr int kRowBytes = 2 * D * kElt;
     static constexpr int kBands = kRowBytes / 128;
-    // Tokens of a stage: 8 to 24 KB of cache; a warp takes a whole stage.
-    static constexpr int kSlots = kRowBytes <= 256 ? 64 : kRowBytes <= 768 ? 32 : 16;
+    // Tokens of a stage: 8 to 16 KB of cache; a warp takes a whole stage.
+    static constexpr int kSlots = stage_slots(kRowBytes);
     static constexpr int kStageBytes = kSlots * kRowBytes;
     static constexpr int kSteps = D / 16;                       // QK k-steps
     static constexpr int kQBytes = kSteps * 32 * 16;            // a tile's Q fragments
     static constexpr int kChunk = D == 192 ? 48 : 32;           // output dims merged at a time
     static constexpr int kObufStride = kChunk + 4;
-    static constexpr int kObufBytes = kConsumerWarps * 16 * kObufStride * 4;
+    static constexpr int kObufBytes = kWarps * 16 * kObufStride * 4;
     // Q fragments and the merge buffer share their place: Q is dead when a
     // unit's tiles are done.
     static constexpr int kSharedBytes = MT * kQBytes > kObufBytes ? MT * kQBytes : kObufBytes;
@@ -92,11 +100,12 @@ struct Shape {
     static constexpr int kQOff = kStages * kStageBytes;
     static constexpr int kBarOff = kQOff + kSharedBytes;
     static constexpr int kHdrOff = kBarOff + 16 * kStages;
-    static constexpr int kMlOff = kHdrOff + 8 * kStages;        // [warp][16][2]
-    static constexpr int kRowOff = kMlOff + kConsumerWarps * 16 * 8;   // logit scale, gate per row
+    static constexpr int kIssuedOff = kHdrOff + 8 * kStages;
+    static constexpr int kMlOff = (kIssuedOff + 4 * kStages + 15) / 16 * 16;   // [warp][16][2]
+    static constexpr int kRowOff = kMlOff + kWarps * 16 * 8;   // logit scale, gate per row
     static constexpr int kCtlOff = kRowOff + 2 * kMaxRows * 4;
     static constexpr int kBytes = kCtlOff + 128 + 1024;         // + the base's alignment
-    static constexpr int kAlternate = kConsumerWarps / MT;      // warps of an M tile
+    static constexpr int kAlternate = kWarps / MT;      // warps of an M tile
     static_assert(kStageBytes % 1024 == 0 && kStages >= 3 && kBytes <= 115712, "ring");
     static_assert(kBarOff % 16 == 0 && kSharedBytes % 16 == 0, "alignment");
 };
@@ -162,11 +171,6 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *map
         " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
         : "memory");
-}
-
-__device__ __forceinline__ void consumer_bar()
-{
-    asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr)
@@ -373,6 +377,101 @@ __device__ __forceinline__ void find_part(const Params &p, long long *scan, int 
     w.tile = ctl[2];
 }
 
+// A warp's share of the stream: the stages it issues (every kAlternate-th of
+// the CTA's), a batch of their pieces looked up a lane a piece, and the next
+// batch's table entries on their way.  A batch lies in one segment.
+template <bool FP8, int D, int MT>
+struct Feed {
+    using S = Shape<FP8, D, MT>;
+    Walk walk;
+    Segment seg;
+    int base;                                   // number of the segment's first stage
+    int stage;                                  // the next stage to look up
+    bool more;
+    int per_stage, lane_stage, lane_piece;      // pieces of a stage; this lane's place in a batch
+    int at, n, group, page, off, left;          // the batch: next stage to issue, stages, ...
+    int n2, group2, page2, off2, left2;         // the one after
+
+    __device__ __forceinline__ void advance(const Params &p)
+    {
+        while (more && stage >= base + (seg.last - seg.first)) {
+            base += seg.last - seg.first;
+            more = walk.next(p, seg);
+        }
+    }
+
+    __device__ __forceinline__ void look_up(const Params &p)
+    {
+        n = n2;
+        group = group2;
+        page = page2;
+        off = off2;
+        left = left2;
+        at = 0;
+        n2 = 0;
+        if (!more)
+            return;
+        const int P = p.piece, per_block = p.block / P;
+        const int ahead = base + (seg.last - seg.first) - stage;       // > 0
+        n2 = min(32 / per_stage, (ahead - 1) / S::kAlternate + 1);
+        group2 = seg.group;
+        const int f = (seg.first + stage - base + lane_stage * S::kAlternate) * per_stage + lane_piece;
+        const int col = f / per_block;
+        off2 = (f - col * per_block) * P;
+        left2 = lane_stage < n2 ? seg.len - f * P : 0;  // tokens from the piece's first on
+        // a column past the table is a length past it: cut off with a flag already
+        page2 = left2 > 0 && col < p.table_cols ? p.block_table[seg.request * p.bt_s0 + col] : -1;
+        stage += n2 * S::kAlternate;
+        advance(p);
+    }
+
+    __device__ __forceinline__ void start(const Params &p, const Walk &from, int first, int lane)
+    {
+        walk = from;
+        base = 0;
+        stage = first;
+        per_stage = p.tile / p.piece;
+        lane_stage = lane / per_stage;
+        lane_piece = lane - lane_stage * per_stage;
+        more = walk.next(p, seg);
+        advance(p);
+        n2 = 0;
+        look_up(p);
+        look_up(p);
+    }
+
+    // Issues the next stage into place `slot`, if there is one.
+    __device__ __forceinline__ void issue(const Params &p, const CUtensorMap *tmap, uint32_t ring, uint32_t full,
+                                          uint64_t *hdr, int *issued, int slot, int lane)
+    {
+        if (n == 0)
+            return;
+        const uint32_t piece_bytes = static_cast<uint32_t>(p.piece) * S::kRowBytes;
+        const bool mine = lane_stage == at && left > 0;
+        const bool copy = mine && page >= 0 && page < p.pages;
+        if (mine && !copy)
+            atomicOr(p.flags, SDA_FLAG_BOUNDS);
+        const unsigned cb = __ballot_sync(~0u, copy);
+        const uint64_t bits = copy ? low_bits(min(p.piece, left)) << (lane_piece * p.piece) : 0ull;
+        const unsigned lo = __reduce_or_sync(~0u, static_cast<unsigned>(bits));
+        const unsigned hi = S::kSlots > 32 ? __reduce_or_sync(~0u, static_cast<unsigned>(bits >> 32)) : 0u;
+        if (lane == 0) {
+            hdr[slot] = (static_cast<uint64_t>(hi) << 32) | lo;
+            issued[slot] += 1;
+            if (cb)
+                mbar_expect_tx(full + 8 * slot, __popc(cb) * piece_bytes);
+        }
+        __syncwarp();
+        if (copy)
+            tma_load_5d(ring + slot * S::kStageBytes + lane_piece * piece_bytes, tmap, 0, off, 0, group, page,
+                        full + 8 * slot);
+        if (lane == 0)
+            mbar_arrive(full + 8 * slot);
+        if (++at == n)
+            look_up(p);
+    }
+};
+
 template <bool FP8, int D, int MT>
 __global__ void __launch_bounds__(kThreads, 2)
     sda_paged_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_constant__ Params p)
@@ -384,6 +483,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint32_t sbase = smem_u32(smem);
     const uint32_t full_bar = sbase + S::kBarOff, empty_bar = full_bar + 8 * S::kStages;
     uint64_t *hdr = reinterpret_cast<uint64_t *>(smem + S::kHdrOff);
+    int *issued = reinterpret_cast<int *>(smem + S::kIssuedOff);
     float *ml = reinterpret_cast<float *>(smem + S::kMlOff);
     float *row_scale = reinterpret_cast<float *>(smem + S::kRowOff);
     float *row_gate = row_scale + kMaxRows;
@@ -391,11 +491,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     long long *scan = reinterpret_cast<long long *>(smem + S::kCtlOff + 16);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (warp == kConsumerWarps && lane == 0) {
+    if (threadIdx.x == 0) {
         for (int s = 0; s < S::kStages; ++s) {
             mbar_init(full_bar + 8 * s, 1);
-            mbar_init(empty_bar + 8 * s, MT);   // the warps that take a stage
+            mbar_init(empty_bar + 8 * s, MT > 1 ? MT - 1 : 1);   // the other warps that take a stage
+            issued[s] = 0;
         }
+        ctl[3] = 0;                             // a wait ran out
         mbar_init_fence();
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap)) : "memory");
     }
@@ -408,107 +510,16 @@ __global__ void __launch_bounds__(kThreads, 2)
     int used;
     find_part(p, scan, ctl, walk, x0, total, used);
 
-    if (warp == kConsumerWarps) {
-        // ---- Producer.  A batch is up to 32 pieces of one segment, whole
-        // stages of them, a lane a piece; the next batch's pages are looked up
-        // before this one is issued.
-        const int P = p.piece, per_stage = p.tile / P;
-        const int per_batch = 32 / per_stage * per_stage;
-        const int per_block = p.block / P;
-        const uint32_t piece_bytes = static_cast<uint32_t>(P) * S::kRowBytes;
-        Segment seg;
-        bool more = walk.next(p, seg);
-        int piece = 0, end = 0;                 // of the segment, still to look up
-        auto enter = [&] {
-            piece = seg.first * per_stage;
-            end = min(seg.last * per_stage, (seg.len - 1) / P + 1);
-        };
-        if (more)
-            enter();
-        // the batch looked up last
-        int b_n = 0, b_group = 0, b_left = 0, b_off = 0, b_page = -1;
-        bool b_bad = false;
-        auto fetch = [&] {
-            b_n = 0;
-            if (!more)
-                return;
-            b_n = min(per_batch, end - piece);
-            b_group = seg.group;
-            const int f = piece + lane;
-            const int col = f / per_block;
-            b_off = (f - col * per_block) * P;
-            b_left = seg.len - f * P;           // tokens from the piece's first on
-            const bool have = lane < b_n, in_table = col < p.table_cols;
-            b_page = have && in_table ? p.block_table[seg.request * p.bt_s0 + col] : -1;
-            b_bad = have && !in_table;
-            piece += b_n;
-            if (piece >= end) {
-                more = walk.next(p, seg);
-                if (more)
-                    enter();
-            }
-        };
-        int stage = 0, issued = 0;
-        uint32_t phase = 0;
-        bool aborted = false;
-        fetch();
-        while (b_n > 0 && !aborted) {
-            const int n = b_n, group = b_group, left = b_left, off = b_off;
-            int page = b_page;
-            const bool have = lane < n;
-            if (have && (b_bad || page < 0 || page >= p.pages)) {
-                atomicOr(p.flags, SDA_FLAG_BOUNDS);
-                page = -1;
-            }
-            fetch();
-            for (int done = 0; done < n; done += per_stage) {
-                if (issued >= S::kStages) {
-                    const bool ok = mbar_wait(empty_bar + 8 * stage, phase ^ 1u, p.wait_ns);
-                    if (!__all_sync(~0u, ok)) {
-                        if (lane == 0)
-                            atomicOr(p.flags, SDA_FLAG_TIMEOUT);
-                        aborted = true;
-                        break;
-                    }
-                }
-                const bool copy = have && lane >= done && lane < done + per_stage && page >= 0;
-                const unsigned cb = __ballot_sync(~0u, copy);
-                const uint32_t fb = full_bar + 8 * stage;
-                if (lane == 0 && cb)
-                    mbar_expect_tx(fb, __popc(cb) * piece_bytes);
-                __syncwarp();
-                uint64_t bits = 0;
-                if (copy) {
-                    const int k = lane - done;
-                    tma_load_5d(sbase + stage * S::kStageBytes + k * piece_bytes, &tmap, 0, off, 0, group, page, fb);
-                    bits = low_bits(min(P, left)) << (k * P);
-                }
-                const unsigned lo = __reduce_or_sync(~0u, static_cast<unsigned>(bits));
-                const unsigned hi = S::kSlots > 32 ? __reduce_or_sync(~0u, static_cast<unsigned>(bits >> 32)) : 0u;
-                if (lane == 0) {
-                    hdr[stage] = (static_cast<uint64_t>(hi) << 32) | lo;
-                    mbar_arrive(fb);
-                }
-                ++issued;
-                if (++stage == S::kStages) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
-            }
-        }
-        // Every copy that was started lands before the block's memory can go to another.
-        if (lane == 0) {
-            bool drained = true;
-            for (int k = max(0, issued - S::kStages); k < issued; ++k)
-                drained = mbar_wait(full_bar + 8 * (k % S::kStages),
-                                    static_cast<uint32_t>(k / S::kStages) & 1u, kDrainLimitNs) && drained;
-            if (!drained)
-                atomicOr(p.flags, SDA_FLAG_TIMEOUT);
-        }
-        return;
+    const int mt = warp / S::kAlternate, turn = warp % S::kAlternate;
+    Feed<FP8, D, MT> feed;
+    if (mt == 0) {                              // the tile-0 warps issue
+        feed.start(p, walk, turn, lane);
+        for (int s = turn; s < S::kStages; s += S::kAlternate)
+            feed.issue(p, &tmap, sbase, full_bar, hdr, issued, s, lane);
+        if (S::kStages % S::kAlternate != 0)    // from now on a stage follows the one whose place it takes
+            feed.start(p, walk, turn + S::kStages, lane);
     }
 
-    // ---- Consumers.
     const int ctid = threadIdx.x;               // 0..127
     const int g = lane >> 2, t = lane & 3;      // fragment row and column pair
     const int H = p.heads, R = p.rows;
@@ -522,11 +533,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (len > 0)
             continue;
         if (p.by_unit && !p.whole_units)
-            for (int k = ctid; k < p.groups; k += kConsumers)
+            for (int k = ctid; k < p.groups; k += kThreads)
                 p.tasks[q * p.groups + k] = make_int4(0, 0, 0, 0);
         if (len < 0)
             continue;
-        for (int e = ctid; e < p.groups * R * D; e += kConsumers) {
+        for (int e = ctid; e < p.groups * R * D; e += kThreads) {
             const int d = e % D, gr = e / D;    // gr: [token][group][head]
             const int h = gr % H;
             const int64_t row = static_cast<int64_t>(q) * p.query_len * p.groups + gr / H;
@@ -536,7 +547,6 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
     }
 
-    const int mt = warp / S::kAlternate, turn = warp % S::kAlternate;
     const uint32_t qfrag = sbase + S::kQOff + mt * S::kQBytes;
     float *obuf = reinterpret_cast<float *>(smem + S::kQOff);
     const int r0 = 16 * mt + g, r1 = r0 + 8;    // this thread's query rows
@@ -580,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         // FP8: the fp16 product takes q scaled by a power of two that puts the
         // row's largest |q| in [2^14, 2^15), undone in the row's logit scale:
         // any bf16 row is exact down to 2^-31 of its largest value.
-        constexpr int kPerRow = kConsumers / (16 * MT);         // threads that look at a row
+        constexpr int kPerRow = kThreads / (16 * MT);         // threads that look at a row
         {
             const int r = ctid / kPerRow, part = ctid % kPerRow;
             uint32_t mx = 0;
@@ -610,9 +620,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                                   : 1.0f;
             }
         }
-        consumer_bar();
+        __syncthreads();
 #pragma unroll 1
-        for (int f = warp; f < MT * S::kSteps; f += kConsumerWarps) {
+        for (int f = warp; f < MT * S::kSteps; f += kWarps) {
             const int m = f / S::kSteps, kk = f - m * S::kSteps;
             // the four dims of k-step kk that thread t's K words hold
             const int d = FP8 ? 64 * (kk >> 2) + 16 * t + 4 * (kk & 3) : 32 * (kk >> 1) + 8 * t + 4 * (kk & 1);
@@ -645,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                          "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3])
                          : "memory");
         }
-        consumer_bar();
+        __syncthreads();
         // logit scale in log2 units, the q prescale undone (a power of two: exact)
         const float sl0 = p.scale * kLog2e * ks / row_scale[r0], sl1 = p.scale * kLog2e * ks / row_scale[r1];
 
@@ -660,18 +670,20 @@ __global__ void __launch_bounds__(kThreads, 2)
             if (!dead) {
                 const bool ok = mbar_wait(full_bar + 8 * ring, parity, p.wait_ns);
                 if (!__all_sync(~0u, ok)) {
-                    if (lane == 0)
+                    if (lane == 0) {
                         atomicOr(p.flags, SDA_FLAG_TIMEOUT);
+                        ctl[3] = 1;
+                    }
                     dead = true;
                 }
             }
             const uint64_t loaded = dead ? 0ull : hdr[ring];
-            if (loaded) {
+            const int tok0 = (seg.first + stage - base) * p.tile;
+            // tokens of the stage that every row sees
+            const int common = len - p.query_len + 1 - tok0;
+            auto work = [&](auto plain) {
+                constexpr bool kPlain = decltype(plain)::value;
                 const uint32_t sb = sbase + ring * S::kStageBytes;
-                const int tok0 = (seg.first + stage - base) * p.tile;
-                // tokens of the stage that every row sees, and that a row sees
-                const int common = len - p.query_len + 1 - tok0;
-                const bool plain = loaded == kAll && common >= S::kSlots;
 
                 // ---- S = Q K^T: tile i, column g is slot 8i + slot_of(g).
                 float sc[NT][4];
@@ -679,21 +691,31 @@ __global__ void __launch_bounds__(kThreads, 2)
                 for (int i = 0; i < NT; ++i)
                     sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.0f;
                 const uint32_t krow = sb + ksw * 128u;
+                constexpr int kGroup = NT < 4 ? NT : 4;   // score tiles, independent chains, at a time
                 if constexpr (FP8) {
-                    // thread t holds 16 dims a chunk: four k-steps; tiles in pairs
+                    // thread t holds 16 dims a chunk: four k-steps
 #pragma unroll
-                    for (int i = 0; i < NT; i += 2) {
+                    for (int i0 = 0; i0 < NT; i0 += kGroup) {
 #pragma unroll
                         for (int c = 0; c < NC; ++c) {
                             const uint32_t off = (c >> 1) * bstride + ((((c & 1) * 4 + t) ^ ksw) << 4);
-                            const uint4 ka = lds128(krow + tile_off[i] + off), kb = lds128(krow + tile_off[i + 1] + off);
-                            const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+                            uint32_t w[kGroup][4];
+#pragma unroll
+                            for (int i = 0; i < kGroup; ++i) {
+                                const uint4 v = lds128(krow + tile_off[i0 + i] + off);
+                                w[i][0] = v.x;
+                                w[i][1] = v.y;
+                                w[i][2] = v.z;
+                                w[i][3] = v.w;
+                            }
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
                                 const uint4 qv = lds128(qfrag + ((4 * c + k) * 32 + lane) * 16);
                                 const uint32_t qf[4] = {qv.x, qv.y, qv.z, qv.w};
-                                mma16816<true>(sc[i], qf, e4m3x2_to_f16x2(wa[k]), e4m3x2_to_f16x2(wa[k] >> 16));
-                                mma16816<true>(sc[i + 1], qf, e4m3x2_to_f16x2(wb[k]), e4m3x2_to_f16x2(wb[k] >> 16));
+#pragma unroll
+                                for (int i = 0; i < kGroup; ++i)
+                                    mma16816<true>(sc[i0 + i], qf, e4m3x2_to_f16x2(w[i][k]),
+                                                   e4m3x2_to_f16x2(w[i][k] >> 16));
                             }
                         }
                     }
@@ -705,7 +727,6 @@ __global__ void __launch_bounds__(kThreads, 2)
                         const uint4 qa = lds128(qfrag + ((2 * c) * 32 + lane) * 16);
                         const uint4 qb = lds128(qfrag + ((2 * c + 1) * 32 + lane) * 16);
                         const uint32_t fa[4] = {qa.x, qa.y, qa.z, qa.w}, fb[4] = {qb.x, qb.y, qb.z, qb.w};
-                        constexpr int kGroup = NT < 4 ? NT : 4;
 #pragma unroll
                         for (int i0 = 0; i0 < NT; i0 += kGroup) {
                             uint4 kv[kGroup];
@@ -724,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
                 // ---- Mask; c0/c2 of tile i are slot 8i + t, c1/c3 slot 8i + t + 4.
                 float mx0 = -INFINITY, mx1 = -INFINITY;
-                if (plain) {
+                if constexpr (kPlain) {
 #pragma unroll
                     for (int i = 0; i < NT; ++i) {
                         sc[i][0] *= sl0;
@@ -785,11 +806,11 @@ __global__ void __launch_bounds__(kThreads, 2)
 
                 // ---- O += P V.  P in 11 bits (fp16, next to E4M3 values' 4), or
                 // bf16 twice: rounded, and what the rounding left.
-                const uint64_t seen = plain ? kAll : loaded & low_bits(common);
+                const uint64_t seen = kPlain ? kAll : loaded & low_bits(common);
 #pragma unroll
                 for (int k2 = 0; k2 < KS; ++k2) {
                     const uint32_t km = static_cast<uint32_t>(seen >> (16 * k2)) & 0xFFFFu;
-                    if (km == 0)
+                    if (!kPlain && km == 0)
                         continue;
                     float pr[2][4];
 #pragma unroll
@@ -797,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             // tokens that only some rows see come below
-                            const bool in = km == 0xFFFFu || ((km >> (8 * h + t + 4 * (k & 1))) & 1u);
+                            const bool in = kPlain || km == 0xFFFFu || ((km >> (8 * h + t + 4 * (k & 1))) & 1u);
                             pr[h][k] = in ? sc[2 * k2 + h][k] : 0.0f;
                         }
                     uint32_t pa[4], pb[4] = {0, 0, 0, 0};
@@ -810,7 +831,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                                                hi - __uint_as_float(pa[k] & 0xFFFF0000u));
                     }
                     const uint32_t vrow = sb + ((mi & 1) ? tile_off[2 * k2 + 1] : tile_off[2 * k2]) + vsw * 128u;
-                    if (km == 0xFFFFu) {
+                    if (kPlain || km == 0xFFFFu) {
                         pv_accumulate<FP8, D, false>(o, pa, pb, vrow, bstride, mi, vsw, 0u, 0u);
                     } else {
                         auto both = [&](int s) {
@@ -822,6 +843,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 // ---- The newest query_len - 1 tokens, which only some rows see:
                 // one at a time in fp32, so that a value that is not a number
                 // reaches the rows that see it alone.
+                if constexpr (!kPlain) {
                 for (uint64_t rest = loaded & ~seen & low_bits(common + p.query_len - 1); rest; rest &= rest - 1) {
                     const int s = __ffsll(static_cast<long long>(rest)) - 1;
                     float p0 = 0.0f, p1 = 0.0f;
@@ -871,10 +893,28 @@ __global__ void __launch_bounds__(kThreads, 2)
                         }
                     }
                 }
-            }
+                }
+            };
+            if (loaded == kAll && common >= S::kSlots)
+                work(std::true_type{});
+            else if (loaded)
+                work(std::false_type{});
+            // ---- The place is free: the next stage for it.
             __syncwarp();
-            if (lane == 0)
-                mbar_arrive(empty_bar + 8 * ring);
+            if (MT > 1 && mt > 0) {
+                if (lane == 0)
+                    mbar_arrive(empty_bar + 8 * ring);
+            } else if (!dead) {
+                if (MT > 1 && !__all_sync(~0u, mbar_wait(empty_bar + 8 * ring, parity, p.wait_ns))) {
+                    if (lane == 0) {
+                        atomicOr(p.flags, SDA_FLAG_TIMEOUT);
+                        ctl[3] = 1;
+                    }
+                    dead = true;
+                } else {
+                    feed.issue(p, &tmap, sbase, full_bar, hdr, issued, ring, lane);
+                }
+            }
             ring += S::kAlternate;
             while (ring >= S::kStages) {
                 ring -= S::kStages;
@@ -899,7 +939,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             mine[16] = m_run[1];
             mine[17] = l1;
         }
-        consumer_bar();                         // statistics are there; Q fragments are dead
+        __syncthreads();                         // statistics are there; Q fragments are dead
         float fac[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -943,9 +983,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
                 }
             }
-            consumer_bar();
+            __syncthreads();
             constexpr int kVecs = S::kChunk / 4;
-            for (int e = ctid; e < R * kVecs; e += kConsumers) {
+            for (int e = ctid; e < R * kVecs; e += kThreads) {
                 const int r = e / kVecs, d = 4 * (e - r * kVecs);
                 const float *src = obuf + ((r / 16) * S::kAlternate * 16 + r % 16) * S::kObufStride + d;
                 float4 v = *reinterpret_cast<const float4 *>(src);
@@ -976,7 +1016,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     dst[3] = static_cast<uint16_t>(w.y >> 16);
                 }
             }
-            consumer_bar();
+            __syncthreads();
         }
         // ---- Who joins the unit's pieces: the CTA that holds its first tile says.
         if (!p.whole_units && begins && ctid == 0) {
@@ -996,6 +1036,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     if (!p.whole_units && !p.by_unit && !task_done && ctid == 0)
         p.tasks[blockIdx.x] = make_int4(0, 0, 0, 0);
+
+    // After a wait that ran out, copies may be in flight: they land before the
+    // block's memory can go to another.
+    __syncthreads();
+    if (ctl[3] && ctid < S::kStages && issued[ctid] > 0 &&
+        !mbar_wait(full_bar + 8 * ctid, static_cast<uint32_t>(issued[ctid] - 1) & 1u, kDrainLimitNs))
+        atomicOr(p.flags, SDA_FLAG_TIMEOUT);
 }
 
 template <bool FP8, int D, int MT>
@@ -1020,12 +1067,6 @@ sda_status launch_dim(bool fp8, const CUtensorMap &tmap, const Params &p, void *
     return tiles == 1   ? launch_shape<false, D, 1>(tmap, p, stream)
            : tiles == 2 ? launch_shape<false, D, 2>(tmap, p, stream)
                         : launch_shape<false, D, 4>(tmap, p, stream);
-}
-
-// Tokens of a stage for a cache row of `row_bytes` (Shape::kSlots).
-constexpr int stage_slots(int row_bytes)
-{
-    return row_bytes <= 256 ? 64 : row_bytes <= 768 ? 32 : 16;
 }
 
 // One translation unit per head size.
