@@ -12,11 +12,12 @@ using namespace sda;
 using namespace sda::paged;
 
 // ---------------------------------------------------------------------------
-// Join kernel: a CTA a (task, query row).  With partial outputs O_k and their
-// log-sum-exps L_k, o = sum_k e^(L_k - M) O_k / sum_k e^(L_k - M), L = M + log of
-// that sum.  A request alone on the GPU leaves one piece per CTA, so the
-// pieces are dealt over the block's thread groups, which add up through shared
-// memory in a fixed order.
+// Join kernel.  With partial outputs O_k and their log-sum-exps L_k,
+//     o = sum_k e^(L_k - M) O_k / sum_k e^(L_k - M),  L = M + log of that sum.
+// The split kernel lists what is to be joined, so the work does not grow with
+// the batch.  A row of few pieces is one warp's; one of many (a request alone on
+// the GPU leaves a piece per worker) is shared by a block's warps, which add up
+// through shared memory in a fixed order.
 // ---------------------------------------------------------------------------
 
 __device__ __forceinline__ float warp_max(float v)
@@ -38,85 +39,141 @@ __device__ __forceinline__ float warp_sum(float v)
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) sda_paged_join_kernel(const __grid_constant__ Params p)
 {
-    constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes, kUnroll = 4;
-    __shared__ float4 sums[kGroups][kLanes];
+    constexpr int kVecs = D / 64, kUnroll = 4;  // pairs of dims a lane has; pieces loaded at a time
+    __shared__ float2 sums[kJoinWarps][D / 2];
+    __shared__ int list_piece[kMaxWorkers], counts[kJoinWarps];
+    __shared__ float list_lse[kMaxWorkers];
     pdl_launch_dependents();
     pdl_wait();
-    const int4 task = p.tasks[blockIdx.x];
-    const int n = task.x, r = blockIdx.y;
-    if (n == 0)
-        return;
-    const int H = p.heads, j = r / H, h = r - j * H;
-    const int64_t row = (static_cast<int64_t>(task.y) * p.query_len + j) * p.groups + task.z;
-    // piece k: the first CTA's part goes on, the others' continues it
-    auto piece = [&](int k) { return (static_cast<int64_t>(task.w) + k) * 2 + (k == 0 ? 1 : 0); };
-    auto lse_of = [&](int k) { return p.part_lse[piece(k) * p.rows + r]; };
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int count = min(static_cast<int>(p.flags[kItemWord]), kMaxItems), H = p.heads;
+    for (int i = blockIdx.x; i < count; i += gridDim.x) {
+        const JoinItem item = p.items[i];
+        const int n = item.pieces;
+        const bool shared = n > kManyPieces;
+        const int r = item.row + (shared ? 0 : warp);
+        if (!shared && warp >= item.rows)
+            continue;
+        // piece k: the first worker's part goes on, the others' continue it
+        auto place = [&](int k) {
+            return ((static_cast<int64_t>(item.first) + k) * 2 + (k == 0 ? 1 : 0)) * p.rows + r;
+        };
+        // The pieces that saw a token (and were not merged into a neighbour's),
+        // in order: a lane each, or a list in shared memory.
+        int live = 0, mine = 0;                 // this lane's piece
+        float l = -INFINITY;
+        if (!shared) {
+            l = lane < n ? p.part_lse[place(lane)] : -INFINITY;
+            const unsigned have = __ballot_sync(~0u, l != -INFINITY);
+            live = __popc(have);
+            mine = lane < live ? __fns(have, 0, lane + 1) : 0;
+            l = __shfl_sync(~0u, l, mine);
+        } else {
+            for (int k0 = 0; k0 < n; k0 += kJoinThreads) {
+                const int k = k0 + threadIdx.x;
+                const float x = k < n ? p.part_lse[place(k)] : -INFINITY;
+                const unsigned have = __ballot_sync(~0u, x != -INFINITY);
+                __syncthreads();                // the list and counts of the last round, or item, have been read
+                if (lane == 0)
+                    counts[warp] = __popc(have);
+                __syncthreads();
+                int at = live + __popc(have & ((1u << lane) - 1u));
+                for (int w = 0; w < kJoinWarps; ++w) {
+                    at += w < warp ? counts[w] : 0;
+                    live += counts[w];
+                }
+                if (x != -INFINITY) {
+                    list_piece[at] = k;
+                    list_lse[at] = x;
+                }
+            }
+            __syncthreads();
+        }
+        auto lse_at = [&](int k) { return shared ? list_lse[k] : __shfl_sync(~0u, l, k); };
+        float M = -INFINITY;
+        for (int k = lane; k < live; k += 32)
+            M = fmaxf(M, shared ? list_lse[k] : l);
+        M = warp_max(M);
+        const float ref = M == -INFINITY ? 0.0f : M;
+        float W = 0.0f;
+        for (int k = lane; k < live; k += 32)
+            W += exp2f((shared ? list_lse[k] : l) - ref);
+        W = warp_sum(W);
 
-    const int lane = threadIdx.x & 31;
-    float M = -INFINITY;
-    for (int k = lane; k < n; k += 32)
-        M = fmaxf(M, lse_of(k));
-    M = warp_max(M);
-    const float ref = M == -INFINITY ? 0.0f : M;
-    float W = 0.0f;
-    for (int k = lane; k < n; k += 32)
-        W += exp2f(lse_of(k) - ref);
-    W = warp_sum(W);
-
-    const int grp = threadIdx.x / kLanes, d = threadIdx.x % kLanes;
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (grp < kGroups) {
-        for (int k0 = grp; k0 < n; k0 += kGroups * kUnroll) {
-            float4 v[kUnroll];
+        float2 acc[kVecs];
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j)
+            acc[j] = make_float2(0.0f, 0.0f);
+        const int first = shared ? warp : 0, step = shared ? kJoinWarps : 1;
+        for (int k0 = first; k0 < live; k0 += step * kUnroll) {
+            float2 x[kUnroll][kVecs];
             float w[kUnroll];
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
-                const int k = k0 + u * kGroups;
-                w[u] = k < n ? lse_of(k) : -INFINITY;
-                v[u] = k < n ? *reinterpret_cast<const float4 *>(p.partial + (piece(k) * p.rows + r) * D + 4 * d)
-                             : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                const int k = min(k0 + u * step, live - 1);
+                w[u] = k0 + u * step < live ? lse_at(k) : -INFINITY;
+                const int piece = shared ? list_piece[k] : __shfl_sync(~0u, mine, k);
+                const float2 *src = reinterpret_cast<const float2 *>(p.partial + place(piece) * D) + lane;
+#pragma unroll
+                for (int j = 0; j < kVecs; ++j)
+                    x[u][j] = k0 + u * step < live ? src[32 * j] : make_float2(0.0f, 0.0f);
             }
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
                 const float f = exp2f(w[u] - ref);
-                acc.x += f * v[u].x;
-                acc.y += f * v[u].y;
-                acc.z += f * v[u].z;
-                acc.w += f * v[u].w;
+#pragma unroll
+                for (int j = 0; j < kVecs; ++j) {
+                    acc[j].x += f * x[u][j].x;
+                    acc[j].y += f * x[u][j].y;
+                }
             }
         }
-        sums[grp][d] = acc;
-    }
-    __syncthreads();
-    if (grp != 0)
-        return;
+        if (shared) {
+            // the last item's sums were read before this item's list was made
 #pragma unroll
-    for (int k = 1; k < kGroups; ++k) {
-        const float4 v = sums[k][d];
-        acc.x += v.x;
-        acc.y += v.y;
-        acc.z += v.z;
-        acc.w += v.w;
+            for (int j = 0; j < kVecs; ++j)
+                sums[warp][32 * j + lane] = acc[j];
+            __syncthreads();
+            if (warp > 0)
+                continue;
+#pragma unroll
+            for (int w = 1; w < kJoinWarps; ++w)
+#pragma unroll
+                for (int j = 0; j < kVecs; ++j) {
+                    acc[j].x += sums[w][32 * j + lane].x;
+                    acc[j].y += sums[w][32 * j + lane].y;
+                }
+        }
+
+        const bool empty = M == -INFINITY && W == 0.0f;         // a row that saw no token; NaN goes on
+        const int j = r / H, h = r - j * H;
+        const int64_t token = static_cast<int64_t>(item.request) * p.query_len + j;
+        const int64_t row = token * p.groups + item.group;
+        float f = empty ? 0.0f : 1.0f / W;
+        if (p.v_scale)
+            f *= *p.v_scale;
+        if (p.gate)
+            f *= gate_factor(p.gate[token * p.g_s0 + static_cast<int64_t>(item.group * H + h) * p.g_s1]);
+        uint16_t *dst = p.output + row * p.o_s0 + h * p.o_s1 + 2 * lane;
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j) {
+            const uint32_t w = pack_bf16(acc[j].x * f, acc[j].y * f);
+            if (p.o_vec) {
+                *reinterpret_cast<uint32_t *>(dst + 64 * j) = w;
+            } else {
+                dst[64 * j] = static_cast<uint16_t>(w);
+                dst[64 * j + 1] = static_cast<uint16_t>(w >> 16);
+            }
+        }
+        if (p.lse && lane == 0)
+            p.lse[row * p.l_s0 + h * p.l_s1] = empty ? -INFINITY : (M + log2f(W)) * kLn2;
     }
-    const bool empty = M == -INFINITY && W == 0.0f;   // a row that saw no token; NaN goes through
-    float f = empty ? 0.0f : 1.0f / W;
-    if (!empty && p.v_scale)
-        f *= *p.v_scale;
-    if (p.gate)
-        f *= gate_factor(p.gate[(static_cast<int64_t>(task.y) * p.query_len + j) * p.g_s0 +
-                                static_cast<int64_t>(task.z * H + h) * p.g_s1]);
-    uint16_t *dst = p.output + row * p.o_s0 + h * p.o_s1 + 4 * d;
-    const uint2 w = make_uint2(pack_bf16(acc.x * f, acc.y * f), pack_bf16(acc.z * f, acc.w * f));
-    if (p.o_vec) {
-        *reinterpret_cast<uint2 *>(dst) = w;
-    } else {
-        dst[0] = static_cast<uint16_t>(w.x);
-        dst[1] = static_cast<uint16_t>(w.x >> 16);
-        dst[2] = static_cast<uint16_t>(w.y);
-        dst[3] = static_cast<uint16_t>(w.y >> 16);
+    // The list is empty again for the next call once every block has read its length.
+    __syncthreads();
+    if (threadIdx.x == 0 && atomicAdd(p.flags + kTicketWord, 1u) == gridDim.x - 1) {
+        p.flags[kItemWord] = 0;
+        p.flags[kTicketWord] = 0;
     }
-    if (p.lse && d == 0)
-        p.lse[row * p.l_s0 + h * p.l_s1] = empty ? -INFINITY : (M + log2f(W)) * kLn2;
 }
 
 // ---------------------------------------------------------------------------
@@ -153,10 +210,16 @@ size_t align256(size_t n)
     return (n + 255) & ~static_cast<size_t>(255);
 }
 
-// A CTA takes at least this many tiles before the line is cut finer.
+// A worker takes at least this many tiles before the line is cut finer.
 constexpr int kMinTiles = 2;
 // Units of at most this many tiles (by the table's width) are never cut.
 constexpr int kWholeTiles = 8;
+
+// Workers of a CTA.
+int workers_of(int64_t rows)
+{
+    return kWarps / tiles_of_rows(static_cast<int>(rows));
+}
 
 }  // namespace
 
@@ -165,8 +228,8 @@ extern "C" size_t sparse_decode_paged_workspace_bytes(int heads, int query_len, 
     if (heads < 1 || query_len < 1 || heads > kMaxRows || query_len > kMaxRows || heads * query_len > kMaxRows ||
         !dim_ok(head_dim))
         return 0;
-    const size_t rows = static_cast<size_t>(kMaxCtas) * 2 * heads * query_len;
-    return kHeaderBytes + align256(kTaskBytes) + rows * head_dim * sizeof(float) + align256(rows * sizeof(float));
+    const size_t rows = static_cast<size_t>(kMaxCtas) * workers_of(heads * query_len) * 2 * heads * query_len;
+    return kHeaderBytes + align256(kItemBytes) + rows * head_dim * sizeof(float) + align256(rows * sizeof(float));
 }
 
 extern "C" sda_status sparse_decode_paged_attention(const sda_tensor *query, const sda_tensor *cache,
@@ -219,7 +282,7 @@ extern "C" sda_status sparse_decode_paged_attention(const sda_tensor *query, con
         return SDA_ERR_UNSUPPORTED;
     // A TMA box holds the longest run of tokens that fits a stage and divides the page.
     const int elt = fp8 ? 1 : 2, row_bytes = static_cast<int>(2 * dim) * elt;
-    const int slots = stage_slots(row_bytes);
+    const int slots = stage_slots(row_bytes, tiles_of_rows(static_cast<int>(heads) * query_len));
     int piece = static_cast<int>(std::min<int64_t>(block, slots)) / 8 * 8;
     while (piece > 0 && block % piece != 0)
         piece -= 8;
@@ -285,10 +348,11 @@ extern "C" sda_status sparse_decode_paged_attention(const sda_tensor *query, con
     p.k_scale = fp8 ? k_scale : nullptr;
     p.v_scale = fp8 ? v_scale : nullptr;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    const size_t parts = static_cast<size_t>(kMaxCtas) * 2 * heads * query_len;
+    const int per_cta = workers_of(heads * query_len);
+    const size_t parts = static_cast<size_t>(kMaxCtas) * per_cta * 2 * heads * query_len;
     p.flags = reinterpret_cast<unsigned int *>(ws);
-    p.tasks = reinterpret_cast<int4 *>(ws + kHeaderBytes);
-    p.partial = reinterpret_cast<float *>(ws + kHeaderBytes + align256(kTaskBytes));
+    p.items = reinterpret_cast<JoinItem *>(ws + kHeaderBytes);
+    p.partial = reinterpret_cast<float *>(ws + kHeaderBytes + align256(kItemBytes));
     p.part_lse = p.partial + parts * dim;
     p.pages = pages;
     p.wait_ns = sda_wait_limit_ns();
@@ -318,9 +382,10 @@ extern "C" sda_status sparse_decode_paged_attention(const sda_tensor *query, con
     const int most = std::min(kMaxCtas, 2 * sms);
     p.min_tiles = kMinTiles;
     p.whole_units = widest <= kWholeTiles;
-    const int64_t want = p.whole_units ? units : (units * widest + kMinTiles - 1) / kMinTiles;
+    // Few tiles: a worker on each of as many SMs first.
+    const int64_t want = p.whole_units ? units : (units * (widest + kUnitCost) - 1) / (kMinTiles + kUnitCost) + 1;
     p.ctas = static_cast<int>(std::min<int64_t>(most, std::max<int64_t>(1, want)));
-    p.by_unit = units <= p.ctas;
+    p.workers = p.ctas * per_cta;
 
     const sda_status st = dim == 64    ? launch_64(fp8, tmap, p, stream)
                           : dim == 128 ? launch_128(fp8, tmap, p, stream)
@@ -328,7 +393,8 @@ extern "C" sda_status sparse_decode_paged_attention(const sda_tensor *query, con
                                        : launch_256(fp8, tmap, p, stream);
     if (st != SDA_OK || p.whole_units)
         return st;
-    const dim3 grid(static_cast<unsigned>(p.by_unit ? units : p.ctas), static_cast<unsigned>(p.rows));
+    const int64_t rows_to_join = units * p.rows;
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(most, rows_to_join)));
     auto join = dim == 64    ? sda_paged_join_kernel<64>
                 : dim == 128 ? sda_paged_join_kernel<128>
                 : dim == 192 ? sda_paged_join_kernel<192>
