@@ -9,15 +9,16 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib.util
 import os
 import re
-import struct
 import threading
 
 import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libsdattn.so")
+MARSHAL_PATH = os.path.join(_HERE, "_build", "_marshal.so")
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "sdattn.h")
 
 SDA_OK, SDA_ERR_INVALID, SDA_ERR_UNSUPPORTED, SDA_ERR_WORKSPACE, SDA_ERR_CUDA, SDA_ERR_TIMEOUT, SDA_ERR_BOUNDS = range(7)
@@ -49,6 +50,7 @@ class SdaError(RuntimeError):
 
 _lock = threading.Lock()
 _lib = None
+_marshal = None
 
 
 def _declare(lib):
@@ -147,48 +149,6 @@ def describe(t: torch.Tensor | None) -> SdaTensor | None:
         d.shape[i] = t.shape[i]
         d.stride[i] = t.stride(i)
     return d
-
-
-_DESCRIPTOR_BYTES = ctypes.sizeof(SdaTensor)
-_PACKERS = (None,) + tuple(struct.Struct(f"=Qii{n}q{32 - 8 * n}x{n}q{32 - 8 * n}x") for n in range(1, 5))
-
-
-def _pack(*tensors):
-    """Descriptors of `tensors` side by side in one buffer, written without a
-    ctypes object each: (the buffer, to be kept until the call has returned; an
-    address per tensor, None for None).  Raises as `describe` and `_device_of`."""
-    raw = bytearray(_DESCRIPTOR_BYTES * len(tensors))
-    at = ctypes.addressof((ctypes.c_char * len(raw)).from_buffer(raw))
-    where = []
-    offset = 0
-    for t in tensors:
-        if t is None:
-            where.append(None)
-        else:
-            n = t.dim()
-            code = _DTYPES.get(t.dtype)
-            if code is None:
-                raise TypeError(f"unsupported dtype {t.dtype}")
-            if not 1 <= n <= 4:
-                raise ValueError("1 to 4 dimensions")
-            _PACKERS[n].pack_into(raw, offset, t.data_ptr(), code, n, *t.shape, *t.stride())
-            where.append(at + offset)
-        offset += _DESCRIPTOR_BYTES
-    return raw, where
-
-
-def _same_device(tensors, stream) -> torch.device:
-    """`_device_of`, quick where all is well."""
-    index = -1
-    for t in tensors:
-        if t is not None:
-            i = t.get_device()
-            if i < 0 or (index >= 0 and i != index):
-                return _device_of(*tensors, stream=stream)
-            index = i
-    if index < 0 or stream is not None:
-        return _device_of(*tensors, stream=stream)
-    return torch.device("cuda", index)
 
 
 def _ref(d):
@@ -369,38 +329,68 @@ def sparse_decode_summary_scores(query, weights, summaries, block_table, seq_len
     return scores
 
 
+_NOTHING = contextlib.nullcontext()
 _step_workspaces: dict = {}
 
 
-def _step_workspace(device: torch.device, handle: int, nbytes: int) -> torch.Tensor:
-    """The serving-step entries' default workspace, on the current stream: kept per
-    (device, stream) like `default_workspace`, but a capture gets one of its own,
-    zeroed in the graph, that no other graph or eager call shares."""
-    if torch.cuda.is_current_stream_capturing():
-        return torch.zeros(nbytes, dtype=torch.uint8, device=device)
-    key = (device, handle)
-    ws = _step_workspaces.get(key)
-    if ws is None or ws.numel() < nbytes:
-        ws = _step_workspaces[key] = torch.zeros(nbytes, dtype=torch.uint8, device=device)
-    return ws
+def _new_step_workspace(index: int, handle: int, nbytes: int, stream) -> torch.Tensor:
+    """The serving-step entries' default workspace, zeroed on the call's stream: kept per
+    (device, stream) and grown on demand like `default_workspace`'s, but a capture gets one
+    of its own, zeroed in the graph, that no other graph or eager call shares."""
+    dev = torch.device("cuda", index)
+    with torch.cuda.stream(stream) if stream is not None else _current(dev):
+        if torch.cuda.is_current_stream_capturing():
+            return torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+        ws = _step_workspaces.get((index, handle))
+        if ws is None or ws.numel() < nbytes:
+            ws = _step_workspaces[index, handle] = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+        return ws
 
 
-def _enter(tensors, workspace, need: int, stream):
-    """What the serving-step entries share: (what the call needs kept, addresses
-    of the descriptors, device, stream handle, workspace address and bytes).  Where
-    no workspace is given, the stream's default one of at least `need` bytes."""
-    dev = _same_device((*tensors, workspace), stream)
-    keep, where = _pack(*tensors)
-    handle = (stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream
-    if workspace is None:
+def _scale_address(x, index: int, stream):
+    """(address, what keeps it) of an FP8 scale: None, a device tensor, or a number to upload."""
+    if x is None:
+        return None, None
+    if not isinstance(x, torch.Tensor):
+        dev = torch.device("cuda", index)
         with torch.cuda.stream(stream) if stream is not None else _current(dev):
-            workspace = _step_workspace(dev, handle, need)
-    return (keep, workspace), where, dev, handle, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+            x = torch.full((1,), float(x), dtype=torch.float32, device=dev)
+    return _marshal.scalar(x, index), x
 
 
-def _check(lib, rc: int) -> None:
+def load_marshal():
+    """The native marshalling module (csrc/sda_marshal.cpp).  Raises if it has not been built."""
+    global _marshal
+    with _lock:
+        if _marshal is None:
+            if not os.path.exists(MARSHAL_PATH):
+                raise ImportError(f"{MARSHAL_PATH} is missing: build it with "
+                                  "`python -c 'import __graft_entry__ as g; g.build()'`")
+            spec = importlib.util.spec_from_file_location("_marshal", MARSHAL_PATH)
+            _marshal = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(_marshal)
+    return _marshal
+
+
+def _call(fn, tensors, arguments, need: int, workspace, stream, scales=()):
+    """What the serving-step entries share: fn(*arguments(descriptor addresses, scale
+    addresses), workspace, its bytes, stream) on the tensors' device.  Where no workspace
+    is given it is the stream's default one of at least `need` bytes."""
+    keep, where, index, current, handle = (_marshal or load_marshal()).pack(*tensors)
+    if index < 0 or stream is not None or (workspace is not None and workspace.get_device() != index):
+        _device_of(*tensors, workspace, stream=stream)          # raises where they are apart
+        if stream is not None:
+            handle = stream.cuda_stream
+    if workspace is None:
+        workspace = _step_workspaces.get((index, handle))
+        if workspace is None or workspace.numel() < need or torch.cuda.is_current_stream_capturing():
+            workspace = _new_step_workspace(index, handle, need, stream)
+    pointers = [_scale_address(x, index, stream) for x in scales]
+    with _NOTHING if current else torch.cuda.device(index):
+        rc = fn(*arguments(where, [x[0] for x in pointers]), workspace.data_ptr(),
+                workspace.numel() * workspace.element_size(), handle)
     if rc != SDA_OK:
-        raise SdaError(rc, lib.sparse_decode_status_string(rc).decode())
+        raise SdaError(rc, load().sparse_decode_status_string(rc).decode())
 
 
 def sparse_decode_plan_step(context_lens, new_lens, free_pages, free_state, block_table, *, block_size: int,
@@ -421,11 +411,9 @@ def sparse_decode_plan_step(context_lens, new_lens, free_pages, free_state, bloc
     positions, requests = new(positions, slots.shape[0]), new(requests, slots.shape[0])
     seq_lens, token_starts = new(seq_lens, context_lens.shape[0]), new(token_starts, context_lens.shape[0] + 1)
     free_next = new(free_next, 2)
-    keep, d, dev, handle, ws, wsb = _enter((context_lens, new_lens, free_pages, free_state, free_next, block_table,
-                                            seq_lens, token_starts, slots, positions, requests), workspace, 256, stream)
-    with _current(dev):
-        rc = lib.sparse_decode_plan_step(d[0], d[1], int(block_size), *d[2:], ws, wsb, handle)
-    _check(lib, rc)
+    _call(lib.sparse_decode_plan_step, (context_lens, new_lens, free_pages, free_state, free_next, block_table, seq_lens,
+                                        token_starts, slots, positions, requests),
+          lambda d, _: (d[0], d[1], int(block_size), *d[2:]), 256, workspace, stream)
     return seq_lens, token_starts, slots, positions, requests, free_next
 
 
@@ -447,19 +435,14 @@ def sparse_decode_rope_append(query, key, value, positions, inv_freq, slots, cac
         query_out = torch.zeros_like(query) if slots is not None else torch.empty_like(query)
     if key is None:
         cache = None
-    keep, d, dev, handle, ws, wsb = _enter((query, query_out, key, value, positions, inv_freq, slots, cache),
-                                           workspace, 256, stream)
-    ks, _keep_k = _scale_ptr(k_scale, dev)
-    vs, _keep_v = _scale_ptr(v_scale, dev)
     parts = None
     if sections is not None:
         if positions is None or len(sections) != positions.shape[0]:
             raise ValueError("sparse_decode: a section for each axis of positions")
         parts = (ctypes.c_int32 * len(sections))(*sections)
-    with _current(dev):
-        rc = lib.sparse_decode_rope_append(*d[:6], parts, bool(interleaved_axes), bool(adjacent_pairs),
-                                           float(amplitude), d[6], d[7], ks, vs, ws, wsb, handle)
-    _check(lib, rc)
+    _call(lib.sparse_decode_rope_append, (query, query_out, key, value, positions, inv_freq, slots, cache),
+          lambda d, s: (*d[:6], parts, bool(interleaved_axes), bool(adjacent_pairs), float(amplitude), *d[6:], *s), 256,
+          workspace, stream, (k_scale, v_scale))
     return query_out
 
 
@@ -476,13 +459,8 @@ def sparse_decode_paged_attention(query, cache, block_table, seq_lens, output, *
     include/sdattn.h for the contract."""
     lib = load()
     need = lib.sparse_decode_paged_workspace_bytes(query.shape[1], int(query_len), query.shape[-1]) or 256
-    keep, d, dev, handle, ws, wsb = _enter((query, cache, block_table, seq_lens, output, lse, gate), workspace, need,
-                                           stream)
-    ks, _keep_k = _scale_ptr(k_scale, dev)
-    vs, _keep_v = _scale_ptr(v_scale, dev)
-    with _current(dev):
-        rc = lib.sparse_decode_paged_attention(*d[:6], float(scale), int(query_len), ks, vs, d[6], ws, wsb, handle)
-    _check(lib, rc)
+    _call(lib.sparse_decode_paged_attention, (query, cache, block_table, seq_lens, output, lse, gate),
+          lambda d, s: (*d[:6], float(scale), int(query_len), *s, d[6]), need, workspace, stream, (k_scale, v_scale))
 
 
 def read_errors(workspace: torch.Tensor, clear: bool = False,

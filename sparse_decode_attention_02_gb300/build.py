@@ -1,4 +1,5 @@
-"""Builds libsdattn.so (the C-ABI library) in-tree with nvcc for sm_103a."""
+"""Builds, in-tree, libsdattn.so (the C-ABI library; nvcc for sm_103a) and _marshal.so
+(the binding's native argument marshalling; g++ against the installed torch)."""
 from __future__ import annotations
 
 import os
@@ -14,6 +15,8 @@ INCLUDES = [os.path.join(HERE, "csrc", name) for name in ("sda_common.cuh", "sda
 HEADER = os.path.join(ROOT, "include", "sdattn.h")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libsdattn.so")
+MARSHAL_SOURCE = os.path.join(HERE, "csrc", "sda_marshal.cpp")
+MARSHAL = os.path.join(OUT_DIR, "_marshal.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -55,6 +58,35 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
     return out
 
 
+def build_marshal(force: bool = False, out: str = MARSHAL) -> str:
+    """Compile the marshalling module unless it is newer than its sources; returns its path."""
+    import sysconfig
+
+    import torch
+
+    if not force and os.path.exists(out) and os.path.getmtime(out) >= max(os.path.getmtime(x)
+                                                                           for x in (MARSHAL_SOURCE, HEADER)):
+        return out
+    os.makedirs(os.path.dirname(out), exist_ok=True)
+    base = os.path.dirname(torch.__file__)
+    lib = os.path.join(base, "lib")
+    cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
+    tmp = out + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", MARSHAL_SOURCE, "-o", tmp,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", os.path.join(ROOT, "include"), "-I", sysconfig.get_paths()["include"],
+           *(a for d in (os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+                         os.path.join(cuda, "include")) for a in ("-isystem", d)),
+           "-L", lib, f"-Wl,-rpath,{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("g++ failed building _marshal.so")
+    os.replace(tmp, out)
+    return out
+
+
 if __name__ == "__main__":
     build(force=True, verbose="-v" in sys.argv)
+    build_marshal(force=True)
     print(LIB)
