@@ -342,7 +342,7 @@ sda_status sparse_decode_plan_step(const sda_tensor *context_lens, const sda_ten
  *   adjacent_pairs    zero: pair i is dims (i, i + R); nonzero: dims (2i, 2i + 1).
  *   amplitude   factor on the turned dims (1 for plain rotary positions).
  *   slots       [T] int64, stride 1: page * B + offset; -1 marks a padding row:
- *               nothing of it is read, and its query_out row is left as it was.
+ *               nothing of it is used, and its query_out row is left as it was.
  *               A slot outside the cache leaves its row out with
  *               SDA_FLAG_BOUNDS.  Two rows must not name the same slot (its
  *               contents would be a mix of the two).

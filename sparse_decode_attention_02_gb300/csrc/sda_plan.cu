@@ -7,10 +7,14 @@
 // prefix sum of need), token rows likewise (a prefix sum of n).  Every CTA
 // computes both sums over all requests (they are small: 8 bytes a request) and
 // keeps them in shared memory; the token rows and the page entries are then
-// dealt out over the grid and find their request by binary search.  The work
-// is bound by latency for a decode step (one CTA) and by the 16 bytes written
-// per token row for prompts.
+// dealt out over the grid and find their request there.  A warp takes 128
+// consecutive rows: the requests of the first and the last are searched once for
+// all lanes, a lane's own only between those two.  A decode step is bound by
+// latency (one CTA; the sums are 32-bit and saturate, divisions by B are
+// multiplications), prompts by the 16 bytes written per token row.
 #include "sda_common.cuh"
+
+#include <algorithm>
 
 namespace {
 
@@ -18,9 +22,11 @@ using namespace sda;
 
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxRequests = 8192;              // five int32 arrays of them in shared memory: 160 KB
-constexpr int kQuad = 4;                        // token rows a thread writes at a time
-constexpr int kRowsPerCta = 2 * kThreads * kQuad;
+constexpr int kMaxRequests = 8192;              // six int32 arrays of them in shared memory: 192 KB
+constexpr int kArrays = 6;
+constexpr int kQuad = 4;                        // consecutive token rows a thread writes at a time
+constexpr int kWarpRows = 32 * kQuad;           // rows of a warp's turn
+constexpr uint32_t kMostSum = 0x7FFFFFFFu;      // sums stay here: beyond any count of pages or rows
 constexpr int kTicketWord = 16;                 // of the workspace header: CTAs past their reads
 
 struct PlanParams {
@@ -37,51 +43,66 @@ struct PlanParams {
     int32_t *positions, *owners;
     unsigned int *header;
     int requests, width, block, ring_size, rows;
+    unsigned long long inverse;                 // floor(2^64 / block) + 1 (0 for block 1)
     int vec;                                    // the row outputs take 16-byte stores
 };
 
-// Sums of up to three values over the block, exclusive, in thread order.
+// x / block, exactly, for any 32-bit x.
+__device__ __forceinline__ uint32_t pages_before(const PlanParams &p, uint32_t x)
+{
+    return p.inverse ? static_cast<uint32_t>(__umul64hi(x, p.inverse)) : x;
+}
+
+// Three sums over requests: pages needed, pages returned, rows added.
 struct Sums {
-    long long need, back, add;
+    uint32_t need, back, add;
 };
+
+// A sum that stops at kMostSum; associative for terms up to there.
+__device__ __forceinline__ uint32_t plus(uint32_t a, uint32_t b)
+{
+    return min(a + b, kMostSum);
+}
+
+__device__ __forceinline__ Sums operator+(Sums a, Sums b)
+{
+    return {plus(a.need, b.need), plus(a.back, b.back), plus(a.add, b.add)};
+}
+
+__device__ __forceinline__ Sums shfl(Sums v, int lane)
+{
+    return {__shfl_sync(~0u, v.need, lane), __shfl_sync(~0u, v.back, lane), __shfl_sync(~0u, v.add, lane)};
+}
 
 __device__ __forceinline__ Sums warp_inclusive(Sums v, int lane)
 {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long a = __shfl_up_sync(~0u, v.need, o), b = __shfl_up_sync(~0u, v.back, o),
-                        c = __shfl_up_sync(~0u, v.add, o);
-        if (lane >= o) {
-            v.need += a;
-            v.back += b;
-            v.add += c;
-        }
+        const Sums u = {__shfl_up_sync(~0u, v.need, o), __shfl_up_sync(~0u, v.back, o), __shfl_up_sync(~0u, v.add, o)};
+        if (lane >= o)
+            v = v + u;
     }
     return v;
 }
 
+// The sums over the threads before this one, in thread order, and over all.
 __device__ __forceinline__ Sums block_exclusive(const Sums mine, Sums *warp_sums, Sums &total)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Sums inc = warp_inclusive(mine, lane);
-    __syncthreads();                            // warp_sums may still be read from the last call
     if (lane == 31)
         warp_sums[warp] = inc;
     __syncthreads();
     const Sums w = warp_inclusive(warp_sums[lane], lane);   // kWarps == 32: a lane a warp
-    auto at = [&](long long x, int l) { return __shfl_sync(~0u, x, l); };
-    total = {at(w.need, 31), at(w.back, 31), at(w.add, 31)};
-    const int before = warp > 0 ? warp - 1 : 0;
-    Sums e = {at(w.need, before), at(w.back, before), at(w.add, before)};
-    if (warp == 0)
-        e = {0, 0, 0};
-    return {e.need + inc.need - mine.need, e.back + inc.back - mine.back, e.add + inc.add - mine.add};
+    total = shfl(w, 31);
+    const Sums none = {0, 0, 0}, before = shfl(w, max(warp - 1, 0)), left = shfl(inc, max(lane - 1, 0));
+    return (warp > 0 ? before : none) + (lane > 0 ? left : none);
 }
 
-// The last index whose value is at most x (a[0] <= x; a ascends).
-__device__ __forceinline__ int last_at_most(const int32_t *a, int n, int x)
+// The last index in [lo, hi] whose value is at most x (a[lo] <= x; a ascends).
+__device__ __forceinline__ int last_at_most(const int32_t *a, int lo, int hi, int x)
 {
-    int lo = 0, len = n;
+    int len = hi - lo + 1;
     while (len > 1) {
         const int half = len >> 1;
         lo = a[lo + half] <= x ? lo + half : lo;
@@ -90,9 +111,18 @@ __device__ __forceinline__ int last_at_most(const int32_t *a, int n, int x)
     return lo;
 }
 
-__device__ __forceinline__ int32_t clip32(long long x)
+// The same for the whole array and one x for the warp: 32 probes at a time.
+__device__ __forceinline__ int warp_last_at_most(const int32_t *a, int n, int x, int lane)
 {
-    return static_cast<int32_t>(min(x, static_cast<long long>(INT32_MAX)));
+    int lo = 0;
+    while (n > 1) {
+        const int stride = (n + 31) >> 5;
+        const bool ok = lane * stride < n && a[lo + lane * stride] <= x;
+        const int last = __popc(__ballot_sync(~0u, ok)) - 1;
+        lo += last * stride;
+        n = min(stride, n - last * stride);
+    }
+    return lo;
 }
 
 __global__ void __launch_bounds__(kThreads) sda_plan_kernel(const __grid_constant__ PlanParams p)
@@ -103,7 +133,8 @@ __global__ void __launch_bounds__(kThreads) sda_plan_kernel(const __grid_constan
     int32_t *tok = len + p.requests;            // token rows before the request
     int32_t *pag = tok + p.requests;            // pages taken before it
     int32_t *rel = pag + p.requests;            // pages returned before it
-    __shared__ Sums warp_sums[kWarps];
+    int32_t *adj = rel + p.requests;            // pag less the pages the request holds: new column to ring entry
+    __shared__ Sums warp_sums[2][kWarps];
     __shared__ int granted[3];                  // token rows, pages taken, pages returned
     __shared__ int is_last;
 
@@ -123,19 +154,21 @@ __global__ void __launch_bounds__(kThreads) sda_plan_kernel(const __grid_constan
 
     // What request q asks for: pages it needs, pages it returns, rows it adds.
     // Requests outside the contract ask for nothing and raise the flag.
+    auto held = [&](int c) { return pages_before(p, static_cast<uint32_t>(max(c, 0)) + (B - 1)); };
     auto asks = [&](int c, int n, Sums &s) {
         s = {0, 0, 0};
-        const long long have = (static_cast<long long>(max(c, 0)) + B - 1) / B;
         if (n == 0 && c >= 0)
             return true;
-        if (c < 0 || n < -1 || have > p.width)
+        const uint32_t have = held(c);
+        if (c < 0 || n < -1 || have > static_cast<uint32_t>(p.width))
             return false;
         if (n == -1) {
             s.back = have;
             return true;
         }
-        const long long end = (static_cast<long long>(c) + n + B - 1) / B;
-        if (end > p.width || static_cast<long long>(c) + n > INT32_MAX)
+        const uint32_t after = static_cast<uint32_t>(c) + static_cast<uint32_t>(n);
+        const uint32_t end = after <= kMostSum ? held(static_cast<int>(after)) : kMostSum;
+        if (after > kMostSum || end > static_cast<uint32_t>(p.width))
             return false;
         s.need = end - have;
         s.add = n;
@@ -149,23 +182,21 @@ __global__ void __launch_bounds__(kThreads) sda_plan_kernel(const __grid_constan
         bad = !asks(c, n, s) || bad;
         ctx[q] = c;
         len[q] = n;
-        mine.need += s.need;
-        mine.back += s.back;
-        mine.add += s.add;
+        mine = mine + s;
     }
     Sums total;
-    Sums run = block_exclusive(mine, warp_sums, total);
-    if (total.need > count) {
+    Sums run = block_exclusive(mine, warp_sums[0], total);
+    if (total.need > static_cast<uint32_t>(count)) {
         // Not all pages are there: rows count only for requests whose pages are.
-        long long need = run.need, add = 0;
+        uint32_t need = run.need, add = 0;
         for (int q = q0; q < q1; ++q) {
             Sums s;
             asks(ctx[q], len[q], s);
-            need += s.need;
-            add += s.need == 0 || need <= count ? s.add : 0;
+            need = plus(need, s.need);
+            add = plus(add, s.need == 0 || need <= static_cast<uint32_t>(count) ? s.add : 0);
         }
         Sums t2;
-        run.add = block_exclusive({0, 0, add}, warp_sums, t2).add;
+        run.add = block_exclusive({0, 0, add}, warp_sums[1], t2).add;
     }
 
     // Grants, in the order of the requests: pages and rows both have to fit.
@@ -176,16 +207,17 @@ __global__ void __launch_bounds__(kThreads) sda_plan_kernel(const __grid_constan
         const int c = ctx[q], n = len[q];
         Sums s;
         asks(c, n, s);
-        tok[q] = clip32(run.add);
-        pag[q] = clip32(run.need);
-        rel[q] = clip32(run.back);
-        run.need += s.need;
-        run.back += s.back;
+        tok[q] = static_cast<int>(run.add);
+        pag[q] = static_cast<int>(run.need);
+        rel[q] = static_cast<int>(run.back);
+        adj[q] = static_cast<int>(run.need) - static_cast<int>(held(c));
+        run.need = plus(run.need, s.need);
+        run.back = plus(run.back, s.back);
         int after = c;
         if (s.add > 0) {
-            bool ok = s.need == 0 || run.need <= count;
-            run.add += ok ? s.add : 0;
-            ok = ok && run.add <= p.rows;
+            bool ok = s.need == 0 || run.need <= static_cast<uint32_t>(count);
+            run.add = plus(run.add, ok ? s.add : 0);
+            ok = ok && run.add <= static_cast<uint32_t>(p.rows);
             if (ok) {
                 after = c + n;
                 top[0] = static_cast<int>(run.add);
@@ -193,7 +225,7 @@ __global__ void __launch_bounds__(kThreads) sda_plan_kernel(const __grid_constan
             }
             full = full || !ok;
         } else if (n == -1 && c >= 0 && (s.back > 0 || c == 0)) {
-            const bool ok = ring_ok && count + run.back <= p.ring_size;
+            const bool ok = ring_ok && run.back <= static_cast<uint32_t>(p.ring_size - count);
             if (ok) {
                 after = 0;
                 top[2] = static_cast<int>(run.back);
@@ -244,40 +276,75 @@ __global__ void __launch_bounds__(kThreads) sda_plan_kernel(const __grid_constan
         }
     }
 
-    const int first = blockIdx.x * kThreads + threadIdx.x, step = gridDim.x * kThreads;
     // index into the ring: i < 2 * ring_size
-    auto ring_at = [&](long long i) { return i >= p.ring_size ? i - p.ring_size : i; };
+    auto ring_at = [&](uint32_t i) { return i >= static_cast<uint32_t>(p.ring_size) ? i - p.ring_size : i; };
 
-    // ---- Token rows, four at a time: one search, then a walk.
-    for (int r0 = first * kQuad; r0 < p.rows && r0 >= 0; r0 += step * kQuad) {
-        long long slot[kQuad];
-        int pos[kQuad], own[kQuad];
-        int q = r0 < rows ? last_at_most(tok, Q, r0) : 0;
-        int page = -1, column = -1;
+    // ---- Token rows.
+    const int lane = threadIdx.x & 31;
+    const int warps = gridDim.x * kWarps, warp = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    // a warp's turns are neighbours: its requests follow one another
+    const int turns = ((p.rows + kWarpRows - 1) / kWarpRows + warps - 1) / warps;
+    int qa = 0, qb = -1;                        // requests of the turn's first and last token row
+    for (int turn = 0; turn < turns; ++turn) {
+        const long long w = (static_cast<long long>(warp) * turns + turn) * kWarpRows;
+        if (w >= p.rows)
+            break;
+        const int w0 = static_cast<int>(w);
+        if (w0 < rows) {
+            qa = qb < 0 ? warp_last_at_most(tok, Q, w0, lane) : qb;
+            const int last = min(w0 + kWarpRows, rows) - 1;
+            int more = 0;
+            qb = qa;
+            do {                                // tok ascends: the requests that begin by then are a run
+                const int q = qb + 1 + lane;
+                more = __popc(__ballot_sync(~0u, q < Q && tok[min(q, Q - 1)] <= last));
+                qb += more;
+            } while (more == 32);
+        }
+        const int r0 = w0 + lane * kQuad;
+        long long slot[kQuad] = {-1, -1, -1, -1};
+        int pos[kQuad] = {-1, -1, -1, -1}, own[kQuad] = {-1, -1, -1, -1};
+        if (r0 < rows) {
+            int q = last_at_most(tok, qa, qb, r0);
+            int next = q < qb ? tok[q + 1] : rows;              // row of the next request
+            int c = ctx[q], at = c + (r0 - tok[q]);             // the row's position
+            int col = static_cast<int>(pages_before(p, static_cast<uint32_t>(at))), off = at - col * B;
+            // a column that holds older tokens is the table's, the others come from the ring
+            auto page_of = [&] {
+                return at - off < c ? p.table[q * p.table_s0 + col]
+                                    : p.ring[ring_at(static_cast<uint32_t>(start + adj[q] + col))];
+            };
+            int page = page_of();
 #pragma unroll
-        for (int k = 0; k < kQuad; ++k) {
-            const int r = r0 + k;
-            slot[k] = -1;
-            pos[k] = own[k] = -1;
-            if (r < rows) {
-                while (q + 1 < Q && tok[q + 1] <= r) {
-                    ++q;
-                    column = -1;
-                }
-                const int c = ctx[q];
-                pos[k] = c + (r - tok[q]);
-                own[k] = q;
-                const int col = pos[k] / B;
-                if (col != column) {
-                    const int have = static_cast<int>((static_cast<long long>(c) + B - 1) / B);
-                    page = col < have ? p.table[q * p.table_s0 + col]
-                                      : p.ring[ring_at(static_cast<long long>(start) + pag[q] + (col - have))];
-                    column = col;
-                }
+            for (int k = 0; k < kQuad; ++k) {
+                const int r = r0 + k;
+                if (r >= rows)
+                    break;
                 if (page >= 0)
-                    slot[k] = static_cast<long long>(page) * B + (pos[k] - col * B);
+                    slot[k] = static_cast<long long>(page) * B + off;
                 else
                     atomicOr(p.header, SDA_FLAG_BOUNDS);
+                pos[k] = at;
+                own[k] = q;
+                if (k + 1 == kQuad || r + 1 >= rows)
+                    break;
+                if (r + 1 >= next) {                            // on to the next request with rows
+                    do
+                        ++q;
+                    while (q < qb && tok[q + 1] <= r + 1);
+                    next = q < qb ? tok[q + 1] : rows;
+                    at = c = ctx[q];
+                    col = static_cast<int>(pages_before(p, static_cast<uint32_t>(at)));
+                    off = at - col * B;
+                    page = page_of();
+                } else {
+                    ++at;
+                    if (++off == B) {
+                        off = 0;
+                        ++col;
+                        page = page_of();
+                    }
+                }
             }
         }
         if (p.vec && r0 + kQuad <= p.rows) {
@@ -297,16 +364,16 @@ __global__ void __launch_bounds__(kThreads) sda_plan_kernel(const __grid_constan
         }
     }
 
+    const int first = blockIdx.x * kThreads + threadIdx.x, step = gridDim.x * kThreads;
     // ---- Pages taken: their table columns.
     for (int i = first; i < taken; i += step) {
-        const int q = last_at_most(pag, Q, i);
-        const int have = static_cast<int>((static_cast<long long>(ctx[q]) + B - 1) / B);
-        p.table[q * p.table_s0 + have + (i - pag[q])] = p.ring[ring_at(static_cast<long long>(start) + i)];
+        const int q = last_at_most(pag, 0, Q - 1, i);
+        p.table[q * p.table_s0 + (i - adj[q])] = p.ring[ring_at(static_cast<uint32_t>(start + i))];
     }
     // ---- Pages returned: behind the ring's last free page.
     for (int i = first; i < returned; i += step) {
-        const int q = last_at_most(rel, Q, i);
-        const long long at = static_cast<long long>(start) + count + i;       // < 2 * ring_size: they fit
+        const int q = last_at_most(rel, 0, Q - 1, i);
+        const uint32_t at = static_cast<uint32_t>(start) + count + i;         // < 2 * ring_size: they fit
         p.ring[ring_at(at)] = p.table[q * p.table_s0 + (i - rel[q])];
     }
 }
@@ -377,17 +444,19 @@ extern "C" sda_status sparse_decode_plan_step(const sda_tensor *context_lens, co
     p.block = block_size;
     p.ring_size = static_cast<int>(ring);
     p.rows = static_cast<int>(rows);
+    p.inverse = block_size > 1 ? ~0ull / static_cast<unsigned>(block_size) + 1 : 0;
     p.vec = aligned(p.slots, 16) && aligned(p.positions, 16) && aligned(p.owners, 16);
 
-    const size_t smem = 5 * sizeof(int32_t) * static_cast<size_t>(Q);
+    const size_t smem = kArrays * sizeof(int32_t) * static_cast<size_t>(Q);
     static size_t raised[64] = {};
-    if (smem > 48 * 1024 && !raise_smem(sda_plan_kernel, 5 * sizeof(int32_t) * kMaxRequests, raised))
+    if (smem > 48 * 1024 && !raise_smem(sda_plan_kernel, kArrays * sizeof(int32_t) * kMaxRequests, raised))
         return SDA_ERR_CUDA;
     const int sms = sm_count();
     if (sms < 1)
         return SDA_ERR_CUDA;
-    // One CTA while it can write the rows in two turns; else as many as have two turns to do.
-    const int64_t want = (rows + kRowsPerCta - 1) / kRowsPerCta;
-    const int grid = static_cast<int>(want < 1 ? 1 : want < sms ? want : sms);
+    // One CTA while its warps have one turn of rows each; else a turn per warp, up to
+    // a CTA an SM.
+    const int64_t want = (rows + kWarps * kWarpRows - 1) / (kWarps * kWarpRows);
+    const int grid = static_cast<int>(std::min<int64_t>(sms, std::max<int64_t>(1, want)));
     return launch_pdl(sda_plan_kernel, dim3(grid), dim3(kThreads), smem, stream, p);
 }

@@ -1,18 +1,20 @@
 // Rotary positions with several axes, and keys and values into the paged cache.
 //
 // A pair (a, b) turned by the angle t becomes (a cos t - b sin t, b cos t + a
-// sin t), t = position * inv_freq.  In turns, t / 2 pi = position * f with f in
-// [0, 1) held as a 64-bit fraction: the low 64 bits of the integer product are
-// the fractional turn, so an angle of any position is reduced with no loss
-// beyond f's own 2^-53, where an fp32 angle near 2^18 is off by 2^-6.
+// sin t), t = position * inv_freq.  In turns, t / 2 pi = position * f with f held
+// as a 64-bit fraction of a turn: the low 64 bits of the integer product are the
+// fractional turn, so an angle of any position is reduced with no loss beyond
+// f's own last bit (2^-33 of a turn at position 2^31), where an fp32 angle near
+// 2^18 is off by 2^-6.
 //
-// The work is one pass over q, k and v: bound by memory.  A CTA takes one or
-// more tokens: its threads first fill a table of the tokens' (cos, sin) pairs
-// in shared memory, once for all heads; then each thread keeps the eight pairs
-// of its chunk of a head in registers and walks over the heads, 32 bytes in and
-// 32 out at a time, neighbouring lanes on neighbouring bytes.
+// The work is one pass over q, k and v, bound by memory.  A CTA takes one or
+// more tokens: its threads fill a table of the tokens' (cos, sin) pairs in
+// shared memory, once for all heads, while their first loads are in flight;
+// then each thread keeps to one 16-dim chunk and walks over its rows, the next
+// one loaded while one is turned, neighbouring lanes on neighbouring bytes.
 #include "sda_common.cuh"
 
+#include <algorithm>
 #include <cmath>
 
 namespace {
@@ -22,7 +24,8 @@ using namespace sda;
 constexpr int kMaxThreads = 256;
 constexpr int kMaxAxes = 4;
 constexpr int kPairs = 8;                       // pairs of a chunk: 16 dims
-constexpr int kAhead = 2;                       // heads a thread loads before it turns them
+constexpr int kMaxTokens = 16;                  // of a CTA
+constexpr int kQueryTokens = 8;                 // of a CTA with queries, where there are many
 
 struct RopeParams {
     const uint16_t *query, *key, *value;
@@ -40,7 +43,8 @@ struct RopeParams {
     float amplitude;
     int tokens, heads, groups, dim, half, block;   // half: pairs a head turns
     int axes, interleaved, sections[kMaxAxes];
-    int per_cta, parts;                         // tokens a CTA takes; CTAs that share a token's heads
+    int query_ctas, query_tokens, kv_tokens;    // CTAs for the query; tokens of a CTA, of either kind
+    int parts;                                  // CTAs that share the heads of the same tokens
 };
 
 __device__ __forceinline__ uint2 quantise(const float (&x)[8], float scale)
@@ -75,136 +79,156 @@ __device__ __forceinline__ void widen(const uint4 &v, float (&x)[8])
     }
 }
 
-// A thread owns chunk j of the heads: 16 dims as two runs of eight.  Turned
-// chunks hold eight pairs: dims (8j.., half + 8j..) or, adjacent, 16j..16j+15;
-// the chunks behind them pass through.
-template <bool FP8, bool ADJACENT>
-__global__ void __launch_bounds__(kMaxThreads) sda_rope_kernel(const __grid_constant__ RopeParams p)
+// 2^64 / (2 pi) * |f|, modulo 2^64: a frequency in radians as a fraction of a
+// turn, from f's 24-bit significand times the 64-bit constant.
+__device__ __forceinline__ unsigned long long turns_of(float f)
 {
-    extern __shared__ float2 turn[];            // [per_cta][half] (cos, sin)
-    pdl_launch_dependents();
-    pdl_wait();
+    constexpr unsigned long long kPerRadian = 0x28BE60DB9391054Aull;    // floor(2^64 / (2 pi))
+    const uint32_t bits = __float_as_uint(f);
+    const int exponent = (bits >> 23) & 0xFF;
+    const unsigned long long m = (bits & 0x7FFFFFu) | (exponent ? 0x800000u : 0u);
+    const unsigned long long lo = m * kPerRadian, hi = __umul64hi(m, kPerRadian);
+    const int down = 150 - max(exponent, 1);                            // f = m * 2^-down
+    const unsigned long long t = down <= 0    ? (down > -64 ? lo << -down : 0ull)
+                                 : down < 64  ? (lo >> down) | (hi << (64 - down))
+                                 : down < 128 ? hi >> (down - 64)
+                                              : 0ull;
+    return bits >> 31 ? 0ull - t : t;
+}
 
+// One CTA's rows: the query heads, or the key and value heads, of its tokens.  A
+// thread owns chunk j of its rows: 16 dims as two runs of eight.  Turned chunks
+// hold eight pairs: dims (8j.., half + 8j..) or, adjacent, 16j..16j+15; the
+// chunks behind them pass through.
+template <bool KV, bool FP8, bool ADJACENT>
+__device__ __forceinline__ void rope_rows(const RopeParams &p, float4 *turn, int64_t *cache_at, int t0, int tokens,
+                                          int part)
+{
     const int chunks = p.dim / 16, lanes = blockDim.x / chunks;
     const int j = threadIdx.x % chunks, y = threadIdx.x / chunks;
-    const int part = blockIdx.x % p.parts;
-    const int t0 = static_cast<int>(blockIdx.x / p.parts) * p.per_cta, t1 = min(p.tokens, t0 + p.per_cta);
     const bool turned = j < p.half / kPairs;
     const int lo = turned && !ADJACENT ? kPairs * j : 16 * j;
     const int hi = turned && !ADJACENT ? p.half + kPairs * j : 16 * j + 8;
+    const int heads = KV ? 2 * p.groups : p.heads;              // of a token: keys, then values
 
-    // ---- (cos, sin) of the tokens' angles.
-    for (int i = threadIdx.x; i < p.half * (t1 - t0); i += blockDim.x) {
-        const int tok = i / p.half, pair = i - tok * p.half;
+    // This thread's rows: number part * lanes + y of the CTA's, and every
+    // `step`-th after it; the next is loaded while one is turned.
+    const int step = lanes * p.parts;
+    int tok = 0, head = part * lanes + y;       // of the next row; token >= tokens: none
+    uint4 a, b;                                 // its two runs
+    auto load = [&] {
+        while (head >= heads && tok < tokens) {
+            head -= heads;
+            ++tok;
+        }
+        if (tok < tokens) {
+            const bool v = KV && head >= p.groups;
+            const uint16_t *src = !KV  ? p.query + (t0 + tok) * p.q_s0 + head * p.q_s1
+                                  : !v ? p.key + (t0 + tok) * p.k_s0 + head * p.k_s1
+                                       : p.value + (t0 + tok) * p.v_s0 + (head - p.groups) * p.v_s1;
+            a = *reinterpret_cast<const uint4 *>(src + (v ? 16 * j : lo));
+            b = *reinterpret_cast<const uint4 *>(src + (v ? 16 * j + 8 : hi));
+        }
+    };
+    load();
+
+    // ---- The tokens' places and (cos, sin) of their angles.
+    for (int i = threadIdx.x; i < tokens; i += blockDim.x) {
+        int64_t place = 0;
+        if (p.slots) {
+            const int64_t slot = p.slots[t0 + i];
+            const bool bad = slot < 0 || (p.key && slot >= p.cache_slots);
+            if (bad && slot != -1 && p.flags)
+                atomicOr(p.flags, SDA_FLAG_BOUNDS);
+            if (!bad && KV) {
+                const int64_t page = slot / p.block;
+                place = page * p.c_s0 + (slot - page * p.block) * p.c_s2;
+            }
+            place = bad ? -1 : place;
+        }
+        cache_at[i] = place;
+    }
+    for (int i = threadIdx.x; i < p.half * tokens; i += blockDim.x) {
+        const int tk = i / p.half, pair = i - tk * p.half;
         int axis = 0;
         if (p.interleaved) {
-            const int a = pair % p.axes;
-            axis = a > 0 && pair / p.axes < p.sections[a] ? a : 0;
+            const int ax = pair % p.axes;
+            axis = ax > 0 && pair / p.axes < p.sections[ax] ? ax : 0;
         } else {
             int end = p.sections[0];
             while (axis + 1 < p.axes && pair >= end)
                 end += p.sections[++axis];
         }
-        const double f = static_cast<double>(p.inv_freq[pair]) * 0.15915494309189533577;   // / 2 pi
-        const unsigned long long frac = __double2ull_rn((f - floor(f)) * 18446744073709551616.0);
-        const long long pos = p.positions[axis * p.p_s0 + static_cast<int64_t>(t0 + tok) * p.p_s1];
-        const long long turns = static_cast<long long>(static_cast<unsigned long long>(pos) * frac);
+        const long long pos = p.positions[axis * p.p_s0 + static_cast<int64_t>(t0 + tk) * p.p_s1];
+        const long long turns = static_cast<long long>(static_cast<unsigned long long>(pos) * turns_of(p.inv_freq[pair]));
         float s, c;
         sincospif(static_cast<float>(static_cast<int>(turns >> 32)) * 4.656612873077393e-10f, &s, &c);   // * 2^-31
-        turn[i] = make_float2(c * p.amplitude, s * p.amplitude);
+        reinterpret_cast<float2 *>(turn)[i] = make_float2(c * p.amplitude, s * p.amplitude);
     }
     __syncthreads();
 
-    const float ks = FP8 && p.key ? *p.k_scale : 1.0f, vs = FP8 && p.key ? *p.v_scale : 1.0f;
-    const int total = p.heads + (p.key ? 2 * p.groups : 0);      // q heads, then k, then v
-    const int stride = lanes * p.parts;
-    if (y >= lanes)
-        return;
-    for (int t = t0; t < t1; ++t) {
-        int64_t slot = -1;
-        if (p.slots) {
-            slot = p.slots[t];
-            if (slot < 0 || (p.key && slot >= p.cache_slots)) {
-                if (slot != -1 && p.flags && threadIdx.x == 0)
-                    atomicOr(p.flags, SDA_FLAG_BOUNDS);
-                continue;
+    const float ks = FP8 && KV ? *p.k_scale : 1.0f, vs = FP8 && KV ? *p.v_scale : 1.0f;
+    while (tok < tokens) {
+        const int t = tok, h = head;
+        float x[8], z[8];
+        widen(a, x);
+        widen(b, z);
+        head += step;
+        load();
+        const int64_t token_at = cache_at[t];
+        if (token_at < 0)
+            continue;
+        const bool v = KV && h >= p.groups;
+        if (turned && !v) {
+            const float4 *cs = turn + (t * p.half + kPairs * j) / 2;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float4 w = cs[i];                     // pairs 2i, 2i + 1 of the chunk
+                float *r = ADJACENT ? (i < 2 ? x : z) + 4 * (i & 1) : nullptr;
+                float &a0 = ADJACENT ? r[0] : x[2 * i], &b0 = ADJACENT ? r[1] : z[2 * i];
+                float &a1 = ADJACENT ? r[2] : x[2 * i + 1], &b1 = ADJACENT ? r[3] : z[2 * i + 1];
+                const float u0 = a0, u1 = a1;
+                a0 = u0 * w.x - b0 * w.y;
+                b0 = b0 * w.x + u0 * w.y;
+                a1 = u1 * w.z - b1 * w.w;
+                b1 = b1 * w.z + u1 * w.w;
             }
         }
-        int64_t page = 0, off = 0;
-        if (p.key) {
-            page = slot / p.block;
-            off = slot - page * p.block;
-        }
-        float2 cs[kPairs];
-        if (turned) {
-#pragma unroll
-            for (int i = 0; i < kPairs; ++i)
-                cs[i] = turn[(t - t0) * p.half + kPairs * j + i];
-        }
-        for (int h0 = part * lanes + y; h0 < total; h0 += stride * kAhead) {
-            uint4 a[kAhead], b[kAhead];
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const int h = h0 + k * stride;
-                if (h < total) {
-                    const int kh = h - p.heads;                  // >= 0: k head, then v head
-                    const uint16_t *src = kh < 0 ? p.query + t * p.q_s0 + h * p.q_s1
-                                          : kh < p.groups ? p.key + t * p.k_s0 + kh * p.k_s1
-                                                          : p.value + t * p.v_s0 + (kh - p.groups) * p.v_s1;
-                    const bool v = kh >= p.groups;
-                    a[k] = *reinterpret_cast<const uint4 *>(src + (v ? 16 * j : lo));
-                    b[k] = *reinterpret_cast<const uint4 *>(src + (v ? 16 * j + 8 : hi));
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const int h = h0 + k * stride;
-                if (h >= total)
-                    break;
-                const int kh = h - p.heads;
-                const bool v = kh >= p.groups;
-                float x[8], z[8];
-                widen(a[k], x);
-                widen(b[k], z);
-                if (turned && !v) {
-                    if constexpr (ADJACENT) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float x0 = x[2 * i], x1 = x[2 * i + 1], z0 = z[2 * i], z1 = z[2 * i + 1];
-                            x[2 * i] = x0 * cs[i].x - x1 * cs[i].y;
-                            x[2 * i + 1] = x1 * cs[i].x + x0 * cs[i].y;
-                            z[2 * i] = z0 * cs[4 + i].x - z1 * cs[4 + i].y;
-                            z[2 * i + 1] = z1 * cs[4 + i].x + z0 * cs[4 + i].y;
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float x0 = x[i], z0 = z[i];
-                            x[i] = x0 * cs[i].x - z0 * cs[i].y;
-                            z[i] = z0 * cs[i].x + x0 * cs[i].y;
-                        }
-                    }
-                }
-                const int d0 = v ? 16 * j : lo, d1 = v ? 16 * j + 8 : hi;
-                if (kh < 0) {
-                    uint16_t *dst = p.query_out + t * p.o_s0 + h * p.o_s1;
-                    *reinterpret_cast<uint4 *>(dst + d0) = round_bf16(x);
-                    *reinterpret_cast<uint4 *>(dst + d1) = round_bf16(z);
-                } else {
-                    const int64_t at = page * p.c_s0 + (v ? kh - p.groups : kh) * p.c_s1 + off * p.c_s2 +
-                                       (v ? p.dim : 0);
-                    if constexpr (FP8) {
-                        uint8_t *dst = static_cast<uint8_t *>(p.cache) + at;
-                        *reinterpret_cast<uint2 *>(dst + d0) = quantise(x, v ? vs : ks);
-                        *reinterpret_cast<uint2 *>(dst + d1) = quantise(z, v ? vs : ks);
-                    } else {
-                        uint16_t *dst = static_cast<uint16_t *>(p.cache) + at;
-                        *reinterpret_cast<uint4 *>(dst + d0) = round_bf16(x);
-                        *reinterpret_cast<uint4 *>(dst + d1) = round_bf16(z);
-                    }
-                }
+        if constexpr (!KV) {
+            uint16_t *dst = p.query_out + (t0 + t) * p.o_s0 + h * p.o_s1;
+            *reinterpret_cast<uint4 *>(dst + lo) = round_bf16(x);
+            *reinterpret_cast<uint4 *>(dst + hi) = round_bf16(z);
+        } else {
+            const int64_t place = token_at + (v ? h - p.groups : h) * p.c_s1;
+            const int d0 = v ? p.dim + 16 * j : lo, d1 = v ? p.dim + 16 * j + 8 : hi;
+            if constexpr (FP8) {
+                uint8_t *dst = static_cast<uint8_t *>(p.cache) + place;
+                *reinterpret_cast<uint2 *>(dst + d0) = quantise(x, v ? vs : ks);
+                *reinterpret_cast<uint2 *>(dst + d1) = quantise(z, v ? vs : ks);
+            } else {
+                uint16_t *dst = static_cast<uint16_t *>(p.cache) + place;
+                *reinterpret_cast<uint4 *>(dst + d0) = round_bf16(x);
+                *reinterpret_cast<uint4 *>(dst + d1) = round_bf16(z);
             }
         }
+    }
+}
+
+template <bool FP8, bool ADJACENT>
+__global__ void __launch_bounds__(kMaxThreads, 5) sda_rope_kernel(const __grid_constant__ RopeParams p)
+{
+    extern __shared__ float4 turn[];            // [tokens][half / 2]: (cos, sin, cos, sin) of two pairs
+    __shared__ int64_t cache_at[kMaxTokens];    // each token's place in the cache, -1: a row to leave out
+    pdl_launch_dependents();
+    pdl_wait();
+    const int cta = static_cast<int>(blockIdx.x);
+    if (cta < p.query_ctas) {
+        const int t0 = cta / p.parts * p.query_tokens;
+        rope_rows<false, FP8, ADJACENT>(p, turn, cache_at, t0, min(p.tokens - t0, p.query_tokens), cta % p.parts);
+    } else {
+        const int t0 = (cta - p.query_ctas) / p.parts * p.kv_tokens;
+        rope_rows<true, FP8, ADJACENT>(p, turn, cache_at, t0, min(p.tokens - t0, p.kv_tokens),
+                                       (cta - p.query_ctas) % p.parts);
     }
 }
 
@@ -353,17 +377,29 @@ extern "C" sda_status sparse_decode_rope_append(const sda_tensor *query, const s
     const int sms = sm_count();
     if (sms < 1)
         return SDA_ERR_CUDA;
-    const int chunks = static_cast<int>(dim) / 16, lanes = kMaxThreads / chunks;
-    const int total = static_cast<int>(heads + 2 * groups);
-    // Many tokens: four to a CTA, so that the table of angles keeps all threads
-    // busy.  Few: a token's heads are shared by CTAs until each SM has two.
-    p.per_cta = tokens >= 16 * static_cast<int64_t>(sms) ? 4 : 1;
-    const int64_t ctas = (tokens + p.per_cta - 1) / p.per_cta;
+    const int chunks = static_cast<int>(dim) / 16, most = kMaxThreads / chunks;
+    // Many tokens: a few to a CTA, so that the table of angles keeps all threads
+    // busy.  Few: a token to a CTA, its heads shared by CTAs until each SM has two.
+    // Keys and values have CTAs of their own, with more tokens for their fewer rows.
+    const int rows = static_cast<int>(std::max(heads, 2 * groups));
+    const bool many = tokens >= 16 * static_cast<int64_t>(sms);
+    p.query_tokens = many ? kQueryTokens : 1;
+    p.kv_tokens = many ? static_cast<int>(std::clamp<int64_t>(kQueryTokens * heads / std::max<int64_t>(1, 2 * groups),
+                                                              kQueryTokens, kMaxTokens))
+                       : 1;
+    auto blocks = [&](int64_t h, int per) { return h > 0 ? (tokens + per - 1) / per : 0; };
+    const int64_t ctas = blocks(heads, p.query_tokens) + blocks(groups, p.kv_tokens);
     p.parts = 1;
-    while (ctas * p.parts < 2 * sms && p.parts * lanes < total)
+    while (ctas * p.parts < 2 * sms && p.parts * most < rows)
         p.parts *= 2;
+    p.query_ctas = static_cast<int>(blocks(heads, p.query_tokens) * p.parts);
+    // Threads for as many rows at a time as take the fewest turns, none of them short.
+    const int longest = rows * (heads > 0 ? p.query_tokens : p.kv_tokens);
+    const int turns = (longest + most * p.parts - 1) / (most * p.parts);
+    const int lanes = (longest + turns * p.parts - 1) / (turns * p.parts);
     const dim3 grid(static_cast<unsigned>(ctas * p.parts)), block(static_cast<unsigned>(chunks * lanes));
-    const size_t smem = sizeof(float2) * static_cast<size_t>(p.per_cta) * static_cast<size_t>(half);
+    const size_t smem = sizeof(float2) * static_cast<size_t>(std::max(p.query_tokens, p.kv_tokens)) *
+                        static_cast<size_t>(half);
     auto kernel = fp8 ? (adjacent_pairs ? sda_rope_kernel<true, true> : sda_rope_kernel<true, false>)
                       : (adjacent_pairs ? sda_rope_kernel<false, true> : sda_rope_kernel<false, false>);
     return launch_pdl(kernel, grid, block, smem, stream, p);
