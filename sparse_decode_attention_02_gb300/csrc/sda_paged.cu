@@ -386,6 +386,9 @@ extern "C" sda_status sparse_decode_paged_attention(const sda_tensor *query, con
     const int64_t want = p.whole_units ? units : (units * (widest + kUnitCost) - 1) / (kMinTiles + kUnitCost) + 1;
     p.ctas = static_cast<int>(std::min<int64_t>(most, std::max<int64_t>(1, want)));
     p.workers = p.ctas * per_cta;
+    p.workers_inv = inverse_of(static_cast<unsigned>(p.workers));
+    p.tile_inv = inverse_of(static_cast<unsigned>(p.tile));
+    p.per_block_inv = inverse_of(static_cast<unsigned>(p.block / p.piece));
 
     const sda_status st = dim == 64    ? launch_64(fp8, tmap, p, stream)
                           : dim == 128 ? launch_128(fp8, tmap, p, stream)

@@ -82,6 +82,7 @@ struct Params {
     int table_cols, block, cap;                 // cap: tokens the table's width can hold
     int piece, tile;                            // tokens of a TMA box and of a stage
     int ctas, workers, min_tiles, whole_units;
+    unsigned long long per_block_inv, tile_inv, workers_inv;    // inverse_of the pieces of a page, tile, workers
     int q_vec, o_vec;                           // 8-byte loads of q and stores of the output
 };
 
@@ -101,6 +102,18 @@ constexpr int tiles_of_rows(int rows)
     return rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
 }
 
+// x / d as a product: floor(x * inverse_of(d) / 2^64) is exact for x, d < 2^32
+// (d == 1 has no 64-bit inverse: 0 stands for it).
+constexpr unsigned long long inverse_of(unsigned d)
+{
+    return d > 1 ? ~0ull / d + 1 : 0;
+}
+
+__device__ __forceinline__ uint32_t quotient(uint32_t x, unsigned long long inverse)
+{
+    return inverse ? static_cast<uint32_t>(__umul64hi(x, inverse)) : x;
+}
+
 template <bool FP8, int D, int MT>
 struct Shape {
     static constexpr int kElt = FP8 ? 1 : 2;
@@ -110,9 +123,14 @@ struct Shape {
     static constexpr int kStageBytes = kSlots * kRowBytes;
     static constexpr int kSteps = D / 16;                       // QK k-steps
     static constexpr int kWorkers = kWarps / MT;                // of a CTA
-    static constexpr int kRing = 96 * 1024 / kStageBytes / kWorkers;    // stages of a worker
+    // Q fragments stay in registers, beside the output's D / 2, but for 256 dims:
+    // there they take a third of the ring's place (each lane its own words).
+    static constexpr bool kQShared = D > 192;
+    static constexpr int kQBytes = kQShared ? kSteps * 32 * 16 : 0;     // of a warp
+    static constexpr int kRing = (96 * 1024 - kWarps * kQBytes) / kStageBytes / kWorkers;   // stages of a worker
     static constexpr int kStages = kRing * kWorkers;
-    static constexpr int kBarOff = kStages * kStageBytes;
+    static constexpr int kQOff = kStages * kStageBytes;
+    static constexpr int kBarOff = kQOff + kWarps * kQBytes;
     static constexpr int kHdrOff = kBarOff + 16 * kStages;
     static constexpr int kIssuedOff = kHdrOff + 8 * kStages;
     static constexpr int kCtlOff = (kIssuedOff + 4 * kStages + 15) / 16 * 16;
@@ -136,7 +154,7 @@ struct Walk {
 
     static __device__ __forceinline__ int tiles_of(const Params &p, int len)
     {
-        return len > 0 ? (len - 1) / p.tile + 1 : 0;
+        return len > 0 ? static_cast<int>(quotient(len - 1, p.tile_inv)) + 1 : 0;
     }
 
     __device__ __forceinline__ bool next(const Params &p, Segment &s)
@@ -414,7 +432,18 @@ __device__ __forceinline__ int2 find_parts(const Params &p, long long *scan, Par
     long long *ends = scan + kWarps;            // where the workers' parts begin and end on the line
     if (threadIdx.x < 2 * WORKERS) {
         const int v = who.x + static_cast<int>(threadIdx.x >> 1) * who.y;
-        ends[threadIdx.x] = v < used ? total * (v + static_cast<int>(threadIdx.x & 1)) / used : -1;
+        const int i = v + static_cast<int>(threadIdx.x & 1);
+        long long x = -1;
+        if (used < p.workers) {                 // a short line
+            if (v < used)
+                x = static_cast<unsigned>(total) * static_cast<unsigned>(i) / static_cast<unsigned>(used);
+        } else {                                // floor(total * i / workers); the product's inverse may fall one short
+            const unsigned long long n = static_cast<unsigned long long>(total) * i;
+            unsigned long long k = p.workers > 1 ? __umul64hi(n, p.workers_inv - 1) : n;
+            k += n - k * p.workers >= static_cast<unsigned>(p.workers);
+            x = static_cast<long long>(k);
+        }
+        ends[threadIdx.x] = x;
     }
     __syncthreads();
     const long long at0 = (before + inc - mine) * p.groups, at1 = at0 + mine * p.groups;   // this thread's requests
@@ -433,7 +462,8 @@ __device__ __forceinline__ int2 find_parts(const Params &p, long long *scan, Par
                 break;
             at += len * p.groups;
         }
-        const int g = static_cast<int>((x - at) / len);
+        const unsigned long long in = x - at;
+        const int g = static_cast<int>(in >> 32 || len >> 32 ? in / len : static_cast<unsigned>(in) / static_cast<unsigned>(len));
         const long long u0 = at + g * len;
         parts[w] = {x1 - u0, u0, q, g, static_cast<int>(max(x - u0 - kUnitCost, 0ll)), 0};
     }
@@ -450,7 +480,7 @@ struct Feed {
     Segment seg;
     bool more;
     int tile;                                   // of the segment, the next to look up
-    int per_stage, lane_stage, lane_piece;      // pieces of a stage; this lane's place in a batch
+    int per_stage, batch, lane_stage, lane_piece;   // pieces of a stage, stages of a batch; the lane's place in one
     int at, n, group, page, off, left;          // the batch: next stage to issue, stages, ...
     int n2, group2, page2, off2, left2;         // the one after
 
@@ -465,12 +495,12 @@ struct Feed {
         n2 = 0;
         if (!more)
             return;
-        const int P = p.piece, per_block = p.block / P;
-        n2 = min(32 / per_stage, seg.last - tile);
+        const int P = p.piece;
+        n2 = min(batch, seg.last - tile);
         group2 = seg.group;
         const int f = (tile + lane_stage) * per_stage + lane_piece;
-        const int col = f / per_block;
-        off2 = (f - col * per_block) * P;
+        const int col = static_cast<int>(quotient(f, p.per_block_inv));
+        off2 = f * P - col * p.block;
         left2 = lane_stage < n2 ? seg.len - f * P : 0;          // tokens from the piece's first on
         page2 = left2 > 0 && col < p.table_cols ? p.block_table[seg.request * p.bt_s0 + col] : -1;
         tile += n2;
@@ -484,6 +514,7 @@ struct Feed {
     {
         walk = from;
         per_stage = p.tile / p.piece;
+        batch = 32 / per_stage;
         lane_stage = lane / per_stage;
         lane_piece = lane - lane_stage * per_stage;
         more = walk.next(p, seg);
@@ -623,24 +654,25 @@ __global__ void __launch_bounds__(kThreads, 2)
         // that puts the row's largest |q| in [2^14, 2^15), undone in the logit
         // scale: any bf16 row is exact down to 2^-31 of its largest value.
         uint32_t qf[S::kSteps][4];
-        {
-            const uint16_t *qp[2] = {p.query + row_of(r0) * p.q_s0 + (r0 % H) * p.q_s1,
-                                     p.query + row_of(r1) * p.q_s0 + (r1 % H) * p.q_s1};
 #pragma unroll
-            for (int kk = 0; kk < S::kSteps; ++kk) {
-                const int d = FP8 ? 64 * (kk >> 2) + 16 * t + 4 * (kk & 3) : 32 * (kk >> 1) + 8 * t + 4 * (kk & 1);
+        for (int k = 0; k < 2; ++k) {
+            const int r = k ? r1 : r0, rq = r < R ? r : 0;      // rows past R read row 0 and count as zeros
+            const uint32_t keep = r < R ? ~0u : 0u;
+            const uint16_t *q = p.query + row_of(rq) * p.q_s0 + (rq % H) * p.q_s1 + (FP8 ? 16 : 8) * t;
+            auto dim = [](int kk) { return FP8 ? 64 * (kk >> 2) + 4 * (kk & 3) : 32 * (kk >> 1) + 4 * (kk & 1); };
+            if (p.q_vec) {
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    uint2 w = make_uint2(0, 0);
-                    if ((k ? r1 : r0) < R) {
-                        if (p.q_vec)
-                            w = *reinterpret_cast<const uint2 *>(qp[k] + d);
-                        else
-                            w = make_uint2(qp[k][d] | (static_cast<uint32_t>(qp[k][d + 1]) << 16),
-                                           qp[k][d + 2] | (static_cast<uint32_t>(qp[k][d + 3]) << 16));
-                    }
-                    qf[kk][k] = w.x;
-                    qf[kk][2 + k] = w.y;
+                for (int kk = 0; kk < S::kSteps; ++kk) {
+                    const uint2 w = *reinterpret_cast<const uint2 *>(q + dim(kk));
+                    qf[kk][k] = w.x & keep;
+                    qf[kk][2 + k] = w.y & keep;
+                }
+            } else {
+#pragma unroll
+                for (int kk = 0; kk < S::kSteps; ++kk) {
+                    const uint16_t *w = q + dim(kk);
+                    qf[kk][k] = (w[0] | (static_cast<uint32_t>(w[1]) << 16)) & keep;
+                    qf[kk][2 + k] = (w[2] | (static_cast<uint32_t>(w[3]) << 16)) & keep;
                 }
             }
         }
@@ -665,6 +697,15 @@ __global__ void __launch_bounds__(kThreads, 2)
                         qf[kk][i] = pack2<true>(__uint_as_float(qf[kk][i] << 16) * up,
                                                 __uint_as_float(qf[kk][i] & 0xFFFF0000u) * up);
             }
+        }
+
+        const uint32_t qshared = smem_u32(smem) + S::kQOff + warp * S::kQBytes + lane * 16;
+        if constexpr (S::kQShared) {
+#pragma unroll
+            for (int kk = 0; kk < S::kSteps; ++kk)
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(qshared + kk * 512), "r"(qf[kk][0]),
+                             "r"(qf[kk][1]), "r"(qf[kk][2]), "r"(qf[kk][3])
+                             : "memory");
         }
 
         float o[D / 8][4];
@@ -713,19 +754,29 @@ __global__ void __launch_bounds__(kThreads, 2)
                             w[i][2] = x.z;
                             w[i][3] = x.w;
                         }
-                        if constexpr (FP8) {
+                        constexpr int kChunkSteps = FP8 ? 4 : 2;
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
+                        for (int k = 0; k < kChunkSteps; ++k) {
+                            uint32_t q[4];
+                            if constexpr (S::kQShared) {
+                                const uint4 x = lds128(qshared + (kChunkSteps * c + k) * 512);
+                                q[0] = x.x;
+                                q[1] = x.y;
+                                q[2] = x.z;
+                                q[3] = x.w;
+                            } else {
 #pragma unroll
-                                for (int i = 0; i < kGroup; ++i)
-                                    mma16816<true>(sc[i0 + i], qf[4 * c + k], e4m3x2_to_f16x2(w[i][k]),
+                                for (int i = 0; i < 4; ++i)
+                                    q[i] = qf[kChunkSteps * c + k][i];
+                            }
+#pragma unroll
+                            for (int i = 0; i < kGroup; ++i) {
+                                if constexpr (FP8)
+                                    mma16816<true>(sc[i0 + i], q, e4m3x2_to_f16x2(w[i][k]),
                                                    e4m3x2_to_f16x2(w[i][k] >> 16));
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 2; ++k)
-#pragma unroll
-                                for (int i = 0; i < kGroup; ++i)
-                                    mma16816<false>(sc[i0 + i], qf[2 * c + k], w[i][2 * k], w[i][2 * k + 1]);
+                                else
+                                    mma16816<false>(sc[i0 + i], q, w[i][2 * k], w[i][2 * k + 1]);
+                            }
                         }
                     }
                 }
@@ -998,37 +1049,34 @@ __global__ void __launch_bounds__(kThreads, 2)
             uint16_t *out = p.output + row * p.o_s0 + h * p.o_s1;
             float *part = p.partial + (piece * R + r) * D;
             // E4M3: thread t has four dims of each 16; bf16: two of each 8
-            constexpr int kRun = FP8 ? 4 : 2;
+            constexpr int kRun = FP8 ? 4 : 2, kRuns = D / (4 * kRun);
+            out += kRun * t;
+            part += kRun * t;
+            auto value = [&](int c, int i) { return (FP8 ? o[2 * c + (i & 1)][2 * k + (i >> 1)] : o[c][2 * k + i]) * f; };
+            if (!whole) {
 #pragma unroll
-            for (int c = 0; c < D / (4 * kRun); ++c) {
-                const int d = 4 * kRun * c + kRun * t;
-                float x[kRun];
-#pragma unroll
-                for (int i = 0; i < kRun; ++i)
-                    x[i] = (FP8 ? o[2 * c + (i & 1)][2 * k + (i >> 1)] : o[c][2 * k + i]) * f;
-                if (!whole) {
+                for (int c = 0; c < kRuns; ++c) {
                     if constexpr (FP8)
-                        *reinterpret_cast<float4 *>(part + d) = make_float4(x[0], x[1], x[2], x[3]);
+                        *reinterpret_cast<float4 *>(part + 16 * c) =
+                            make_float4(value(c, 0), value(c, 1), value(c, 2), value(c, 3));
                     else
-                        *reinterpret_cast<float2 *>(part + d) = make_float2(x[0], x[1]);
-                    continue;
+                        *reinterpret_cast<float2 *>(part + 8 * c) = make_float2(value(c, 0), value(c, 1));
                 }
-                uint32_t w[kRun / 2];
+            } else if (p.o_vec) {
 #pragma unroll
-                for (int i = 0; i < kRun / 2; ++i)
-                    w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
-                if (p.o_vec) {
+                for (int c = 0; c < kRuns; ++c) {
+                    const uint32_t w = pack_bf16(value(c, 0), value(c, 1));
                     if constexpr (FP8)
-                        *reinterpret_cast<uint2 *>(out + d) = make_uint2(w[0], w[1]);
+                        *reinterpret_cast<uint2 *>(out + 16 * c) = make_uint2(w, pack_bf16(value(c, 2), value(c, 3)));
                     else
-                        *reinterpret_cast<uint32_t *>(out + d) = w[0];
-                } else {
-#pragma unroll
-                    for (int i = 0; i < kRun / 2; ++i) {
-                        out[d + 2 * i] = static_cast<uint16_t>(w[i]);
-                        out[d + 2 * i + 1] = static_cast<uint16_t>(w[i] >> 16);
-                    }
+                        *reinterpret_cast<uint32_t *>(out + 8 * c) = w;
                 }
+            } else {
+#pragma unroll
+                for (int c = 0; c < kRuns; ++c)
+#pragma unroll
+                    for (int i = 0; i < kRun; ++i)
+                        out[4 * kRun * c + i] = __bfloat16_as_ushort(__float2bfloat16_rn(value(c, i)));
             }
         }
         // ---- The worker that has a cut unit's first tile lists it for the join.
