@@ -10,7 +10,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SOURCES = [os.path.join(HERE, "csrc", name) for name in (
     "sdattn.cu", "sda_select.cu", "sda_index.cu", "sda_plan.cu", "sda_rope.cu", "sda_paged.cu",
-    "sda_paged_64.cu", "sda_paged_128.cu", "sda_paged_192.cu", "sda_paged_256.cu")]
+    *(f"sda_paged_{kind}_{dim}.cu" for kind in ("bf16", "fp8") for dim in (64, 128, 192, 256)))]
 INCLUDES = [os.path.join(HERE, "csrc", name) for name in ("sda_common.cuh", "sda_paged.cuh")]
 HEADER = os.path.join(ROOT, "include", "sdattn.h")
 OUT_DIR = os.path.join(HERE, "_build")

@@ -47,8 +47,11 @@ __global__ void __launch_bounds__(kJoinThreads) sda_paged_join_kernel(const __gr
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int count = min(static_cast<int>(p.flags[kItemWord]), kMaxItems), H = p.heads;
+    JoinItem next = p.items[min(static_cast<int>(blockIdx.x), kMaxItems - 1)];     // beside the count: one latency
     for (int i = blockIdx.x; i < count; i += gridDim.x) {
-        const JoinItem item = p.items[i];
+        const JoinItem item = next;
+        if (i + static_cast<int>(gridDim.x) < count)
+            next = p.items[i + gridDim.x];
         const int n = item.pieces;
         const bool shared = n > kManyPieces;
         const int r = item.row + (shared ? 0 : warp);
@@ -390,14 +393,17 @@ extern "C" sda_status sparse_decode_paged_attention(const sda_tensor *query, con
     p.tile_inv = inverse_of(static_cast<unsigned>(p.tile));
     p.per_block_inv = inverse_of(static_cast<unsigned>(p.block / p.piece));
 
-    const sda_status st = dim == 64    ? launch_64(fp8, tmap, p, stream)
-                          : dim == 128 ? launch_128(fp8, tmap, p, stream)
-                          : dim == 192 ? launch_192(fp8, tmap, p, stream)
-                                       : launch_256(fp8, tmap, p, stream);
+    Launch *launch = dim == 64    ? (fp8 ? launch_fp8_64 : launch_bf16_64)
+                     : dim == 128 ? (fp8 ? launch_fp8_128 : launch_bf16_128)
+                     : dim == 192 ? (fp8 ? launch_fp8_192 : launch_bf16_192)
+                                  : (fp8 ? launch_fp8_256 : launch_bf16_256);
+    const sda_status st = launch(tmap, p, stream);
     if (st != SDA_OK || p.whole_units)
         return st;
-    const int64_t rows_to_join = units * p.rows;
-    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(most, rows_to_join)));
+    // A block an item (at most eight rows of a unit) as long as they run together.
+    const int64_t items = units * ((p.rows + kJoinWarps - 1) / kJoinWarps);
+    const int64_t rows_to_join = units <= p.workers / kManyPieces ? units * p.rows : items;
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(2 * most, rows_to_join)));
     auto join = dim == 64    ? sda_paged_join_kernel<64>
                 : dim == 128 ? sda_paged_join_kernel<128>
                 : dim == 192 ? sda_paged_join_kernel<192>

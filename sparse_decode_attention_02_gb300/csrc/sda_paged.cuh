@@ -114,8 +114,13 @@ __device__ __forceinline__ uint32_t quotient(uint32_t x, unsigned long long inve
     return inverse ? static_cast<uint32_t>(__umul64hi(x, inverse)) : x;
 }
 
-template <bool FP8, int D, int MT>
+constexpr int kStateBytes = 144;                // WarpState
+
+// FULL: a piece fills a stage (pages of at least a stage's tokens, in whole
+// stages), so the offsets in a stage are constants.
+template <bool FP8, int D, int MT, bool FULL>
 struct Shape {
+    static constexpr bool kFull = FULL;
     static constexpr int kElt = FP8 ? 1 : 2;
     static constexpr int kRowBytes = 2 * D * kElt;
     static constexpr int kBands = kRowBytes / 128;
@@ -134,7 +139,8 @@ struct Shape {
     static constexpr int kHdrOff = kBarOff + 16 * kStages;
     static constexpr int kIssuedOff = kHdrOff + 8 * kStages;
     static constexpr int kCtlOff = (kIssuedOff + 4 * kStages + 15) / 16 * 16;
-    static constexpr int kBytes = kCtlOff + 128 + 4 * 32 + 1024;         // + the base's alignment
+    static constexpr int kStateOff = kCtlOff + 16 + 8 * (kThreads + kWarps);
+    static constexpr int kBytes = kStateOff + kWarps * kStateBytes + 1024;         // + the base's alignment
     static_assert(kStageBytes % 1024 == 0 && kRing >= 2 && kBytes <= 115712, "ring");
 };
 
@@ -372,112 +378,155 @@ __device__ __forceinline__ void pv_accumulate8(float (&o)[D / 8][4], const uint3
 // Where a worker's part begins, and how long it is.
 struct Part {
     long long left, start;                      // as Walk::left; the unit's place on the line
-    int request, group, tile, spare;
+    int request, group, tile;
 };
-static_assert(sizeof(Part) == 32, "four in the control block");
 
-// The line's length, the workers that get a part of it, and the parts of this
-// CTA's workers.  Where all workers get one, a CTA's four are neighbours, so that
-// their pieces of a long unit can be merged here; where there are fewer tiles,
-// worker w of the CTA is number w * CTAs + CTA, which spreads them over the SMs.
-// Every thread of the block calls it; returns the number of the CTA's first
-// worker and the step to the next.
-template <int WORKERS>
-__device__ __forceinline__ int2 find_parts(const Params &p, long long *scan, Part *parts, long long &total, int &used)
+// floor(total * i / workers) by the workers' inverse, which may fall one short.
+__device__ __forceinline__ long long boundary(const Params &p, long long total, int i)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cta = static_cast<int>(blockIdx.x);
-    const int2 spread = make_int2(cta, static_cast<int>(gridDim.x)), near = make_int2(cta * WORKERS, 1);
+    const unsigned long long n = static_cast<unsigned long long>(total) * i;
+    unsigned long long k = p.workers > 1 ? __umul64hi(n, p.workers_inv - 1) : n;
+    k += n - k * p.workers >= static_cast<unsigned>(p.workers);
+    return static_cast<long long>(k);
+}
+
+// The part of worker w of this CTA, the line's length, the workers that get a
+// part of it (`used`) and the number v of the worker among them.  Where all
+// workers get one, a CTA's are neighbours, so that their pieces of a long unit
+// can be merged here; where there are fewer tiles, worker w of the CTA is number
+// w * CTAs + CTA, which spreads them over the SMs.  Every thread of the block
+// calls it; a worker's warps look for its part together.
+// `sums`: kThreads + kWarps values of shared memory.
+template <int WORKERS>
+__device__ __forceinline__ Part find_part(const Params &p, long long *sums, int w, long long &total, int &used, int &v)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int spread = w * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
     if (p.whole_units) {
         total = static_cast<long long>(p.requests) * p.groups;
         used = p.workers;
-        if (threadIdx.x < WORKERS) {
-            const unsigned v = spread.x + threadIdx.x * spread.y;
-            const unsigned units = static_cast<unsigned>(total);        // at most 2^26, and 1216 workers
-            const long long u0 = static_cast<long long>(units) * v / p.workers;
-            const long long u1 = static_cast<long long>(units) * (v + 1) / p.workers;
-            parts[threadIdx.x] = {u1 - u0, 0, static_cast<int>(u0 / p.groups), static_cast<int>(u0 % p.groups), 0, 0};
-        }
-        __syncthreads();
-        return spread;
+        v = spread;
+        const long long u0 = boundary(p, total, v);
+        const unsigned q = static_cast<unsigned>(u0) / static_cast<unsigned>(p.groups);
+        return {boundary(p, total, v + 1) - u0, 0, static_cast<int>(q), static_cast<int>(u0 - q * p.groups), 0};
     }
+    // Spans of the requests on the line, of one group each; a thread sums a run of them.
     const int per = (p.requests + kThreads - 1) / kThreads;
     const int q0 = min(p.requests, static_cast<int>(threadIdx.x) * per), q1 = min(p.requests, q0 + per);
-    auto span = [&](int q) -> long long {       // a unit's share of the line
+    auto span = [&](int q) -> long long {
         const int tiles = Walk::tiles_of(p, Walk::length(p, q));
         return tiles > 0 ? tiles + kUnitCost : 0;
     };
     long long mine = 0;
     for (int q = q0; q < q1; ++q)
         mine += span(q);
-    long long inc = mine;
+    auto scan = [&](long long x) {              // inclusive, over the warp
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(~0u, inc, o);
-        inc += lane >= o ? v : 0;
-    }
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(~0u, x, o);
+            x += lane >= o ? y : 0;
+        }
+        return x;
+    };
+    const long long inc = scan(mine);
+    sums[threadIdx.x] = inc - mine;             // before the thread's run, in its warp
     if (lane == 31)
-        scan[warp] = inc;
+        sums[kThreads + warp] = inc;
     __syncthreads();
-    long long before = 0, all = 0;
+    long long warp_sum[kWarps], all = 0;
 #pragma unroll
     for (int k = 0; k < kWarps; ++k) {
-        before += k < warp ? scan[k] : 0;
-        all += scan[k];
+        warp_sum[k] = all;
+        all += sums[kThreads + k];
     }
     total = all * p.groups;
     const int least = p.min_tiles + kUnitCost;
     used = total >= static_cast<long long>(p.workers) * least ? p.workers
                                                                : (static_cast<int>(total) + least - 1) / least;
-    const int2 who = used == p.workers ? near : spread;
-    long long *ends = scan + kWarps;            // where the workers' parts begin and end on the line
-    if (threadIdx.x < 2 * WORKERS) {
-        const int v = who.x + static_cast<int>(threadIdx.x >> 1) * who.y;
-        const int i = v + static_cast<int>(threadIdx.x & 1);
-        long long x = -1;
-        if (used < p.workers) {                 // a short line
-            if (v < used)
-                x = static_cast<unsigned>(total) * static_cast<unsigned>(i) / static_cast<unsigned>(used);
-        } else {                                // floor(total * i / workers); the product's inverse may fall one short
-            const unsigned long long n = static_cast<unsigned long long>(total) * i;
-            unsigned long long k = p.workers > 1 ? __umul64hi(n, p.workers_inv - 1) : n;
-            k += n - k * p.workers >= static_cast<unsigned>(p.workers);
-            x = static_cast<long long>(k);
+    v = used == p.workers ? static_cast<int>(blockIdx.x) * WORKERS + w : spread;
+    if (v >= used)
+        return {0, 0, 0, 0, 0};
+    const unsigned shorter = static_cast<unsigned>(total);              // of a line with fewer workers
+    const long long x = used == p.workers ? boundary(p, total, v) : shorter * static_cast<unsigned>(v) / used;
+    const long long x1 = used == p.workers ? boundary(p, total, v + 1) : shorter * static_cast<unsigned>(v + 1) / used;
+
+    // The run that x lies in: the last that begins at or before it.
+    int run = -1;
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k)
+        run += __popc(__ballot_sync(~0u, (warp_sum[k] + sums[32 * k + lane]) * p.groups <= x));
+    // The request in the run, 32 at a time; requests without tokens span nothing.
+    long long at = warp_sum[0];
+#pragma unroll
+    for (int k = 1; k < kWarps; ++k)
+        at = run >= 32 * k ? warp_sum[k] : at;
+    at = (at + sums[run]) * p.groups;
+    int q = run * per;
+    long long len = 0;
+    for (;; q += 32) {
+        const long long s = q + lane < p.requests ? span(q + lane) : 0;
+        const long long to = scan(s) * p.groups;                        // past each request
+        const unsigned past = __ballot_sync(~0u, at + to > x);
+        if (past) {
+            const int l = __ffs(past) - 1;
+            len = __shfl_sync(~0u, s, l);
+            at += __shfl_sync(~0u, to, l) - len * p.groups;
+            q += l;
+            break;
         }
-        ends[threadIdx.x] = x;
+        if (q + 32 >= p.requests)                                       // not reached: x is on the line
+            return {0, 0, 0, 0, 0};
+        at += __shfl_sync(~0u, to, 31);
     }
-    __syncthreads();
-    const long long at0 = (before + inc - mine) * p.groups, at1 = at0 + mine * p.groups;   // this thread's requests
-#pragma unroll 1
-    for (int w = 0; w < WORKERS; ++w) {
-        const long long x = ends[2 * w], x1 = ends[2 * w + 1];
-        if (x < 0 && threadIdx.x == 0)
-            parts[w].left = 0;
-        if (x < at0 || x >= at1)
-            continue;
-        long long at = at0, len = 0;            // one thread: it has the request that x lies in
-        int q = q0;
-        for (;; ++q) {
-            len = span(q);
-            if (x < at + len * p.groups || q + 1 >= q1)
-                break;
-            at += len * p.groups;
-        }
-        const unsigned long long in = x - at;
-        const int g = static_cast<int>(in >> 32 || len >> 32 ? in / len : static_cast<unsigned>(in) / static_cast<unsigned>(len));
-        const long long u0 = at + g * len;
-        parts[w] = {x1 - u0, u0, q, g, static_cast<int>(max(x - u0 - kUnitCost, 0ll)), 0};
-    }
-    __syncthreads();
-    return who;
+    const unsigned long long in = x - at;
+    const int g = static_cast<int>(in >> 32 || len >> 32 ? in / len : static_cast<unsigned>(in) / static_cast<unsigned>(len));
+    const long long u0 = at + g * len;
+    return {x1 - u0, u0, q, g, static_cast<int>(max(x - u0 - kUnitCost, 0ll))};
 }
+
+// Where a warp is on the line.  It lies in shared memory (all lanes write the
+// same): between units it is not needed, and registers are short.
+struct Place {
+    Walk walk;
+    Segment seg;
+    long long unit;                             // where the segment's unit begins on the line
+
+    // The next segment into seg; a copy of it in `s`.
+    __device__ __forceinline__ bool next(const Params &p, long long part_end, Segment &s)
+    {
+        Walk w = walk;
+        __syncwarp();                           // every lane has read it
+        unit = part_end - w.left;
+        const bool some = w.next(p, s);
+        walk = w;
+        seg = s;
+        __syncwarp();
+        return some;
+    }
+};
+
+struct WarpState {
+    Place here, ahead;                          // of the warp's products and of its feed
+    long long part_end, total;                  // on the line; the line's length
+    int used, number, from_start, spare;        // workers with a part; this one's number
+};
+
+static_assert(sizeof(WarpState) == kStateBytes, "shared memory of a warp");
+
+// A worker's ring of stages: their places, barriers, headers (the slots that
+// hold tokens) and how often each was issued.
+struct Ring {
+    uint32_t stages, full;
+    uint64_t *hdr;
+    int *issued;
+};
 
 // A worker's stream: its stages in order, a batch of their pieces looked up a
 // lane a piece, and the next batch's table entries on their way.  A batch lies
 // in one segment.
 template <class S>
 struct Feed {
-    Walk walk;
-    Segment seg;
+    Place *at_line;                             // of the next segment to look up
     bool more;
     int tile;                                   // of the segment, the next to look up
     int per_stage, batch, lane_stage, lane_piece;   // pieces of a stage, stages of a batch; the lane's place in one
@@ -496,6 +545,7 @@ struct Feed {
         if (!more)
             return;
         const int P = p.piece;
+        Segment seg = at_line->seg;
         n2 = min(batch, seg.last - tile);
         group2 = seg.group;
         const int f = (tile + lane_stage) * per_stage + lane_piece;
@@ -505,62 +555,97 @@ struct Feed {
         page2 = left2 > 0 && col < p.table_cols ? p.block_table[seg.request * p.bt_s0 + col] : -1;
         tile += n2;
         if (tile >= seg.last) {
-            more = walk.next(p, seg);
+            more = at_line->next(p, 0, seg);
             tile = seg.first;
         }
     }
 
-    __device__ __forceinline__ void start(const Params &p, const Walk &from, int lane)
+    // The feed's place is where the worker's part begins.
+    __device__ __forceinline__ void start(const Params &p, Place *place, int lane)
     {
-        walk = from;
-        per_stage = p.tile / p.piece;
+        at_line = place;
+        per_stage = S::kFull ? 1 : p.tile / p.piece;
         batch = 32 / per_stage;
         lane_stage = lane / per_stage;
         lane_piece = lane - lane_stage * per_stage;
-        more = walk.next(p, seg);
+        Segment seg;
+        more = at_line->next(p, 0, seg);
         tile = seg.first;
         n2 = 0;
         look_up(p);
         look_up(p);
     }
 
-    // Issues the next stage, if there is one, into the place at `ring` with the
-    // barrier `full`, the header `hdr` and the count `issued`.
-    __device__ __forceinline__ void issue(const Params &p, const CUtensorMap *tmap, uint32_t ring, uint32_t full,
-                                          uint64_t *hdr, int *issued, int lane)
+    // Issues the batch's next stage, if there is one, into place `slot` of the
+    // worker's ring.
+    __device__ __forceinline__ void issue(const Params &p, const CUtensorMap *tmap, const Ring &r, int slot, int lane)
     {
-        if (n == 0)
-            return;
+        if (n > 0) {
+            send(p, tmap, r, slot, 1, lane);
+            if (at == n)
+                look_up(p);
+        }
+    }
+
+    // Fills the ring at the start: what the batch has at once, the rest one by one.
+    __device__ __forceinline__ void fill(const Params &p, const CUtensorMap *tmap, const Ring &r, int lane)
+    {
+        int slot = 0;
+        if (n > 0) {
+            slot = min(n, S::kRing);
+            send(p, tmap, r, 0, slot, lane);
+            if (at == n)
+                look_up(p);
+        }
+#pragma unroll 1
+        for (; slot < S::kRing && n > 0; ++slot)
+            issue(p, tmap, r, slot, lane);
+    }
+
+private:
+    // Stages at .. at + count - 1 of the batch into places slot, slot + 1, ...:
+    // a stage's first lane announces its bytes and the tokens that it will hold.
+    __device__ __forceinline__ void send(const Params &p, const CUtensorMap *tmap, const Ring &r, int slot, int count,
+                                         int lane)
+    {
         const uint32_t piece_bytes = static_cast<uint32_t>(p.piece) * S::kRowBytes;
-        const bool mine = lane_stage == at && left > 0;
-        const bool copy = mine && page >= 0 && page < p.pages;
-        if (mine && !copy)
+        const int mine = lane_stage - at;
+        const bool wanted = mine >= 0 && mine < count && left > 0;
+        const bool copy = wanted && page >= 0 && page < p.pages;
+        if (wanted && !copy)
             atomicOr(p.flags, SDA_FLAG_BOUNDS);
-        const unsigned cb = __ballot_sync(~0u, copy);
-        const uint64_t bits = copy ? low_bits(min(p.piece, left)) << (lane_piece * p.piece) : 0ull;
-        const unsigned lo = __reduce_or_sync(~0u, static_cast<unsigned>(bits));
-        const unsigned hi = S::kSlots > 32 ? __reduce_or_sync(~0u, static_cast<unsigned>(bits >> 32)) : 0u;
-        if (lane == 0) {
-            *hdr = (static_cast<uint64_t>(hi) << 32) | lo;
-            *issued += 1;
-            if (cb)
-                mbar_expect_tx(full, __popc(cb) * piece_bytes);
+        const unsigned copies = __ballot_sync(~0u, copy);
+        const int place = slot + mine;
+        const uint32_t full = r.full + 8 * place;
+        const bool leads = mine >= 0 && mine < count && lane_piece == 0;
+        if (leads) {
+            uint64_t bits = 0;
+            const unsigned of_stage = copies >> lane;           // this lane is the stage's first
+            int pieces = 0;
+            for (int k = 0; k < per_stage; ++k)
+                if ((of_stage >> k) & 1u) {
+                    ++pieces;
+                    bits |= low_bits(min(p.piece, left - k * p.piece)) << (k * p.piece);
+                }
+            r.hdr[place] = bits;
+            r.issued[place] += 1;
+            if (pieces > 0)
+                mbar_expect_tx(full, pieces * piece_bytes);
         }
         __syncwarp();
         if (copy)
-            tma_load_5d(ring + lane_piece * piece_bytes, tmap, 0, off, 0, group, page, full);
-        if (lane == 0)
+            tma_load_5d(r.stages + place * S::kStageBytes + lane_piece * piece_bytes, tmap, 0, off, 0, group, page, full);
+        if (leads)
             mbar_arrive(full);
-        if (++at == n)
-            look_up(p);
+        at += count;
     }
 };
 
-template <bool FP8, int D, int MT>
+template <bool FP8, int D, int MT, bool FULL>
 __global__ void __launch_bounds__(kThreads, 2)
     sda_paged_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_constant__ Params p)
 {
-    using S = Shape<FP8, D, MT>;
+    using S = Shape<FP8, D, MT, FULL>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
@@ -572,8 +657,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     uint64_t *hdr = reinterpret_cast<uint64_t *>(smem + S::kHdrOff) + worker * S::kRing;
     int *issued = reinterpret_cast<int *>(smem + S::kIssuedOff) + worker * S::kRing;
     int *timed_out = reinterpret_cast<int *>(smem + S::kCtlOff);
-    long long *scan = reinterpret_cast<long long *>(smem + S::kCtlOff + 16);
-    Part *parts = reinterpret_cast<Part *>(smem + S::kCtlOff + 128);
+    long long *sums = reinterpret_cast<long long *>(smem + S::kCtlOff + 16);
 
     if (threadIdx.x < S::kStages) {
         mbar_init(bars + 8 * threadIdx.x, 1);
@@ -590,19 +674,18 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncthreads();
 
     long long total;
-    int used;
-    const int2 who = find_parts<S::kWorkers>(p, scan, parts, total, used);
-    const int v = who.x + worker * who.y;
-    Walk walk = {parts[worker].left, parts[worker].request, parts[worker].group, parts[worker].tile};
-    const long long part_end = parts[worker].start + walk.left;
-
+    int used, v;
+    const Part part = find_part<S::kWorkers>(p, sums, worker, total, used, v);
+    // What is needed between units only: this warp's place, its feed's, the line.
+    WarpState *state = reinterpret_cast<WarpState *>(smem + S::kStateOff) + warp;
+    state->here.walk = state->ahead.walk = {part.left, part.request, part.group, part.tile};
+    state->part_end = part.start + part.left;
+    state->total = total;
+    state->used = used;
+    state->number = v;
+    __syncwarp();
     Feed<S> feed;
-    if (mt == 0) {
-        feed.start(p, walk, lane);
-#pragma unroll 1
-        for (int s = 0; s < S::kRing; ++s)
-            feed.issue(p, &tmap, sbase + s * S::kStageBytes, full_bar + 8 * s, hdr + s, issued + s, lane);
-    }
+    const Ring place = {sbase, full_bar, hdr, issued};
 
     const int g = lane >> 2, t = lane & 3;      // fragment row and column pair
     const int H = p.heads, R = p.rows;
@@ -614,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
     // Shared-memory offsets of this lane's K rows and V rows in a stage.  A
     // stage holds its pieces one after another, each [band][token][128 bytes].
-    const uint32_t bstride = static_cast<uint32_t>(p.piece) * 128u;
+    const uint32_t bstride = static_cast<uint32_t>(FULL ? S::kSlots : p.piece) * 128u;
     const int mi = lane >> 3;
     const int ksw = slot_of(g), vsw = slot_of(lane & 7);
     constexpr int NT = S::kSlots / 8, KS = S::kSlots / 16, NC = D * S::kElt / 64;
@@ -623,31 +706,38 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
         const int k = 8 * i / p.piece;
-        tile_off[i] = 8 * i < p.tile ? k * bstride * S::kBands + (8 * i - k * p.piece) * 128u : 0u;
+        tile_off[i] = FULL             ? 1024u * i
+                      : 8 * i < p.tile ? k * bstride * S::kBands + (8 * i - k * p.piece) * 128u : 0u;
     }
 
     // A long unit's pieces of neighbouring workers are merged by the CTA where
-    // they are all that its workers have: one piece for the join, not four.
+    // they are all that its workers have: one piece for the join, not four.  The
+    // CTA's part of the line lies in one unit, and its first worker has a tile.
     bool merged = false;
     if (S::kWorkers > 1 && used == p.workers && !p.whole_units) {
-        const long long u0 = parts[0].start;
-        const int tiles = Walk::tiles_of(p, Walk::length(p, parts[0].request));
-        merged = parts[0].left > kUnitCost && parts[S::kWorkers - 1].start == u0 &&
-                 parts[S::kWorkers - 1].left <= tiles + kUnitCost;
+        const int w0 = static_cast<int>(blockIdx.x) * S::kWorkers;
+        const long long x0 = boundary(p, total, w0), first_end = boundary(p, total, w0 + 1);
+        const long long x1 = boundary(p, total, w0 + S::kWorkers);
+        const int tiles = Walk::tiles_of(p, Walk::length(p, part.request));
+        merged = x0 >= part.start && first_end > part.start + kUnitCost && x1 <= part.start + tiles + kUnitCost;
+        state->from_start = x0 <= part.start + kUnitCost;       // the first worker's piece begins the unit
     }
 
     int ring = 0;                               // the worker's next stage: its place and parity
     uint32_t parity = 0;
-    bool dead = false;
+    bool dead = false, started = false;
 
     for (;;) {
-        const long long unit = part_end - walk.left;            // its place on the line
-        Segment seg;
-        if (!walk.next(p, seg))
-            break;
-        const int len = seg.len;
-        const int64_t out_row0 = static_cast<int64_t>(seg.request) * p.query_len * p.groups + seg.group;
-        auto row_of = [&](int r) { return out_row0 + static_cast<int64_t>(r / H) * p.groups; };
+        int common, left;                       // tokens that every row sees, from the segment's first on; its stages
+        const uint16_t *q_rows;                 // the unit's first query row
+        {
+            Segment seg;
+            if (!state->here.next(p, state->part_end, seg))
+                break;
+            common = seg.len - p.query_len + 1 - seg.first * p.tile;
+            left = seg.last - seg.first;
+            q_rows = p.query + (static_cast<int64_t>(seg.request) * p.query_len * p.groups + seg.group) * p.q_s0;
+        }
 
         // ---- Q fragments: thread t of k-step kk holds the four dims that its
         // K words hold.  FP8: the fp16 product takes q scaled by a power of two
@@ -656,24 +746,38 @@ __global__ void __launch_bounds__(kThreads, 2)
         uint32_t qf[S::kSteps][4];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const int r = k ? r1 : r0, rq = r < R ? r : 0;      // rows past R read row 0 and count as zeros
-            const uint32_t keep = r < R ? ~0u : 0u;
-            const uint16_t *q = p.query + row_of(rq) * p.q_s0 + (rq % H) * p.q_s1 + (FP8 ? 16 : 8) * t;
+            const int r = k ? r1 : r0, rq = r < R ? r : 0;      // rows past R read row 0: zeros in the end
+            const uint16_t *q = q_rows + static_cast<int64_t>(rq / H) * p.groups * p.q_s0 + (rq % H) * p.q_s1 +
+                                (FP8 ? 16 : 8) * t;
             auto dim = [](int kk) { return FP8 ? 64 * (kk >> 2) + 4 * (kk & 3) : 32 * (kk >> 1) + 4 * (kk & 1); };
             if (p.q_vec) {
 #pragma unroll
                 for (int kk = 0; kk < S::kSteps; ++kk) {
                     const uint2 w = *reinterpret_cast<const uint2 *>(q + dim(kk));
-                    qf[kk][k] = w.x & keep;
-                    qf[kk][2 + k] = w.y & keep;
+                    qf[kk][k] = w.x;
+                    qf[kk][2 + k] = w.y;
                 }
             } else {
 #pragma unroll
                 for (int kk = 0; kk < S::kSteps; ++kk) {
                     const uint16_t *w = q + dim(kk);
-                    qf[kk][k] = (w[0] | (static_cast<uint32_t>(w[1]) << 16)) & keep;
-                    qf[kk][2 + k] = (w[2] | (static_cast<uint32_t>(w[3]) << 16)) & keep;
+                    qf[kk][k] = w[0] | (static_cast<uint32_t>(w[1]) << 16);
+                    qf[kk][2 + k] = w[2] | (static_cast<uint32_t>(w[3]) << 16);
                 }
+            }
+        }
+        if (!started && mt == 0) {              // behind the first Q, which would wait behind the stages
+            feed.start(p, &state->ahead, lane);
+            feed.fill(p, &tmap, place, lane);
+        }
+        started = true;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {           // not before the loads have had that time
+            const uint32_t keep = (k ? r1 : r0) < R ? ~0u : 0u;
+#pragma unroll
+            for (int kk = 0; kk < S::kSteps; ++kk) {
+                qf[kk][k] &= keep;
+                qf[kk][2 + k] &= keep;
             }
         }
         float sl[2] = {p.scale * kLog2e * ks, p.scale * kLog2e * ks};   // logit scales in log2 units
@@ -714,9 +818,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
         float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.0f, 0.0f};
 
-        // tokens of the stage that every row sees: common, a tile's length less each stage
-        int common = len - p.query_len + 1 - seg.first * p.tile;
-        for (int left = seg.last - seg.first; left > 0; --left, common -= p.tile) {
+        for (; left > 0; --left, common -= FULL ? S::kSlots : p.tile) {
             if (!dead) {
                 const bool ok = mbar_wait(full_bar + 8 * ring, parity, p.wait_ns);
                 if (!__all_sync(~0u, ok)) {
@@ -944,7 +1046,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
                     dead = true;
                 } else {
-                    feed.issue(p, &tmap, sbase + ring * S::kStageBytes, full_bar + 8 * ring, hdr + ring, issued + ring, lane);
+                    feed.issue(p, &tmap, place, ring, lane);
                 }
             }
             if (++ring == S::kRing) {
@@ -954,6 +1056,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
 
         // ---- The unit's result, or its piece's.
+        const volatile Segment &at = state->here.seg;
+        const Segment seg = {at.request, at.group, at.first, at.last, at.tiles, at.len};
+        const int v = static_cast<const volatile WarpState *>(state)->number;
+        const int64_t out_row0 = static_cast<int64_t>(seg.request) * p.query_len * p.groups + seg.group;
+        auto row_of = [&](int r) { return out_row0 + static_cast<int64_t>(r / H) * p.groups; };
         const bool begins = seg.first == 0, ends = seg.last == seg.tiles;
         const bool whole = begins && ends;
         const int64_t piece = static_cast<int64_t>(v) * 2 + (begins ? 1 : 0);
@@ -1008,7 +1115,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
             }
             __syncthreads();
-            const int64_t first = static_cast<int64_t>(who.x) * 2 + (parts[0].tile == 0 ? 1 : 0);
+            const int64_t first = static_cast<int64_t>(v - worker) * 2 + (state->from_start ? 1 : 0);
             for (int e = threadIdx.x; e < R * (D / 4); e += kThreads) {
                 const int r = e / (D / 4), d = 4 * (e - r * (D / 4));
                 const float *src = outs + r * kStride + d;      // row r of worker 0: tile r / 16 is warp r / 16
@@ -1081,8 +1188,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         // ---- The worker that has a cut unit's first tile lists it for the join.
         if (begins && !ends && mt == 0 && lane == 0) {
-            const long long end = unit + kUnitCost + seg.tiles;         // past the unit's last tile
-            const int n = static_cast<int>((end * used - 1) / total) - v + 1;
+            const long long end = state->here.unit + kUnitCost + seg.tiles;     // past the unit's last tile
+            const int n = static_cast<int>((end * state->used - 1) / state->total) - v + 1;
             const int rows = n > kManyPieces ? 1 : kJoinWarps, items = (R + rows - 1) / rows;
             const unsigned at = atomicAdd(p.flags + kItemWord, static_cast<unsigned>(items));
             for (int i = 0; i < items; ++i) {
@@ -1102,12 +1209,13 @@ __global__ void __launch_bounds__(kThreads, 2)
             atomicOr(p.flags, SDA_FLAG_BOUNDS);
         if (len != 0)
             continue;
-        for (int e = threadIdx.x; e < p.groups * R * D; e += kThreads) {
-            const int d = e % D, gr = e / D;    // gr: [token][group][head]
+        for (int gr = warp; gr < p.groups * R; gr += kWarps) {  // [token][group][head]
             const int h = gr % H;
             const int64_t row = static_cast<int64_t>(q) * p.query_len * p.groups + gr / H;
-            p.output[row * p.o_s0 + h * p.o_s1 + d] = 0;
-            if (d == 0 && p.lse)
+            uint16_t *out = p.output + row * p.o_s0 + h * p.o_s1;
+            for (int d = lane; d < D; d += 32)
+                out[d] = 0;
+            if (lane == 0 && p.lse)
                 p.lse[row * p.l_s0 + h * p.l_s1] = -INFINITY;
         }
     }
@@ -1122,35 +1230,37 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
 }
 
-template <bool FP8, int D, int MT>
+template <bool FP8, int D, int MT, bool FULL>
 sda_status launch_shape(const CUtensorMap &tmap, const Params &p, void *stream)
 {
-    using S = Shape<FP8, D, MT>;
+    using S = Shape<FP8, D, MT, FULL>;
     static size_t raised[64] = {};
-    if (!raise_smem(sda_paged_kernel<FP8, D, MT>, S::kBytes, raised))
+    if (!raise_smem(sda_paged_kernel<FP8, D, MT, FULL>, S::kBytes, raised))
         return SDA_ERR_CUDA;
-    return launch_pdl(sda_paged_kernel<FP8, D, MT>, dim3(static_cast<unsigned>(p.ctas)), dim3(kThreads), S::kBytes,
-                      stream, tmap, p);
+    return launch_pdl(sda_paged_kernel<FP8, D, MT, FULL>, dim3(static_cast<unsigned>(p.ctas)), dim3(kThreads),
+                      S::kBytes, stream, tmap, p);
 }
 
-template <int D>
-sda_status launch_dim(bool fp8, const CUtensorMap &tmap, const Params &p, void *stream)
+template <bool FP8, int D, int MT>
+sda_status launch_tiles(const CUtensorMap &tmap, const Params &p, void *stream)
+{
+    return p.piece == Shape<FP8, D, MT, true>::kSlots ? launch_shape<FP8, D, MT, true>(tmap, p, stream)
+                                                      : launch_shape<FP8, D, MT, false>(tmap, p, stream);
+}
+
+template <bool FP8, int D>
+sda_status launch_dim(const CUtensorMap &tmap, const Params &p, void *stream)
 {
     const int tiles = tiles_of_rows(p.rows);
-    if (fp8)
-        return tiles == 1   ? launch_shape<true, D, 1>(tmap, p, stream)
-               : tiles == 2 ? launch_shape<true, D, 2>(tmap, p, stream)
-                            : launch_shape<true, D, 4>(tmap, p, stream);
-    return tiles == 1   ? launch_shape<false, D, 1>(tmap, p, stream)
-           : tiles == 2 ? launch_shape<false, D, 2>(tmap, p, stream)
-                        : launch_shape<false, D, 4>(tmap, p, stream);
+    return tiles == 1   ? launch_tiles<FP8, D, 1>(tmap, p, stream)
+           : tiles == 2 ? launch_tiles<FP8, D, 2>(tmap, p, stream)
+                        : launch_tiles<FP8, D, 4>(tmap, p, stream);
 }
 
-// One translation unit per head size.
-sda_status launch_64(bool fp8, const CUtensorMap &tmap, const Params &p, void *stream);
-sda_status launch_128(bool fp8, const CUtensorMap &tmap, const Params &p, void *stream);
-sda_status launch_192(bool fp8, const CUtensorMap &tmap, const Params &p, void *stream);
-sda_status launch_256(bool fp8, const CUtensorMap &tmap, const Params &p, void *stream);
+// One translation unit per head size and cache type.
+using Launch = sda_status(const CUtensorMap &tmap, const Params &p, void *stream);
+Launch launch_bf16_64, launch_bf16_128, launch_bf16_192, launch_bf16_256;
+Launch launch_fp8_64, launch_fp8_128, launch_fp8_192, launch_fp8_256;
 
 }  // namespace paged
 }  // namespace sda
