@@ -114,7 +114,7 @@ __device__ __forceinline__ uint32_t quotient(uint32_t x, unsigned long long inve
     return inverse ? static_cast<uint32_t>(__umul64hi(x, inverse)) : x;
 }
 
-constexpr int kStateBytes = 144;                // WarpState
+constexpr int kStateBytes = 136;                // WarpState
 
 // FULL: a piece fills a stage (pages of at least a stage's tokens, in whole
 // stages), so the offsets in a stage are constants.
@@ -508,7 +508,7 @@ struct Place {
 struct WarpState {
     Place here, ahead;                          // of the warp's products and of its feed
     long long part_end, total;                  // on the line; the line's length
-    int used, number, from_start, spare;        // workers with a part; this one's number
+    int used, number;                           // workers with a part; this one's number
 };
 
 static_assert(sizeof(WarpState) == kStateBytes, "shared memory of a warp");
@@ -572,8 +572,7 @@ struct Feed {
         more = at_line->next(p, 0, seg);
         tile = seg.first;
         n2 = 0;
-        look_up(p);
-        look_up(p);
+        look_up(p);                             // the first batch's table entries are on their way
     }
 
     // Issues the batch's next stage, if there is one, into place `slot` of the
@@ -590,6 +589,7 @@ struct Feed {
     // Fills the ring at the start: what the batch has at once, the rest one by one.
     __device__ __forceinline__ void fill(const Params &p, const CUtensorMap *tmap, const Ring &r, int lane)
     {
+        look_up(p);
         int slot = 0;
         if (n > 0) {
             slot = min(n, S::kRing);
@@ -686,6 +686,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncwarp();
     Feed<S> feed;
     const Ring place = {sbase, full_bar, hdr, issued};
+    if (mt == 0)
+        feed.start(p, &state->ahead, lane);
 
     const int g = lane >> 2, t = lane & 3;      // fragment row and column pair
     const int H = p.heads, R = p.rows;
@@ -708,19 +710,6 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int k = 8 * i / p.piece;
         tile_off[i] = FULL             ? 1024u * i
                       : 8 * i < p.tile ? k * bstride * S::kBands + (8 * i - k * p.piece) * 128u : 0u;
-    }
-
-    // A long unit's pieces of neighbouring workers are merged by the CTA where
-    // they are all that its workers have: one piece for the join, not four.  The
-    // CTA's part of the line lies in one unit, and its first worker has a tile.
-    bool merged = false;
-    if (S::kWorkers > 1 && used == p.workers && !p.whole_units) {
-        const int w0 = static_cast<int>(blockIdx.x) * S::kWorkers;
-        const long long x0 = boundary(p, total, w0), first_end = boundary(p, total, w0 + 1);
-        const long long x1 = boundary(p, total, w0 + S::kWorkers);
-        const int tiles = Walk::tiles_of(p, Walk::length(p, part.request));
-        merged = x0 >= part.start && first_end > part.start + kUnitCost && x1 <= part.start + tiles + kUnitCost;
-        state->from_start = x0 <= part.start + kUnitCost;       // the first worker's piece begins the unit
     }
 
     int ring = 0;                               // the worker's next stage: its place and parity
@@ -766,11 +755,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
             }
         }
-        if (!started && mt == 0) {              // behind the first Q, which would wait behind the stages
-            feed.start(p, &state->ahead, lane);
-            feed.fill(p, &tmap, place, lane);
+        if (!started) {
+            started = true;
+            if (mt == 0)                        // behind the first Q, which would wait behind the stages
+                feed.fill(p, &tmap, place, lane);
         }
-        started = true;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {           // not before the loads have had that time
             const uint32_t keep = (k ? r1 : r0) < R ? ~0u : 0u;
@@ -1069,6 +1058,19 @@ __global__ void __launch_bounds__(kThreads, 2)
             l_run[k] += __shfl_xor_sync(~0u, l_run[k], 1);
             l_run[k] += __shfl_xor_sync(~0u, l_run[k], 2);
         }
+        // A long unit's pieces of neighbouring workers are merged by the CTA where
+        // they are all that its workers have: one piece for the join, not four.
+        // The CTA's part of the line lies in the unit, and its first worker has a
+        // tile (so every worker comes here once, with this segment).
+        bool merged = false, from_start = false;
+        if (S::kWorkers > 1 && !whole && state->used == p.workers) {
+            const long long n = state->total, u0 = state->here.unit;
+            const int w0 = static_cast<int>(blockIdx.x) * S::kWorkers;
+            const long long x0 = boundary(p, n, w0);
+            merged = x0 >= u0 && boundary(p, n, w0 + 1) > u0 + kUnitCost &&
+                     boundary(p, n, w0 + S::kWorkers) <= u0 + seg.tiles + kUnitCost;
+            from_start = x0 <= u0 + kUnitCost;                  // the first worker's piece begins the unit
+        }
         if (merged) {
             // The workers' stages are used up, so the ring can hold their outputs.
             constexpr int kStride = D + 4;
@@ -1115,7 +1117,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
             }
             __syncthreads();
-            const int64_t first = static_cast<int64_t>(v - worker) * 2 + (state->from_start ? 1 : 0);
+            const int64_t first = static_cast<int64_t>(v - worker) * 2 + (from_start ? 1 : 0);
             for (int e = threadIdx.x; e < R * (D / 4); e += kThreads) {
                 const int r = e / (D / 4), d = 4 * (e - r * (D / 4));
                 const float *src = outs + r * kStride + d;      // row r of worker 0: tile r / 16 is warp r / 16
