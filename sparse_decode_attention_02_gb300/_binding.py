@@ -329,28 +329,33 @@ def sparse_decode_summary_scores(query, weights, summaries, block_table, seq_len
     return scores
 
 
-_NOTHING = contextlib.nullcontext()
+_INT4 = ctypes.c_int32 * 4
+_NO_SCALE = (None, None)
 _step_workspaces: dict = {}
 
 
-def _new_step_workspace(index: int, handle: int, nbytes: int, stream) -> torch.Tensor:
+def _new_step_workspace(index: int, handle: int, nbytes: int, stream):
     """The serving-step entries' default workspace, zeroed on the call's stream: kept per
     (device, stream) and grown on demand like `default_workspace`'s, but a capture gets one
-    of its own, zeroed in the graph, that no other graph or eager call shares."""
+    of its own, zeroed in the graph, that no other graph or eager call shares.  Returns
+    (tensor, address, bytes)."""
     dev = torch.device("cuda", index)
     with torch.cuda.stream(stream) if stream is not None else _current(dev):
-        if torch.cuda.is_current_stream_capturing():
-            return torch.zeros(nbytes, dtype=torch.uint8, device=dev)
-        ws = _step_workspaces.get((index, handle))
-        if ws is None or ws.numel() < nbytes:
-            ws = _step_workspaces[index, handle] = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
-        return ws
+        capturing = torch.cuda.is_current_stream_capturing()
+        have = _step_workspaces.get((index, handle))
+        if have is not None and have[2] >= nbytes and not capturing:
+            return have
+        ws = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+        have = ws, ws.data_ptr(), nbytes
+        if not capturing:
+            _step_workspaces[index, handle] = have
+        return have
 
 
 def _scale_address(x, index: int, stream):
     """(address, what keeps it) of an FP8 scale: None, a device tensor, or a number to upload."""
     if x is None:
-        return None, None
+        return _NO_SCALE
     if not isinstance(x, torch.Tensor):
         dev = torch.device("cuda", index)
         with torch.cuda.stream(stream) if stream is not None else _current(dev):
@@ -376,19 +381,23 @@ def _call(fn, tensors, arguments, need: int, workspace, stream, scales=()):
     """What the serving-step entries share: fn(*arguments(descriptor addresses, scale
     addresses), workspace, its bytes, stream) on the tensors' device.  Where no workspace
     is given it is the stream's default one of at least `need` bytes."""
-    keep, where, index, current, handle = (_marshal or load_marshal()).pack(*tensors)
+    keep, where, index, current, handle, capturing = (_marshal or load_marshal()).pack(*tensors)
     if index < 0 or stream is not None or (workspace is not None and workspace.get_device() != index):
         _device_of(*tensors, workspace, stream=stream)          # raises where they are apart
         if stream is not None:
             handle = stream.cuda_stream
     if workspace is None:
-        workspace = _step_workspaces.get((index, handle))
-        if workspace is None or workspace.numel() < need or torch.cuda.is_current_stream_capturing():
-            workspace = _new_step_workspace(index, handle, need, stream)
+        have = _step_workspaces.get((index, handle))
+        if have is None or have[2] < need or capturing or stream is not None:
+            have = _new_step_workspace(index, handle, need, stream)
+    else:
+        have = workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
     pointers = [_scale_address(x, index, stream) for x in scales]
-    with _NOTHING if current else torch.cuda.device(index):
-        rc = fn(*arguments(where, [x[0] for x in pointers]), workspace.data_ptr(),
-                workspace.numel() * workspace.element_size(), handle)
+    if current:
+        rc = fn(*arguments(where, pointers), have[1], have[2], handle)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*arguments(where, pointers), have[1], have[2], handle)
     if rc != SDA_OK:
         raise SdaError(rc, load().sparse_decode_status_string(rc).decode())
 
@@ -406,11 +415,13 @@ def sparse_decode_plan_step(context_lens, new_lens, free_pages, free_state, bloc
     None.  For a step in place pass `seq_lens=context_lens` and
     `free_next=free_state`.  Returns (seq_lens, token_starts, slots, positions,
     requests, free_next)."""
-    lib = load()
-    new = lambda t, n: torch.empty(n, dtype=torch.int32, device=slots.device) if t is None else t
-    positions, requests = new(positions, slots.shape[0]), new(requests, slots.shape[0])
-    seq_lens, token_starts = new(seq_lens, context_lens.shape[0]), new(token_starts, context_lens.shape[0] + 1)
-    free_next = new(free_next, 2)
+    lib = _lib or load()
+    if positions is None or requests is None or seq_lens is None or token_starts is None or free_next is None:
+        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+            new = lambda t, n: torch.empty(n, dtype=torch.int32, device=slots.device) if t is None else t
+            positions, requests = new(positions, slots.shape[0]), new(requests, slots.shape[0])
+            seq_lens, token_starts = new(seq_lens, context_lens.shape[0]), new(token_starts, context_lens.shape[0] + 1)
+            free_next = new(free_next, 2)
     _call(lib.sparse_decode_plan_step, (context_lens, new_lens, free_pages, free_state, free_next, block_table, seq_lens,
                                         token_starts, slots, positions, requests),
           lambda d, _: (d[0], d[1], int(block_size), *d[2:]), 256, workspace, stream)
@@ -430,20 +441,24 @@ def sparse_decode_rope_append(query, key, value, positions, inv_freq, slots, cac
     `query_out` is allocated if None and may be `query`.  `sections`: frequency
     pairs of each axis.  `k_scale` / `v_scale`: as in sparse_decode_attention.
     Returns `query_out`."""
-    lib = load()
+    lib = _lib or load()
     if query is not None and query_out is None:
         query_out = torch.zeros_like(query) if slots is not None else torch.empty_like(query)
     if key is None:
         cache = None
     parts = None
     if sections is not None:
-        if positions is None or len(sections) != positions.shape[0]:
+        if positions is None or len(sections) != positions.shape[0] or len(sections) > 4:
             raise ValueError("sparse_decode: a section for each axis of positions")
-        parts = (ctypes.c_int32 * len(sections))(*sections)
+        parts = _INT4(*sections)                # as many as there are axes are read
     _call(lib.sparse_decode_rope_append, (query, query_out, key, value, positions, inv_freq, slots, cache),
-          lambda d, s: (*d[:6], parts, bool(interleaved_axes), bool(adjacent_pairs), float(amplitude), *d[6:], *s), 256,
+          lambda d, s: (*d[:6], parts, bool(interleaved_axes), bool(adjacent_pairs), float(amplitude), *d[6:], s[0][0],
+                        s[1][0]), 256,
           workspace, stream, (k_scale, v_scale))
     return query_out
+
+
+_paged_bytes: dict = {}                        # by (heads, query_len, head_dim)
 
 
 def paged_workspace_bytes(heads: int, query_len: int = 1, head_dim: int = 192) -> int:
@@ -457,10 +472,13 @@ def sparse_decode_paged_attention(query, cache, block_table, seq_lens, output, *
     """Attention of each request's newest `query_len` tokens over its whole paged
     cache into `output`, and the rows' log-sum-exps into `lse` if given; see
     include/sdattn.h for the contract."""
-    lib = load()
-    need = lib.sparse_decode_paged_workspace_bytes(query.shape[1], int(query_len), query.shape[-1]) or 256
+    lib = _lib or load()
+    shape = query.shape[1], int(query_len), query.shape[-1]
+    need = _paged_bytes.get(shape)
+    if need is None:
+        need = _paged_bytes[shape] = lib.sparse_decode_paged_workspace_bytes(*shape) or 256
     _call(lib.sparse_decode_paged_attention, (query, cache, block_table, seq_lens, output, lse, gate),
-          lambda d, s: (*d[:6], float(scale), int(query_len), *s, d[6]), need, workspace, stream, (k_scale, v_scale))
+          lambda d, s: (*d[:6], float(scale), int(query_len), s[0][0], s[1][0], d[6]), need, workspace, stream, (k_scale, v_scale))
 
 
 def read_errors(workspace: torch.Tensor, clear: bool = False,

@@ -77,7 +77,7 @@ def build_marshal(force: bool = False, out: str = MARSHAL) -> str:
            "-I", os.path.join(ROOT, "include"), "-I", sysconfig.get_paths()["include"],
            *(a for d in (os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
                          os.path.join(cuda, "include")) for a in ("-isystem", d)),
-           "-L", lib, f"-Wl,-rpath,{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+           "-L", lib, f"-Wl,-rpath,{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]   # libcudart: c10_cuda's
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode:
         sys.stderr.write(r.stdout + r.stderr)

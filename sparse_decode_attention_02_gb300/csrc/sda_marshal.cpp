@@ -54,7 +54,8 @@ bool describe(const at::Tensor &t, sda_tensor &d)
     return true;
 }
 
-// pack(*tensors or None) -> (memory, addresses, device, on_current_device, stream)
+// pack(*tensors or None) -> (memory, addresses, device, on_current_device, stream,
+// capturing: whether the stream is being captured)
 // The descriptors lie in `memory`, which the caller keeps until its call has
 // returned; None has address None.  device < 0: no CUDA device in common.
 PyObject *pack(PyObject *, PyObject *const *args, Py_ssize_t n)
@@ -66,7 +67,7 @@ PyObject *pack(PyObject *, PyObject *const *args, Py_ssize_t n)
         return nullptr;
     }
     sda_tensor *out = reinterpret_cast<sda_tensor *>(PyBytes_AS_STRING(memory));
-    long device = kNoTensor, current = 0;
+    long device = kNoTensor, current = 0, capturing = 0;
     unsigned long long stream = 0;
     try {
         for (Py_ssize_t i = 0; i < n; ++i) {
@@ -90,8 +91,10 @@ PyObject *pack(PyObject *, PyObject *const *args, Py_ssize_t n)
             PyTuple_SET_ITEM(where, i, slot);
         }
         if (device >= 0) {
-            stream = reinterpret_cast<unsigned long long>(
-                c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream());
+            const cudaStream_t s = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream();
+            stream = reinterpret_cast<unsigned long long>(s);
+            cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+            capturing = cudaStreamIsCapturing(s, &status) != cudaSuccess || status != cudaStreamCaptureStatusNone;
             current = c10::cuda::current_device() == device;
         }
     } catch (const std::exception &e) {
@@ -101,7 +104,7 @@ PyObject *pack(PyObject *, PyObject *const *args, Py_ssize_t n)
         Py_DECREF(memory);
         return nullptr;
     }
-    return Py_BuildValue("(NNllK)", memory, where, device, current, stream);
+    return Py_BuildValue("(NNllKl)", memory, where, device, current, stream, capturing);
 }
 
 // scalar(tensor, device) -> address of a one-element float32 tensor on that device.
