@@ -273,6 +273,11 @@ sda_status sparse_decode_summary_scores(const sda_tensor *query, const sda_tenso
  *                 -1 releases it: its ceil(context / B) pages go back and its
  *                 length becomes 0 (its table entries stay as they were).
  *   block_size    B, tokens per page.
+ *   rows_per_request  0: the token rows are packed, request after request.  k >
+ *                 0: T == Q * k, request q has rows q k .. q k + k - 1 and its
+ *                 tokens are the last of them, as sparse_decode_paged_attention
+ *                 with query_len = k reads them; more than k tokens are outside
+ *                 the contract.
  *   free_pages    [F] int32, a ring of free page ids (read and written).
  *   free_state    [2] int32: the ring's first free entry and how many are free.
  *   free_next     [2] int32 (written): the same after the step; may be
@@ -281,12 +286,13 @@ sda_status sparse_decode_summary_scores(const sda_tensor *query, const sda_tenso
  *                 and written): the columns of the pages taken are written.
  *   seq_lens      [Q] int32 (written): lengths after the step; may be
  *                 context_lens itself (same stride).
- *   token_starts  [Q + 1] int32 (written): the first token row of each request,
- *                 and the number of token rows used.
+ *   token_starts  [Q + 1] int32 (written): the row of each request's first
+ *                 token (where it would be, if there is none), and the row
+ *                 after the last.
  *   slots         [T] int64 (written): page * B + offset of each token row.
  *   positions     [T] int32 (written): the token's position in its request.
  *   requests      [T] int32 (written): the token's request.
- *                 Rows past the last token get -1 in all three.
+ *                 Rows without a token get -1 in all three.
  *   workspace     >= 256 bytes, 256-byte aligned, zeroed once before first use;
  *                 receives the flags below.  Calls that overlap on the GPU
  *                 must not share one.
@@ -306,7 +312,7 @@ sda_status sparse_decode_summary_scores(const sda_tensor *query, const sda_tenso
  * SDA_ERR_CUDA if the launch failed.
  */
 sda_status sparse_decode_plan_step(const sda_tensor *context_lens, const sda_tensor *new_lens,
-                                   int block_size, const sda_tensor *free_pages,
+                                   int block_size, int rows_per_request, const sda_tensor *free_pages,
                                    const sda_tensor *free_state, const sda_tensor *free_next,
                                    const sda_tensor *block_table, const sda_tensor *seq_lens,
                                    const sda_tensor *token_starts, const sda_tensor *slots,

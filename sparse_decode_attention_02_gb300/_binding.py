@@ -76,7 +76,7 @@ def _declare(lib):
                                                  ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
     lib.sparse_decode_summary_scores.restype = ctypes.c_int
     V, I, F, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
-    lib.sparse_decode_plan_step.argtypes = [V, V, I] + 9 * [V] + [V, Z, V]
+    lib.sparse_decode_plan_step.argtypes = [V, V, I, I] + 9 * [V] + [V, Z, V]
     lib.sparse_decode_plan_step.restype = I
     lib.sparse_decode_rope_append.argtypes = 7 * [V] + [I, I, F] + 5 * [V] + [Z, V]
     lib.sparse_decode_rope_append.restype = I
@@ -403,16 +403,16 @@ def _call(fn, tensors, arguments, need: int, workspace, stream, scales=()):
 
 
 def sparse_decode_plan_step(context_lens, new_lens, free_pages, free_state, block_table, *, block_size: int,
-                            slots, positions=None, requests=None, seq_lens=None, token_starts=None,
-                            free_next=None, workspace: torch.Tensor | None = None,
+                            slots, rows_per_request: int = 0, positions=None, requests=None, seq_lens=None,
+                            token_starts=None, free_next=None, workspace: torch.Tensor | None = None,
                             stream: torch.cuda.Stream | None = None):
     """The tables of a step from request lengths, on the GPU: pages from the free
     ring into `block_table`, and a slot, position and request for each row of
     `slots`; see include/sdattn.h for the contract.
 
     `new_lens[q]` tokens are added to request q (-1 releases it).  `slots` ([T]
-    int64) sets how many token rows there are; the other outputs are allocated if
-    None.  For a step in place pass `seq_lens=context_lens` and
+    int64) sets how many token rows there are, packed or (`rows_per_request`) so many
+    for each request; the other outputs are allocated if None.  For a step in place pass `seq_lens=context_lens` and
     `free_next=free_state`.  Returns (seq_lens, token_starts, slots, positions,
     requests, free_next)."""
     lib = _lib or load()
@@ -424,7 +424,7 @@ def sparse_decode_plan_step(context_lens, new_lens, free_pages, free_state, bloc
             free_next = new(free_next, 2)
     _call(lib.sparse_decode_plan_step, (context_lens, new_lens, free_pages, free_state, free_next, block_table, seq_lens,
                                         token_starts, slots, positions, requests),
-          lambda d, _: (d[0], d[1], int(block_size), *d[2:]), 256, workspace, stream)
+          lambda d, _: (d[0], d[1], int(block_size), int(rows_per_request), *d[2:]), 256, workspace, stream)
     return seq_lens, token_starts, slots, positions, requests, free_next
 
 

@@ -43,6 +43,7 @@ struct PlanParams {
     int32_t *positions, *owners;
     unsigned int *header;
     int requests, width, block, ring_size, rows;
+    int per_request;                            // 0: rows packed; else rows of each request
     unsigned long long inverse;                 // floor(2^64 / block) + 1 (0 for block 1)
     int vec;                                    // the row outputs take 16-byte stores
 };
@@ -168,7 +169,7 @@ __global__ void __launch_bounds__(kThreads) sda_plan_kernel(const __grid_constan
         }
         const uint32_t after = static_cast<uint32_t>(c) + static_cast<uint32_t>(n);
         const uint32_t end = after <= kMostSum ? held(static_cast<int>(after)) : kMostSum;
-        if (after > kMostSum || end > static_cast<uint32_t>(p.width))
+        if (after > kMostSum || end > static_cast<uint32_t>(p.width) || (p.per_request > 0 && n > p.per_request))
             return false;
         s.need = end - have;
         s.add = n;
@@ -261,10 +262,10 @@ __global__ void __launch_bounds__(kThreads) sda_plan_kernel(const __grid_constan
     if (gridDim.x == 1 || is_last) {
         for (int q = threadIdx.x; q < Q; q += kThreads) {
             p.seq_lens[q * p.seq_s] = len[q];
-            p.starts[q] = min(tok[q], rows);
+            p.starts[q] = p.per_request > 0 ? (q + 1) * p.per_request - max(len[q] - ctx[q], 0) : min(tok[q], rows);
         }
         if (threadIdx.x == 0) {
-            p.starts[Q] = rows;
+            p.starts[Q] = p.per_request > 0 ? p.rows : rows;
             if (ring_ok) {
                 p.next[0] = static_cast<int>((static_cast<long long>(start) + taken) % p.ring_size);
                 p.next[1] = count - taken + returned;
@@ -279,13 +280,13 @@ __global__ void __launch_bounds__(kThreads) sda_plan_kernel(const __grid_constan
     // index into the ring: i < 2 * ring_size
     auto ring_at = [&](uint32_t i) { return i >= static_cast<uint32_t>(p.ring_size) ? i - p.ring_size : i; };
 
-    // ---- Token rows.
+    // ---- Token rows, packed.
     const int lane = threadIdx.x & 31;
     const int warps = gridDim.x * kWarps, warp = blockIdx.x * kWarps + (threadIdx.x >> 5);
     // a warp's turns are neighbours: its requests follow one another
     const int turns = ((p.rows + kWarpRows - 1) / kWarpRows + warps - 1) / warps;
     int qa = 0, qb = -1;                        // requests of the turn's first and last token row
-    for (int turn = 0; turn < turns; ++turn) {
+    for (int turn = 0; turn < turns && p.per_request == 0; ++turn) {
         const long long w = (static_cast<long long>(warp) * turns + turn) * kWarpRows;
         if (w >= p.rows)
             break;
@@ -364,14 +365,36 @@ __global__ void __launch_bounds__(kThreads) sda_plan_kernel(const __grid_constan
         }
     }
 
-    const int first = blockIdx.x * kThreads + threadIdx.x, step = gridDim.x * kThreads;
+    // ---- Token rows, so many for each request: its tokens are the last of them.
+    const int step = gridDim.x * kThreads, me = blockIdx.x * kThreads + threadIdx.x;
+    for (int r = me; r < p.rows && p.per_request > 0; r += step) {
+        const int q = r / p.per_request, c = ctx[q];
+        const int at = len[q] - ((q + 1) * p.per_request - r);  // the row's position
+        const bool token = at >= c && len[q] > c;
+        long long slot = -1;
+        if (token) {
+            const int col = static_cast<int>(pages_before(p, static_cast<uint32_t>(at))), off = at - col * B;
+            const int page = at - off < c ? p.table[q * p.table_s0 + col]
+                                          : p.ring[ring_at(static_cast<uint32_t>(start + adj[q] + col))];
+            if (page >= 0)
+                slot = static_cast<long long>(page) * B + off;
+            else
+                atomicOr(p.header, SDA_FLAG_BOUNDS);
+        }
+        p.slots[r] = slot;
+        p.positions[r] = token ? at : -1;
+        p.owners[r] = token ? q : -1;
+    }
+
+    // In a decode step the first warps write the rows: the last ones begin with the
+    // pages taken, those in the middle with the pages returned.
     // ---- Pages taken: their table columns.
-    for (int i = first; i < taken; i += step) {
+    for (int i = step - 1 - me; i < taken; i += step) {
         const int q = last_at_most(pag, 0, Q - 1, i);
         p.table[q * p.table_s0 + (i - adj[q])] = p.ring[ring_at(static_cast<uint32_t>(start + i))];
     }
     // ---- Pages returned: behind the ring's last free page.
-    for (int i = first; i < returned; i += step) {
+    for (int i = me < step / 2 ? me + step / 2 : me - step / 2; i < returned; i += step) {
         const int q = last_at_most(rel, 0, Q - 1, i);
         const uint32_t at = static_cast<uint32_t>(start) + count + i;         // < 2 * ring_size: they fit
         p.ring[ring_at(at)] = p.table[q * p.table_s0 + (i - rel[q])];
@@ -381,7 +404,8 @@ __global__ void __launch_bounds__(kThreads) sda_plan_kernel(const __grid_constan
 }  // namespace
 
 extern "C" sda_status sparse_decode_plan_step(const sda_tensor *context_lens, const sda_tensor *new_lens,
-                                              int block_size, const sda_tensor *free_pages,
+                                              int block_size, int rows_per_request,
+                                              const sda_tensor *free_pages,
                                               const sda_tensor *free_state, const sda_tensor *free_next,
                                               const sda_tensor *block_table, const sda_tensor *seq_lens,
                                               const sda_tensor *token_starts, const sda_tensor *slots,
@@ -399,7 +423,8 @@ extern "C" sda_status sparse_decode_plan_step(const sda_tensor *context_lens, co
     const int64_t Q = context_lens->shape[0], rows = slots->shape[0], ring = free_pages->shape[0];
     if (new_lens->shape[0] != Q || block_table->shape[0] != Q || seq_lens->shape[0] != Q ||
         token_starts->shape[0] != Q + 1 || positions->shape[0] != rows || requests->shape[0] != rows ||
-        free_state->shape[0] != 2 || free_next->shape[0] != 2 || ring < 1 || block_size < 1)
+        free_state->shape[0] != 2 || free_next->shape[0] != 2 || ring < 1 || block_size < 1 || rows_per_request < 0 ||
+        (rows_per_request > 0 && rows != Q * rows_per_request))
         return SDA_ERR_INVALID;
     const sda_tensor *dense[] = {free_pages, free_state, free_next, token_starts, slots, positions, requests};
     for (const sda_tensor *t : dense)
@@ -444,6 +469,7 @@ extern "C" sda_status sparse_decode_plan_step(const sda_tensor *context_lens, co
     p.block = block_size;
     p.ring_size = static_cast<int>(ring);
     p.rows = static_cast<int>(rows);
+    p.per_request = rows_per_request;
     p.inverse = block_size > 1 ? ~0ull / static_cast<unsigned>(block_size) + 1 : 0;
     p.vec = aligned(p.slots, 16) && aligned(p.positions, 16) && aligned(p.owners, 16);
 

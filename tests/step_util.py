@@ -10,7 +10,7 @@ import torch
 E4M3_MAX = 448.0
 
 
-def plan(context, new, block, ring, state, table, rows):
+def plan(context, new, block, ring, state, table, rows, per_request=0):
     """The contract of sparse_decode_plan_step, one request after another.  Returns (seq_lens,
     token_starts, slots, positions, requests, free_next, ring, table, flags)."""
     context, new, ring = [int(x) for x in context], [int(x) for x in new], [int(x) for x in ring]
@@ -47,7 +47,7 @@ def plan(context, new, block, ring, state, table, rows):
                 flags |= 1
             continue
         need = -(-(c + n) // block) - have
-        if have + need > W or c + n > 2 ** 31 - 1:
+        if have + need > W or c + n > 2 ** 31 - 1 or 0 < per_request < n:
             flags |= 1
             continue
         asked += need
@@ -70,6 +70,14 @@ def plan(context, new, block, ring, state, table, rows):
             owners.append(q)
         lens[q] = c + n
     starts.append(len(slots))
+    if per_request:                       # spread out: a request's tokens are the last of its rows
+        flat = list(zip(slots, positions, owners))
+        starts = [(q + 1) * per_request - owners.count(q) for q in range(len(context))] + [rows]
+        out = [(-1, -1, -1)] * rows
+        for q in range(len(context)):
+            mine = [x for x in flat if x[2] == q]
+            out[starts[q]:(q + 1) * per_request] = mine
+        slots, positions, owners = (list(x) for x in zip(*out)) if rows else ([], [], [])
     free_next = [(start + taken) % F, count - taken + returned] if usable else [int(x) for x in state]
     pad = [-1] * (rows - len(slots))
     return dict(seq_lens=lens, token_starts=starts, slots=slots + pad, positions=positions + pad,

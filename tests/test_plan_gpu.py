@@ -16,7 +16,8 @@ def i32(x):
     return torch.tensor(x, dtype=torch.int32, device="cuda")
 
 
-def run(context, new, block, ring, state, table, rows, *, in_place=False, offset=0, workspace=None, stream=None):
+def run(context, new, block, ring, state, table, rows, *, in_place=False, offset=0, workspace=None, stream=None,
+        per_request=0):
     ctx, ring_t, st, tab = i32(context), i32(ring), i32(state), i32(np.asarray(table).tolist()).view(np.shape(table))
     raw = torch.full((rows + offset,), -7, dtype=torch.int64, device="cuda")
     pos, own = i32([-7] * (rows + offset)), i32([-7] * (rows + offset))
@@ -24,7 +25,7 @@ def run(context, new, block, ring, state, table, rows, *, in_place=False, offset
     kw = dict(seq_lens=ctx, free_next=st) if in_place else {}
     lens, starts, slots, positions, owners, nxt = sda.sparse_decode_plan_step(
         ctx, i32(new), ring_t, st, tab, block_size=block, slots=raw[offset:], positions=pos[offset:],
-        requests=own[offset:], workspace=ws, stream=stream, **kw)
+        requests=own[offset:], workspace=ws, stream=stream, rows_per_request=per_request, **kw)
     torch.cuda.synchronize()
     got = dict(seq_lens=lens, token_starts=starts, slots=slots, positions=positions, requests=owners, free_next=nxt,
                free_pages=ring_t, table=tab)
@@ -33,7 +34,7 @@ def run(context, new, block, ring, state, table, rows, *, in_place=False, offset
 
 def check(context, new, block, ring, state, table, rows, **kw):
     got, flags = run(context, new, block, ring, state, table, rows, **kw)
-    want, want_flags = step_util.plan(context, new, block, ring, state, table, rows)
+    want, want_flags = step_util.plan(context, new, block, ring, state, table, rows, kw.get("per_request", 0))
     for k, v in want.items():
         assert np.array_equal(got[k].astype(np.int64).reshape(-1), np.asarray(v, dtype=np.int64).reshape(-1)), k
     assert flags == want_flags
@@ -96,6 +97,15 @@ def test_drawn(seed):
     check(*problem(r, r.randint(1, 700), r.choice([1, 8, 16, 48, 64]), r.choice([0, 30, 3000]), low,
                    r.choice([1, 7, 200]), room=r.choice([0.5, 1.0]), row_room=r.choice([0.5, 1.0]),
                    spare=r.choice([0, 5])), in_place=bool(seed & 1), offset=seed % 3)
+
+
+@pytest.mark.parametrize("requests,k,low", [(1, 1, 1), (9, 1, 0), (64, 2, 0), (700, 4, 1), (3000, 3, 0), (8192, 1, 1)])
+def test_so_many_rows_for_each_request(requests, k, low):
+    r = random.Random(requests + k)
+    ctx, new, block, ring, state, table, rows = problem(r, requests, 16, 200, low, k, room=0.9)
+    check(ctx, new, block, ring, state, table, requests * k, per_request=k)
+    new[0] = k + 1                                                            # more tokens than rows: left out
+    check(ctx, new, block, ring, state, table, requests * k, per_request=k, in_place=True)
 
 
 def test_rows_past_the_last_token_and_the_smallest_outputs():
