@@ -218,6 +218,12 @@ constexpr int kMinTiles = 2;
 // Units of at most this many tiles (by the table's width) are never cut.
 constexpr int kWholeTiles = 8;
 
+// CTAs of a launch, at most.
+int ctas_of(int64_t dim, int64_t rows)
+{
+    return kSms * ctas_per_sm(static_cast<int>(dim), tiles_of_rows(static_cast<int>(rows)));
+}
+
 // Workers of a CTA.
 int workers_of(int64_t rows)
 {
@@ -231,7 +237,8 @@ extern "C" size_t sparse_decode_paged_workspace_bytes(int heads, int query_len, 
     if (heads < 1 || query_len < 1 || heads > kMaxRows || query_len > kMaxRows || heads * query_len > kMaxRows ||
         !dim_ok(head_dim))
         return 0;
-    const size_t rows = static_cast<size_t>(kMaxCtas) * workers_of(heads * query_len) * 2 * heads * query_len;
+    const size_t rows = static_cast<size_t>(ctas_of(head_dim, heads * query_len)) * workers_of(heads * query_len) * 2 *
+                        heads * query_len;
     return kHeaderBytes + align256(kItemBytes) + rows * head_dim * sizeof(float) + align256(rows * sizeof(float));
 }
 
@@ -352,7 +359,7 @@ extern "C" sda_status sparse_decode_paged_attention(const sda_tensor *query, con
     p.v_scale = fp8 ? v_scale : nullptr;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     const int per_cta = workers_of(heads * query_len);
-    const size_t parts = static_cast<size_t>(kMaxCtas) * per_cta * 2 * heads * query_len;
+    const size_t parts = static_cast<size_t>(ctas_of(dim, heads * query_len)) * per_cta * 2 * heads * query_len;
     p.flags = reinterpret_cast<unsigned int *>(ws);
     p.items = reinterpret_cast<JoinItem *>(ws + kHeaderBytes);
     p.partial = reinterpret_cast<float *>(ws + kHeaderBytes + align256(kItemBytes));
@@ -382,7 +389,7 @@ extern "C" sda_status sparse_decode_paged_attention(const sda_tensor *query, con
     // Tiles a request can have at most, by the table's width.
     const int64_t units = requests * groups;
     const int64_t widest = (p.cap + static_cast<int64_t>(p.tile) - 1) / p.tile;
-    const int most = std::min(kMaxCtas, 2 * sms);
+    const int most = std::min(ctas_of(dim, p.rows), ctas_per_sm(static_cast<int>(dim), tiles_of_rows(p.rows)) * sms);
     p.min_tiles = kMinTiles;
     p.whole_units = widest <= kWholeTiles;
     // Few tiles: a worker on each of as many SMs first.
@@ -403,7 +410,7 @@ extern "C" sda_status sparse_decode_paged_attention(const sda_tensor *query, con
     // A block an item (at most eight rows of a unit) as long as they run together.
     const int64_t items = units * ((p.rows + kJoinWarps - 1) / kJoinWarps);
     const int64_t rows_to_join = units <= p.workers / kManyPieces ? units * p.rows : items;
-    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(2 * most, rows_to_join)));
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(4 * sms, rows_to_join)));
     auto join = dim == 64    ? sda_paged_join_kernel<64>
                 : dim == 128 ? sda_paged_join_kernel<128>
                 : dim == 192 ? sda_paged_join_kernel<192>

@@ -38,8 +38,8 @@ namespace paged {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxRows = 64;                    // query_len * heads
-constexpr int kMaxCtas = 304;                   // two CTAs on each of 152 SMs
-constexpr int kMaxWorkers = kMaxCtas * kWarps;
+constexpr int kSms = 152;
+constexpr int kMaxWorkers = kSms * 3 * kWarps;  // three CTAs on each SM
 constexpr int kUnitCost = 4;                    // tiles that a unit's end is worth on the line
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
@@ -96,6 +96,15 @@ constexpr int stage_slots(int row_bytes, int mt)
     return mt > 1 && row_bytes > 384 ? 2 * slots : slots;
 }
 
+// CTAs that share an SM.  The products of several tiles of 64 dims gain from a
+// third (32 rows, bf16: 207 -> 177 us for 1 GB of cache; 64 rows: 403 -> 326); one
+// tile would lose its ring (165 -> 192), and from 128 dims on the registers are
+// the second CTA's.
+constexpr int ctas_per_sm(int dim, int mt)
+{
+    return dim <= 64 && mt > 1 ? 3 : 2;
+}
+
 // M tiles (of 16 query rows) of a worker; three make four.
 constexpr int tiles_of_rows(int rows)
 {
@@ -132,7 +141,9 @@ struct Shape {
     // there they take a third of the ring's place (each lane its own words).
     static constexpr bool kQShared = D > 192;
     static constexpr int kQBytes = kQShared ? kSteps * 32 * 16 : 0;     // of a warp
-    static constexpr int kRing = (96 * 1024 - kWarps * kQBytes) / kStageBytes / kWorkers;   // stages of a worker
+    static constexpr int kPerSm = ctas_per_sm(D, MT);
+    static constexpr int kRingBytes = (kPerSm == 2 ? 96 : 64) * 1024;
+    static constexpr int kRing = (kRingBytes - kWarps * kQBytes) / kStageBytes / kWorkers;  // stages of a worker
     static constexpr int kStages = kRing * kWorkers;
     static constexpr int kQOff = kStages * kStageBytes;
     static constexpr int kBarOff = kQOff + kWarps * kQBytes;
@@ -141,7 +152,7 @@ struct Shape {
     static constexpr int kCtlOff = (kIssuedOff + 4 * kStages + 15) / 16 * 16;
     static constexpr int kStateOff = kCtlOff + 16 + 8 * (kThreads + kWarps);
     static constexpr int kBytes = kStateOff + kWarps * kStateBytes + 1024;         // + the base's alignment
-    static_assert(kStageBytes % 1024 == 0 && kRing >= 2 && kBytes <= 115712, "ring");
+    static_assert(kStageBytes % 1024 == 0 && kRing >= 2 && kBytes <= 232448 / kPerSm - 1024, "ring");
 };
 
 // A worker's part of the line, unit by unit.
@@ -642,7 +653,7 @@ private:
 };
 
 template <bool FP8, int D, int MT, bool FULL>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL>::kPerSm)
     sda_paged_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_constant__ Params p)
 {
     using S = Shape<FP8, D, MT, FULL>;
