@@ -335,7 +335,7 @@ _step_workspaces: dict = {}
 
 
 def _new_step_workspace(index: int, handle: int, nbytes: int, stream):
-    """The serving-step entries' default workspace, zeroed on the call's stream: kept per
+    """The serving-step entries' default workspace, its header zeroed on the call's stream: kept per
     (device, stream) and grown on demand like `default_workspace`'s, but a capture gets one
     of its own, zeroed in the graph, that no other graph or eager call shares.  Returns
     (tensor, address, bytes)."""
@@ -345,7 +345,8 @@ def _new_step_workspace(index: int, handle: int, nbytes: int, stream):
         have = _step_workspaces.get((index, handle))
         if have is not None and have[2] >= nbytes and not capturing:
             return have
-        ws = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        ws[:256].zero_()                        # the header: all that has to be zero
         have = ws, ws.data_ptr(), nbytes
         if not capturing:
             _step_workspaces[index, handle] = have

@@ -53,6 +53,10 @@ __global__ void __launch_bounds__(kJoinThreads) sda_paged_join_kernel(const __gr
         if (i + static_cast<int>(gridDim.x) < count)
             next = p.items[i + gridDim.x];
         const int n = item.pieces;
+        // what no split kernel wrote (a workspace whose header was not zeroed) is left out
+        if (n < 1 || item.rows < 1 || item.first < 0 || item.first > p.workers - n || item.request < 0 || item.request >= p.requests ||
+            item.group < 0 || item.group >= p.groups || item.row < 0 || item.row > p.rows - item.rows)
+            continue;
         const bool shared = n > kManyPieces;
         const int r = item.row + (shared ? 0 : warp);
         if (!shared && warp >= item.rows)
@@ -61,26 +65,30 @@ __global__ void __launch_bounds__(kJoinThreads) sda_paged_join_kernel(const __gr
         auto place = [&](int k) {
             return ((static_cast<int64_t>(item.first) + k) * 2 + (k == 0 ? 1 : 0)) * p.rows + r;
         };
+        const int j = r / H, h = r - j * H;
+        const int64_t token = static_cast<int64_t>(item.request) * p.query_len + j;
+        const uint16_t *gate = p.gate ? p.gate + token * p.g_s0 + static_cast<int64_t>(item.group * H + h) * p.g_s1 : nullptr;
+        const uint16_t gate_bits = gate ? *gate : 0;            // beside what follows
+        const float vs = p.v_scale ? *p.v_scale : 1.0f;
+
         // The pieces that saw a token (and were not merged into a neighbour's),
-        // in order: a lane each, or a list in shared memory.
-        int live = 0, mine = 0;                 // this lane's piece
+        // in order: bits and a lane each, or a list in shared memory.
+        unsigned have = 0;
+        int live = 0;
         float l = -INFINITY;
         if (!shared) {
             l = lane < n ? p.part_lse[place(lane)] : -INFINITY;
-            const unsigned have = __ballot_sync(~0u, l != -INFINITY);
-            live = __popc(have);
-            mine = lane < live ? __fns(have, 0, lane + 1) : 0;
-            l = __shfl_sync(~0u, l, mine);
+            have = __ballot_sync(~0u, l != -INFINITY);
         } else {
             for (int k0 = 0; k0 < n; k0 += kJoinThreads) {
                 const int k = k0 + threadIdx.x;
                 const float x = k < n ? p.part_lse[place(k)] : -INFINITY;
-                const unsigned have = __ballot_sync(~0u, x != -INFINITY);
+                const unsigned some = __ballot_sync(~0u, x != -INFINITY);
                 __syncthreads();                // the list and counts of the last round, or item, have been read
                 if (lane == 0)
-                    counts[warp] = __popc(have);
+                    counts[warp] = __popc(some);
                 __syncthreads();
-                int at = live + __popc(have & ((1u << lane) - 1u));
+                int at = live + __popc(some & ((1u << lane) - 1u));
                 for (int w = 0; w < kJoinWarps; ++w) {
                     at += w < warp ? counts[w] : 0;
                     live += counts[w];
@@ -92,80 +100,78 @@ __global__ void __launch_bounds__(kJoinThreads) sda_paged_join_kernel(const __gr
             }
             __syncthreads();
         }
-        auto lse_at = [&](int k) { return shared ? list_lse[k] : __shfl_sync(~0u, l, k); };
-        float M = -INFINITY;
+        float M = l;
         for (int k = lane; k < live; k += 32)
-            M = fmaxf(M, shared ? list_lse[k] : l);
+            M = fmaxf(M, list_lse[k]);
         M = warp_max(M);
         const float ref = M == -INFINITY ? 0.0f : M;
-        float W = 0.0f;
+        float W = shared ? 0.0f : exp2f(l - ref);
         for (int k = lane; k < live; k += 32)
-            W += exp2f((shared ? list_lse[k] : l) - ref);
+            W += exp2f(list_lse[k] - ref);
         W = warp_sum(W);
 
         float2 acc[kVecs];
 #pragma unroll
-        for (int j = 0; j < kVecs; ++j)
-            acc[j] = make_float2(0.0f, 0.0f);
-        const int first = shared ? warp : 0, step = shared ? kJoinWarps : 1;
-        for (int k0 = first; k0 < live; k0 += step * kUnroll) {
+        for (int i = 0; i < kVecs; ++i)
+            acc[i] = make_float2(0.0f, 0.0f);
+        int at = warp;                          // of the list
+        while (have != 0 || at < live) {
             float2 x[kUnroll][kVecs];
             float w[kUnroll];
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
-                const int k = min(k0 + u * step, live - 1);
-                w[u] = k0 + u * step < live ? lse_at(k) : -INFINITY;
-                const int piece = shared ? list_piece[k] : __shfl_sync(~0u, mine, k);
-                const float2 *src = reinterpret_cast<const float2 *>(p.partial + place(piece) * D) + lane;
+                const bool some = shared ? at < live : have != 0;
+                const int k = !some ? 0 : shared ? list_piece[at] : __ffs(have) - 1;
+                w[u] = shared ? (some ? list_lse[at] : 0.0f) : __shfl_sync(~0u, l, k);
+                w[u] = some ? w[u] : -INFINITY;
+                const float2 *src = reinterpret_cast<const float2 *>(p.partial + place(k) * D) + lane;
 #pragma unroll
-                for (int j = 0; j < kVecs; ++j)
-                    x[u][j] = k0 + u * step < live ? src[32 * j] : make_float2(0.0f, 0.0f);
+                for (int i = 0; i < kVecs; ++i)
+                    x[u][i] = some ? src[32 * i] : make_float2(0.0f, 0.0f);
+                have &= have - 1;
+                at += kJoinWarps;
             }
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
                 const float f = exp2f(w[u] - ref);
 #pragma unroll
-                for (int j = 0; j < kVecs; ++j) {
-                    acc[j].x += f * x[u][j].x;
-                    acc[j].y += f * x[u][j].y;
+                for (int i = 0; i < kVecs; ++i) {
+                    acc[i].x += f * x[u][i].x;
+                    acc[i].y += f * x[u][i].y;
                 }
             }
+            if (!shared)
+                at = 0;
         }
         if (shared) {
             // the last item's sums were read before this item's list was made
 #pragma unroll
-            for (int j = 0; j < kVecs; ++j)
-                sums[warp][32 * j + lane] = acc[j];
+            for (int i = 0; i < kVecs; ++i)
+                sums[warp][32 * i + lane] = acc[i];
             __syncthreads();
             if (warp > 0)
                 continue;
 #pragma unroll
             for (int w = 1; w < kJoinWarps; ++w)
 #pragma unroll
-                for (int j = 0; j < kVecs; ++j) {
-                    acc[j].x += sums[w][32 * j + lane].x;
-                    acc[j].y += sums[w][32 * j + lane].y;
+                for (int i = 0; i < kVecs; ++i) {
+                    acc[i].x += sums[w][32 * i + lane].x;
+                    acc[i].y += sums[w][32 * i + lane].y;
                 }
         }
 
         const bool empty = M == -INFINITY && W == 0.0f;         // a row that saw no token; NaN goes on
-        const int j = r / H, h = r - j * H;
-        const int64_t token = static_cast<int64_t>(item.request) * p.query_len + j;
         const int64_t row = token * p.groups + item.group;
-        float f = empty ? 0.0f : 1.0f / W;
-        if (p.v_scale)
-            f *= *p.v_scale;
-        if (p.gate)
-            f *= gate_factor(p.gate[token * p.g_s0 + static_cast<int64_t>(item.group * H + h) * p.g_s1]);
+        const float f = empty ? 0.0f : vs / W * (gate ? gate_factor(gate_bits) : 1.0f);
         uint16_t *dst = p.output + row * p.o_s0 + h * p.o_s1 + 2 * lane;
 #pragma unroll
-        for (int j = 0; j < kVecs; ++j) {
-            const uint32_t w = pack_bf16(acc[j].x * f, acc[j].y * f);
+        for (int i = 0; i < kVecs; ++i) {
+            const uint32_t w = pack_bf16(acc[i].x * f, acc[i].y * f);
             if (p.o_vec) {
-                *reinterpret_cast<uint32_t *>(dst + 64 * j) = w;
+                *reinterpret_cast<uint32_t *>(dst + 64 * i) = w;
             } else {
-                dst[64 * j] = static_cast<uint16_t>(w);
-                dst[64 * j + 1] = static_cast<uint16_t>(w >> 16);
+                dst[64 * i] = static_cast<uint16_t>(w);
+                dst[64 * i + 1] = static_cast<uint16_t>(w >> 16);
             }
         }
         if (p.lse && lane == 0)

@@ -27,7 +27,7 @@ constexpr int kArrays = 6;
 constexpr int kQuad = 4;                        // consecutive token rows a thread writes at a time
 constexpr int kWarpRows = 32 * kQuad;           // rows of a warp's turn
 constexpr uint32_t kMostSum = 0x7FFFFFFFu;      // sums stay here: beyond any count of pages or rows
-constexpr int kTicketWord = 16;                 // of the workspace header: CTAs past their reads
+constexpr int kTicketWord = 18;                 // of the workspace header: CTAs past their reads
 
 struct PlanParams {
     const int32_t *context, *added;
