@@ -221,8 +221,12 @@ size_t align256(size_t n)
 
 // A worker takes at least this many tiles before the line is cut finer.
 constexpr int kMinTiles = 2;
-// Units of at most this many tiles (by the table's width) are never cut.
-constexpr int kWholeTiles = 8;
+// Units of at most this many tiles (by the table's width) are never cut: a worker
+// takes them whole.  Few units, or units of up to as many tiles for each of a CTA's
+// workers, a CTA takes instead (211 tokens of 46 requests x 2 groups, E4M3: cut and
+// joined 16.7 us, by CTAs 11.7), but for units too short to share.
+constexpr int kWholeTiles = 8, kSharedTiles = 3;
+constexpr int kRounds = 4;                      // times the CTAs that run together, at most
 
 // CTAs of a launch, at most.
 int ctas_of(int64_t dim, int64_t rows)
@@ -397,10 +401,12 @@ extern "C" sda_status sparse_decode_paged_attention(const sda_tensor *query, con
     const int64_t widest = (p.cap + static_cast<int64_t>(p.tile) - 1) / p.tile;
     const int most = std::min(ctas_of(dim, p.rows), ctas_per_sm(static_cast<int>(dim), tiles_of_rows(p.rows)) * sms);
     p.min_tiles = kMinTiles;
-    p.whole_units = widest <= kWholeTiles;
+    p.cta_units = per_cta > 1 && widest >= kSharedTiles && widest <= kWholeTiles * per_cta &&
+                  units <= (widest > kWholeTiles ? kRounds : 1) * static_cast<int64_t>(most);
+    p.whole_units = !p.cta_units && widest <= kWholeTiles;
     // Few tiles: a worker on each of as many SMs first.
     const int64_t want = p.whole_units ? units : (units * (widest + kUnitCost) - 1) / (kMinTiles + kUnitCost) + 1;
-    p.ctas = static_cast<int>(std::min<int64_t>(most, std::max<int64_t>(1, want)));
+    p.ctas = static_cast<int>(p.cta_units ? units : std::min<int64_t>(most, std::max<int64_t>(1, want)));
     p.workers = p.ctas * per_cta;
     p.workers_inv = inverse_of(static_cast<unsigned>(p.workers));
     p.tile_inv = inverse_of(static_cast<unsigned>(p.tile));
@@ -411,7 +417,7 @@ extern "C" sda_status sparse_decode_paged_attention(const sda_tensor *query, con
                      : dim == 192 ? (fp8 ? launch_fp8_192 : launch_bf16_192)
                                   : (fp8 ? launch_fp8_256 : launch_bf16_256);
     const sda_status st = launch(tmap, p, stream);
-    if (st != SDA_OK || p.whole_units)
+    if (st != SDA_OK || p.whole_units || p.cta_units)
         return st;
     // A block an item (at most eight rows of a unit) as long as they run together.
     const int64_t items = units * ((p.rows + kJoinWarps - 1) / kJoinWarps);

@@ -23,6 +23,9 @@
 //   * A worker's first warp issues the TMA boxes of the stage that comes into
 //     the place just used up; it looks pages up a lane a piece, a batch ahead,
 //     and runs ahead over unit boundaries.
+//   * Short units (a table of few tiles) are not put on the line: a worker takes
+//     each whole, or where they are few a CTA does (ALONE), its workers a share of
+//     the tiles each, and merges them itself; nothing is left for the join.
 // Two CTAs of four warps an SM: eight warps leave each thread the registers for
 // a tile's whole Q and output.
 #pragma once
@@ -81,7 +84,7 @@ struct Params {
     int requests, groups, heads, query_len, rows;   // rows: query_len * heads
     int table_cols, block, cap;                 // cap: tokens the table's width can hold
     int piece, tile;                            // tokens of a TMA box and of a stage
-    int ctas, workers, min_tiles, whole_units;
+    int ctas, workers, min_tiles, whole_units, cta_units;   // cta_units: ALONE
     unsigned long long per_block_inv, tile_inv, workers_inv;    // inverse_of the pieces of a page, tile, workers
     int q_vec, o_vec;                           // 8-byte loads of q and stores of the output
 };
@@ -126,10 +129,11 @@ __device__ __forceinline__ uint32_t quotient(uint32_t x, unsigned long long inve
 constexpr int kStateBytes = 136;                // WarpState
 
 // FULL: a piece fills a stage (pages of at least a stage's tokens, in whole
-// stages), so the offsets in a stage are constants.
-template <bool FP8, int D, int MT, bool FULL>
+// stages), so the offsets in a stage are constants.  ALONE: each CTA has one unit,
+// its workers a share of the unit's tiles each.
+template <bool FP8, int D, int MT, bool FULL, bool ALONE = false>
 struct Shape {
-    static constexpr bool kFull = FULL;
+    static constexpr bool kFull = FULL, kAlone = ALONE;
     static constexpr int kElt = FP8 ? 1 : 2;
     static constexpr int kRowBytes = 2 * D * kElt;
     static constexpr int kBands = kRowBytes / 128;
@@ -162,7 +166,7 @@ struct Segment {
 
 struct Walk {
     long long left;                             // line from the unit's start to the part's end
-    int request, group, tile;                   // (whole_units: units still to take)
+    int request, group, tile;                   // (whole_units: units still to take; ALONE: 1 + tiles, if there is a unit)
 
     static __device__ __forceinline__ int length(const Params &p, int q)
     {
@@ -174,34 +178,47 @@ struct Walk {
         return len > 0 ? static_cast<int>(quotient(len - 1, p.tile_inv)) + 1 : 0;
     }
 
+    template <bool ALONE>
     __device__ __forceinline__ bool next(const Params &p, Segment &s)
     {
-        while (left > 0 && request < p.requests) {
-            const int len = length(p, request), tiles = tiles_of(p, len);
+        if constexpr (ALONE) {                  // the share may be empty
             s.request = request;
             s.group = group;
             s.first = tile;
-            s.tiles = tiles;
-            s.len = len;
-            // a unit's cost comes before its tiles
-            s.last = p.whole_units ? tiles
-                                   : static_cast<int>(max(min(left - kUnitCost, static_cast<long long>(tiles)),
-                                                          static_cast<long long>(tile)));
-            const bool some = s.last > s.first;
-            if (s.last == tiles) {
-                left -= p.whole_units ? 1 : tiles > 0 ? tiles + kUnitCost : 0;
-                tile = 0;
-                if (++group == p.groups || (tiles == 0 && !p.whole_units)) {
-                    group = 0;
-                    ++request;
+            s.last = tile + static_cast<int>(left) - 1;
+            s.len = length(p, request);
+            s.tiles = tiles_of(p, s.len);
+            const bool some = left > 0;
+            left = 0;
+            return some;
+        } else {
+            while (left > 0 && request < p.requests) {
+                const int len = length(p, request), tiles = tiles_of(p, len);
+                s.request = request;
+                s.group = group;
+                s.first = tile;
+                s.tiles = tiles;
+                s.len = len;
+                // a unit's cost comes before its tiles
+                s.last = p.whole_units ? tiles
+                                       : static_cast<int>(max(min(left - kUnitCost, static_cast<long long>(tiles)),
+                                                              static_cast<long long>(tile)));
+                const bool some = s.last > s.first;
+                if (s.last == tiles) {
+                    left -= p.whole_units ? 1 : tiles > 0 ? tiles + kUnitCost : 0;
+                    tile = 0;
+                    if (++group == p.groups || (tiles == 0 && !p.whole_units)) {
+                        group = 0;
+                        ++request;
+                    }
+                } else {
+                    left = 0;
                 }
-            } else {
-                left = 0;
+                if (some)
+                    return true;
             }
-            if (some)
-                return true;
+            return false;
         }
-        return false;
     }
 };
 
@@ -408,11 +425,18 @@ __device__ __forceinline__ long long boundary(const Params &p, long long total, 
 // w * CTAs + CTA, which spreads them over the SMs.  Every thread of the block
 // calls it; a worker's warps look for its part together.
 // `sums`: kThreads + kWarps values of shared memory.
-template <int WORKERS>
+template <int WORKERS, bool ALONE>
 __device__ __forceinline__ Part find_part(const Params &p, long long *sums, int w, long long &total, int &used, int &v)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int spread = w * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+    if constexpr (ALONE) {
+        const int q = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.groups));
+        const int tiles = Walk::tiles_of(p, Walk::length(p, q));
+        const int first = tiles * w / WORKERS, last = tiles * (w + 1) / WORKERS;
+        total = used = v = 0;
+        return {tiles > 0 ? 1 + last - first : 0, 0, q, static_cast<int>(blockIdx.x) - q * p.groups, first};
+    }
     if (p.whole_units) {
         total = static_cast<long long>(p.requests) * p.groups;
         used = p.workers;
@@ -503,12 +527,13 @@ struct Place {
     long long unit;                             // where the segment's unit begins on the line
 
     // The next segment into seg; a copy of it in `s`.
+    template <bool ALONE>
     __device__ __forceinline__ bool next(const Params &p, long long part_end, Segment &s)
     {
         Walk w = walk;
         __syncwarp();                           // every lane has read it
         unit = part_end - w.left;
-        const bool some = w.next(p, s);
+        const bool some = w.next<ALONE>(p, s);
         walk = w;
         seg = s;
         __syncwarp();
@@ -566,7 +591,7 @@ struct Feed {
         page2 = left2 > 0 && col < p.table_cols ? p.block_table[seg.request * p.bt_s0 + col] : -1;
         tile += n2;
         if (tile >= seg.last) {
-            more = at_line->next(p, 0, seg);
+            more = at_line->template next<S::kAlone>(p, 0, seg);
             tile = seg.first;
         }
     }
@@ -580,7 +605,7 @@ struct Feed {
         lane_stage = lane / per_stage;
         lane_piece = lane - lane_stage * per_stage;
         Segment seg;
-        more = at_line->next(p, 0, seg);
+        more = at_line->template next<S::kAlone>(p, 0, seg);
         tile = seg.first;
         n2 = 0;
         look_up(p);                             // the first batch's table entries are on their way
@@ -652,11 +677,11 @@ private:
     }
 };
 
-template <bool FP8, int D, int MT, bool FULL>
-__global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL>::kPerSm)
+template <bool FP8, int D, int MT, bool FULL, bool ALONE>
+__global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL, ALONE>::kPerSm)
     sda_paged_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_constant__ Params p)
 {
-    using S = Shape<FP8, D, MT, FULL>;
+    using S = Shape<FP8, D, MT, FULL, ALONE>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
@@ -686,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL>::kPerSm)
 
     long long total;
     int used, v;
-    const Part part = find_part<S::kWorkers>(p, sums, worker, total, used, v);
+    const Part part = find_part<S::kWorkers, ALONE>(p, sums, worker, total, used, v);
     // What is needed between units only: this warp's place, its feed's, the line.
     WarpState *state = reinterpret_cast<WarpState *>(smem + S::kStateOff) + warp;
     state->here.walk = state->ahead.walk = {part.left, part.request, part.group, part.tile};
@@ -732,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL>::kPerSm)
         const uint16_t *q_rows;                 // the unit's first query row
         {
             Segment seg;
-            if (!state->here.next(p, state->part_end, seg))
+            if (!state->here.template next<ALONE>(p, state->part_end, seg))
                 break;
             common = seg.len - p.query_len + 1 - seg.first * p.tile;
             left = seg.last - seg.first;
@@ -1073,8 +1098,8 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL>::kPerSm)
         // they are all that its workers have: one piece for the join, not four.
         // The CTA's part of the line lies in the unit, and its first worker has a
         // tile (so every worker comes here once, with this segment).
-        bool merged = false, from_start = false;
-        if (S::kWorkers > 1 && !whole && state->used == p.workers) {
+        bool merged = ALONE, from_start = false;
+        if (S::kWorkers > 1 && !ALONE && !whole && state->used == p.workers) {
             const long long n = state->total, u0 = state->here.unit;
             const int w0 = static_cast<int>(blockIdx.x) * S::kWorkers;
             const long long x0 = boundary(p, n, w0);
@@ -1108,8 +1133,11 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL>::kPerSm)
                     L += st[w * MT * 32 + 1] * (st[w * MT * 32] == -INFINITY ? 1.0f : fast_exp2(st[w * MT * 32] - M));
                 const bool empty = M == -INFINITY && L == 0.0f;
                 const int r = k ? r1 : r0;
-                if (t == 0 && r < R)
-                    p.part_lse[piece * R + r] = worker > 0 || empty ? -INFINITY : M + log2f(L);
+                const float lse2 = empty ? -INFINITY : M + log2f(L);
+                if (!ALONE && t == 0 && r < R)
+                    p.part_lse[piece * R + r] = worker > 0 ? -INFINITY : lse2;
+                if (ALONE && t == 0 && r < R && worker == 0 && p.lse)
+                    p.lse[row_of(r) * p.l_s0 + (r % H) * p.l_s1] = lse2 * kLn2;
                 // all of a warp that saw nothing is 0 (or not a number, and stays that)
                 const float f = empty ? 0.0f : (m_run[k] == -INFINITY ? 1.0f : fast_exp2(m_run[k] - M)) / L;
                 float *dst = outs + (warp * 16 + g + 8 * k) * kStride;
@@ -1141,14 +1169,32 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL>::kPerSm)
                     x.z += y.z;
                     x.w += y.w;
                 }
-                *reinterpret_cast<float4 *>(p.partial + (first * R + r) * D + d) = x;
+                if constexpr (!ALONE) {
+                    *reinterpret_cast<float4 *>(p.partial + (first * R + r) * D + d) = x;
+                    continue;
+                }
+                const int h = r % H;
+                float f = vs;
+                if (p.gate)
+                    f *= gate_factor(p.gate[(static_cast<int64_t>(seg.request) * p.query_len + r / H) * p.g_s0 +
+                                            static_cast<int64_t>(seg.group * H + h) * p.g_s1]);
+                uint16_t *out = p.output + row_of(r) * p.o_s0 + h * p.o_s1 + d;
+                const uint2 w = make_uint2(pack_bf16(x.x * f, x.y * f), pack_bf16(x.z * f, x.w * f));
+                if (p.o_vec) {
+                    *reinterpret_cast<uint2 *>(out) = w;
+                } else {
+                    out[0] = static_cast<uint16_t>(w.x);
+                    out[1] = static_cast<uint16_t>(w.x >> 16);
+                    out[2] = static_cast<uint16_t>(w.y);
+                    out[3] = static_cast<uint16_t>(w.y >> 16);
+                }
             }
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const int r = k ? r1 : r0;
             const float L = l_run[k];
-            if (merged || r >= R)
+            if (ALONE || merged || r >= R)
                 continue;
             // only a row that saw nothing is empty: a sum that is not a number goes on
             const bool empty = m_run[k] == -INFINITY && L == 0.0f;
@@ -1200,7 +1246,7 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL>::kPerSm)
             }
         }
         // ---- The worker that has a cut unit's first tile lists it for the join.
-        if (begins && !ends && mt == 0 && lane == 0) {
+        if (!ALONE && begins && !ends && mt == 0 && lane == 0) {
             const long long end = state->here.unit + kUnitCost + seg.tiles;     // past the unit's last tile
             const int n = static_cast<int>((end * state->used - 1) / state->total) - v + 1;
             const int rows = n > kManyPieces ? 1 : kJoinWarps, items = (R + rows - 1) / rows;
@@ -1243,22 +1289,28 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL>::kPerSm)
     }
 }
 
-template <bool FP8, int D, int MT, bool FULL>
+template <bool FP8, int D, int MT, bool FULL, bool ALONE>
 sda_status launch_shape(const CUtensorMap &tmap, const Params &p, void *stream)
 {
-    using S = Shape<FP8, D, MT, FULL>;
+    using S = Shape<FP8, D, MT, FULL, ALONE>;
     static size_t raised[64] = {};
-    if (!raise_smem(sda_paged_kernel<FP8, D, MT, FULL>, S::kBytes, raised))
+    if (!raise_smem(sda_paged_kernel<FP8, D, MT, FULL, ALONE>, S::kBytes, raised))
         return SDA_ERR_CUDA;
-    return launch_pdl(sda_paged_kernel<FP8, D, MT, FULL>, dim3(static_cast<unsigned>(p.ctas)), dim3(kThreads),
+    return launch_pdl(sda_paged_kernel<FP8, D, MT, FULL, ALONE>, dim3(static_cast<unsigned>(p.ctas)), dim3(kThreads),
                       S::kBytes, stream, tmap, p);
 }
 
 template <bool FP8, int D, int MT>
 sda_status launch_tiles(const CUtensorMap &tmap, const Params &p, void *stream)
 {
-    return p.piece == Shape<FP8, D, MT, true>::kSlots ? launch_shape<FP8, D, MT, true>(tmap, p, stream)
-                                                      : launch_shape<FP8, D, MT, false>(tmap, p, stream);
+    const bool full = p.piece == Shape<FP8, D, MT, true>::kSlots;
+    if constexpr (Shape<FP8, D, MT, true>::kWorkers > 1) {
+        if (p.cta_units)
+            return full ? launch_shape<FP8, D, MT, true, true>(tmap, p, stream)
+                        : launch_shape<FP8, D, MT, false, true>(tmap, p, stream);
+    }
+    return full ? launch_shape<FP8, D, MT, true, false>(tmap, p, stream)
+                : launch_shape<FP8, D, MT, false, false>(tmap, p, stream);
 }
 
 template <bool FP8, int D>
