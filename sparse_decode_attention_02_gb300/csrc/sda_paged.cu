@@ -221,12 +221,18 @@ size_t align256(size_t n)
 
 // A worker takes at least this many tiles before the line is cut finer.
 constexpr int kMinTiles = 2;
-// Units of at most this many tiles (by the table's width) are never cut: a worker
-// takes them whole.  Few units, or units of up to as many tiles for each of a CTA's
-// workers, a CTA takes instead (211 tokens of 46 requests x 2 groups, E4M3: cut and
-// joined 16.7 us, by CTAs 11.7), but for units too short to share.
-constexpr int kWholeTiles = 8, kSharedTiles = 3;
-constexpr int kRounds = 4;                      // times the CTAs that run together, at most
+// Units of at most kWholeTiles tiles (by the table's width) are never cut: a worker
+// takes them whole.  A CTA takes a unit alone instead
+//   * from kSharedTiles tiles on (two of E4M3, 128 dims, 32 rows, 64 requests x 2
+//     groups: 9.0 us shared, 8.4 not);
+//   * up to kAloneTiles tiles a worker (bf16, 192 dims, 2 groups; cut and joined
+//     against alone: 44 tiles, 1 request 15.7, 15.9 us, 76 requests 26.1, 21.0;
+//     94 tiles, 1 request 17.4, 26.9, 76 requests 40.3, 35.0, which lengths that
+//     differ would lose);
+//   * in at most kRounds rounds of CTAs, or one where a worker could take it whole
+//     (10 tiles of E4M3, 128 dims: 1200 units 38.5, 38.5 us, 2400 units 53.5, 71.3).
+constexpr int kWholeTiles = 8, kSharedTiles = 3, kAloneTiles = 12;
+constexpr int kRounds = 4;
 
 // CTAs of a launch, at most.
 int ctas_of(int64_t dim, int64_t rows)
@@ -401,7 +407,7 @@ extern "C" sda_status sparse_decode_paged_attention(const sda_tensor *query, con
     const int64_t widest = (p.cap + static_cast<int64_t>(p.tile) - 1) / p.tile;
     const int most = std::min(ctas_of(dim, p.rows), ctas_per_sm(static_cast<int>(dim), tiles_of_rows(p.rows)) * sms);
     p.min_tiles = kMinTiles;
-    p.cta_units = per_cta > 1 && widest >= kSharedTiles && widest <= kWholeTiles * per_cta &&
+    p.cta_units = per_cta > 1 && widest >= kSharedTiles && widest <= kAloneTiles * per_cta &&
                   units <= (widest > kWholeTiles ? kRounds : 1) * static_cast<int64_t>(most);
     p.whole_units = !p.cta_units && widest <= kWholeTiles;
     // Few tiles: a worker on each of as many SMs first.
