@@ -42,7 +42,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxRows = 64;                    // query_len * heads
 constexpr int kSms = 152;
-constexpr int kMaxWorkers = kSms * 3 * kWarps;  // three CTAs on each SM
+constexpr int kMaxWorkers = kSms * 2 * kWarps;  // two CTAs of them on each SM (or three of two)
 constexpr int kUnitCost = 4;                    // tiles that a unit's end is worth on the line
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
@@ -156,6 +156,7 @@ struct Shape {
     static constexpr int kCtlOff = (kIssuedOff + 4 * kStages + 15) / 16 * 16;
     static constexpr int kStateOff = kCtlOff + 16 + 8 * (kThreads + kWarps);
     static constexpr int kBytes = kStateOff + kWarps * kStateBytes + 1024;         // + the base's alignment
+    static_assert(kPerSm * kWorkers <= 2 * kWarps, "join list");
     static_assert(kStageBytes % 1024 == 0 && kRing >= 2 && kBytes <= 232448 / kPerSm - 1024, "ring");
 };
 

@@ -150,7 +150,8 @@ def test_paged_workspace_bytes(lib):
     assert f(0) == f(65) == f(33, 2) == f(8, 1, 96) == f(8, 0) == 0
     items = 304 * 4 * 8 * 32                                                 # join list
     for heads, ql, dim, workers in ((16, 1, 192, 4), (8, 3, 128, 2), (64, 1, 64, 1), (1, 1, 256, 4), (16, 3, 192, 1)):
-        pieces = 304 * workers * 2 * heads * ql
+        ctas = 456 if dim == 64 and workers < 4 else 304                     # three to an SM, or two
+        pieces = ctas * workers * 2 * heads * ql
         assert f(heads, ql, dim) == 256 + items + pieces * dim * 4 + -(-pieces * 4 // 256) * 256
 
 
