@@ -10,6 +10,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import importlib.util
+import operator
 import os
 import re
 import threading
@@ -100,6 +101,9 @@ def _declare(lib):
     lib.sparse_decode_set_wait_limit_ns.restype = None
     lib.sparse_decode_status_string.argtypes = [ctypes.c_int]
     lib.sparse_decode_status_string.restype = ctypes.c_char_p
+    # of the entry points that csrc/sda_marshal.cpp calls
+    lib.addresses = {f: ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
+                     for f in ("sparse_decode_plan_step", "sparse_decode_rope_append", "sparse_decode_paged_attention")}
     return lib
 
 
@@ -378,8 +382,17 @@ def load_marshal():
     return _marshal
 
 
+def _int32(x) -> int:
+    x = operator.index(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise OverflowError("an argument does not fit 32 bits")
+    return x
+
+
 def _call(fn, tensors, arguments, need: int, workspace, stream, scales=()):
-    """What the serving-step entries share: fn(*arguments(descriptor addresses, scale
+    """What the serving-step entries share where csrc/sda_marshal.cpp does not make the call itself (on
+    a `stream` or device other than the current one, in a capture, the first time, with scales to
+    upload): fn(*arguments(descriptor addresses, scale
     addresses), workspace, its bytes, stream) on the tensors' device.  Where no workspace
     is given it is the stream's default one of at least `need` bytes."""
     keep, where, index, current, handle, capturing = (_marshal or load_marshal()).pack(*tensors)
@@ -399,8 +412,7 @@ def _call(fn, tensors, arguments, need: int, workspace, stream, scales=()):
     else:
         with torch.cuda.device(index):
             rc = fn(*arguments(where, pointers), have[1], have[2], handle)
-    if rc != SDA_OK:
-        raise SdaError(rc, load().sparse_decode_status_string(rc).decode())
+    return rc
 
 
 def sparse_decode_plan_step(context_lens, new_lens, free_pages, free_state, block_table, *, block_size: int,
@@ -423,9 +435,17 @@ def sparse_decode_plan_step(context_lens, new_lens, free_pages, free_state, bloc
             positions, requests = new(positions, slots.shape[0]), new(requests, slots.shape[0])
             seq_lens, token_starts = new(seq_lens, context_lens.shape[0]), new(token_starts, context_lens.shape[0] + 1)
             free_next = new(free_next, 2)
-    _call(lib.sparse_decode_plan_step, (context_lens, new_lens, free_pages, free_state, free_next, block_table, seq_lens,
-                                        token_starts, slots, positions, requests),
-          lambda d, _: (d[0], d[1], int(block_size), int(rows_per_request), *d[2:]), 256, workspace, stream)
+    tensors = (context_lens, new_lens, free_pages, free_state, free_next, block_table, seq_lens, token_starts, slots,
+               positions, requests)
+    rc = None
+    if stream is None:
+        rc = (_marshal or load_marshal()).plan_step(lib.addresses["sparse_decode_plan_step"], _step_workspaces, 256,
+                                                    workspace, *tensors, block_size, rows_per_request)
+    if rc is None:
+        rc = _call(lib.sparse_decode_plan_step, tensors,
+                   lambda d, _: (d[0], d[1], _int32(block_size), _int32(rows_per_request), *d[2:]), 256, workspace, stream)
+    if rc:
+        raise SdaError(rc, lib.sparse_decode_status_string(rc).decode())
     return seq_lens, token_starts, slots, positions, requests, free_next
 
 
@@ -447,15 +467,21 @@ def sparse_decode_rope_append(query, key, value, positions, inv_freq, slots, cac
         query_out = torch.zeros_like(query) if slots is not None else torch.empty_like(query)
     if key is None:
         cache = None
-    parts = None
-    if sections is not None:
-        if positions is None or len(sections) != positions.shape[0] or len(sections) > 4:
-            raise ValueError("sparse_decode: a section for each axis of positions")
-        parts = _INT4(*sections)                # as many as there are axes are read
-    _call(lib.sparse_decode_rope_append, (query, query_out, key, value, positions, inv_freq, slots, cache),
-          lambda d, s: (*d[:6], parts, bool(interleaved_axes), bool(adjacent_pairs), float(amplitude), *d[6:], s[0][0],
-                        s[1][0]), 256,
-          workspace, stream, (k_scale, v_scale))
+    if sections is not None and (positions is None or len(sections) != positions.shape[0] or len(sections) > 4):
+        raise ValueError("sparse_decode: a section for each axis of positions")
+    tensors = query, query_out, key, value, positions, inv_freq, slots, cache
+    rc = None
+    if stream is None:
+        rc = (_marshal or load_marshal()).rope_append(lib.addresses["sparse_decode_rope_append"], _step_workspaces, 256,
+                                                      workspace, *tensors, sections, interleaved_axes, adjacent_pairs,
+                                                      amplitude, k_scale, v_scale)
+    if rc is None:
+        parts = None if sections is None else _INT4(*map(_int32, sections))   # as many as there are axes are read
+        rc = _call(lib.sparse_decode_rope_append, tensors,
+                   lambda d, s: (*d[:6], parts, bool(interleaved_axes), bool(adjacent_pairs), float(amplitude), *d[6:],
+                                 s[0][0], s[1][0]), 256, workspace, stream, (k_scale, v_scale))
+    if rc:
+        raise SdaError(rc, lib.sparse_decode_status_string(rc).decode())
     return query_out
 
 
@@ -463,7 +489,7 @@ _paged_bytes: dict = {}                        # by (heads, query_len, head_dim)
 
 
 def paged_workspace_bytes(heads: int, query_len: int = 1, head_dim: int = 192) -> int:
-    return load().sparse_decode_paged_workspace_bytes(int(heads), int(query_len), int(head_dim))
+    return load().sparse_decode_paged_workspace_bytes(_int32(heads), _int32(query_len), _int32(head_dim))
 
 
 def sparse_decode_paged_attention(query, cache, block_table, seq_lens, output, *, scale: float,
@@ -474,12 +500,24 @@ def sparse_decode_paged_attention(query, cache, block_table, seq_lens, output, *
     cache into `output`, and the rows' log-sum-exps into `lse` if given; see
     include/sdattn.h for the contract."""
     lib = _lib or load()
-    shape = query.shape[1], int(query_len), query.shape[-1]
-    need = _paged_bytes.get(shape)
-    if need is None:
-        need = _paged_bytes[shape] = lib.sparse_decode_paged_workspace_bytes(*shape) or 256
-    _call(lib.sparse_decode_paged_attention, (query, cache, block_table, seq_lens, output, lse, gate),
-          lambda d, s: (*d[:6], float(scale), int(query_len), s[0][0], s[1][0], d[6]), need, workspace, stream, (k_scale, v_scale))
+    need = 0
+    if workspace is None:
+        shape = query.shape[1], int(query_len), query.shape[-1]
+        need = _paged_bytes.get(shape)
+        if need is None:
+            need = _paged_bytes[shape] = paged_workspace_bytes(*shape) or 256
+    tensors = query, cache, block_table, seq_lens, output, lse, gate
+    rc = None
+    if stream is None:
+        rc = (_marshal or load_marshal()).paged_attention(lib.addresses["sparse_decode_paged_attention"],
+                                                          _step_workspaces, need, workspace, *tensors, scale, query_len,
+                                                          k_scale, v_scale)
+    if rc is None:
+        rc = _call(lib.sparse_decode_paged_attention, tensors,
+                   lambda d, s: (*d[:6], float(scale), _int32(query_len), s[0][0], s[1][0], d[6]), need, workspace, stream,
+                   (k_scale, v_scale))
+    if rc:
+        raise SdaError(rc, lib.sparse_decode_status_string(rc).decode())
 
 
 def read_errors(workspace: torch.Tensor, clear: bool = False,
