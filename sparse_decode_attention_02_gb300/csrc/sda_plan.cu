@@ -248,6 +248,9 @@ __global__ void __launch_bounds__(kThreads) sda_plan_kernel(const __grid_constan
     __syncthreads();
     const int rows = granted[0], taken = granted[1], returned = granted[2];
 
+    // index into the ring: i < 2 * ring_size
+    auto ring_at = [&](uint32_t i) { return i >= static_cast<uint32_t>(p.ring_size) ? i - p.ring_size : i; };
+
     // The lengths and the ring's state may be updated in place, so they are
     // written by whichever CTA is the last to have read them.
     if (gridDim.x > 1) {
@@ -267,7 +270,7 @@ __global__ void __launch_bounds__(kThreads) sda_plan_kernel(const __grid_constan
         if (threadIdx.x == 0) {
             p.starts[Q] = p.per_request > 0 ? p.rows : rows;
             if (ring_ok) {
-                p.next[0] = static_cast<int>((static_cast<long long>(start) + taken) % p.ring_size);
+                p.next[0] = static_cast<int>(ring_at(static_cast<uint32_t>(start + taken)));
                 p.next[1] = count - taken + returned;
             } else {
                 const int s0 = p.state[0], s1 = p.state[1];
@@ -277,16 +280,15 @@ __global__ void __launch_bounds__(kThreads) sda_plan_kernel(const __grid_constan
         }
     }
 
-    // index into the ring: i < 2 * ring_size
-    auto ring_at = [&](uint32_t i) { return i >= static_cast<uint32_t>(p.ring_size) ? i - p.ring_size : i; };
-
-    // ---- Token rows, packed.
+    // ---- Token rows, packed: runs of them, where there is more than one a thread.
     const int lane = threadIdx.x & 31;
     const int warps = gridDim.x * kWarps, warp = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int step = gridDim.x * kThreads, me = blockIdx.x * kThreads + threadIdx.x;
+    const bool runs = p.per_request == 0 && p.rows > step;
     // a warp's turns are neighbours: its requests follow one another
     const int turns = ((p.rows + kWarpRows - 1) / kWarpRows + warps - 1) / warps;
     int qa = 0, qb = -1;                        // requests of the turn's first and last token row
-    for (int turn = 0; turn < turns && p.per_request == 0; ++turn) {
+    for (int turn = 0; turn < turns && runs; ++turn) {
         const long long w = (static_cast<long long>(warp) * turns + turn) * kWarpRows;
         if (w >= p.rows)
             break;
@@ -365,17 +367,25 @@ __global__ void __launch_bounds__(kThreads) sda_plan_kernel(const __grid_constan
         }
     }
 
-    // ---- Token rows, so many for each request: its tokens are the last of them.
-    const int step = gridDim.x * kThreads, me = blockIdx.x * kThreads + threadIdx.x;
-    for (int r = me; r < p.rows && p.per_request > 0; r += step) {
-        const int q = r / p.per_request, c = ctx[q];
-        const int at = len[q] - ((q + 1) * p.per_request - r);  // the row's position
-        const bool token = at >= c && len[q] > c;
+    // ---- Token rows, each by itself.  So many for each request: its tokens are the
+    // last of them.
+    for (int r = me; r < p.rows && !runs; r += step) {
+        int q, at;                                              // the row's request and position
+        bool token;
+        if (p.per_request > 0) {
+            q = r / p.per_request;
+            at = len[q] - ((q + 1) * p.per_request - r);
+            token = at >= ctx[q] && len[q] > ctx[q];
+        } else {
+            token = r < rows;
+            q = token ? last_at_most(tok, 0, Q - 1, r) : 0;
+            at = token ? ctx[q] + (r - tok[q]) : 0;
+        }
         long long slot = -1;
         if (token) {
             const int col = static_cast<int>(pages_before(p, static_cast<uint32_t>(at))), off = at - col * B;
-            const int page = at - off < c ? p.table[q * p.table_s0 + col]
-                                          : p.ring[ring_at(static_cast<uint32_t>(start + adj[q] + col))];
+            const int page = at - off < ctx[q] ? p.table[q * p.table_s0 + col]
+                                               : p.ring[ring_at(static_cast<uint32_t>(start + adj[q] + col))];
             if (page >= 0)
                 slot = static_cast<long long>(page) * B + off;
             else
