@@ -306,13 +306,8 @@ extern "C" sda_status sparse_decode_paged_attention(const sda_tensor *query, con
     if (pages > INT32_MAX || rows > INT32_MAX / kMaxRows || block_table->shape[1] > INT32_MAX ||
         block > (1 << 24) || groups > (1 << 16))
         return SDA_ERR_UNSUPPORTED;
-    // A TMA box holds the longest run of tokens that fits a stage and divides the page.
     const int elt = fp8 ? 1 : 2, row_bytes = static_cast<int>(2 * dim) * elt;
-    const int slots = stage_slots(row_bytes, tiles_of_rows(static_cast<int>(heads) * query_len));
-    int piece = static_cast<int>(std::min<int64_t>(block, slots)) / 8 * 8;
-    while (piece > 0 && block % piece != 0)
-        piece -= 8;
-    if (piece == 0)
+    if (block % 8 != 0)
         return SDA_ERR_UNSUPPORTED;
     if (!aligned(cache->data, 16))
         return SDA_ERR_UNSUPPORTED;
@@ -328,6 +323,39 @@ extern "C" sda_status sparse_decode_paged_attention(const sda_tensor *query, con
         (!block_table->data && block_table->shape[1] > 0))
         return SDA_ERR_INVALID;
 
+    // ---- How the work is split, by the tiles that a request can have at most.
+    const int sms = sm_count();
+    if (sms < 1)
+        return SDA_ERR_CUDA;
+    Params p = {};
+    p.rows = static_cast<int>(heads) * query_len;
+    p.cap = static_cast<int>(std::min<int64_t>(block_table->shape[1] * block, INT32_MAX - 4096));
+    const int64_t units = requests * groups;
+    const int mt = tiles_of_rows(p.rows), per_cta = workers_of(p.rows);
+    const int most = std::min(ctas_of(dim, p.rows), ctas_per_sm(static_cast<int>(dim), mt) * sms);
+    // A TMA box holds the longest run of tokens that fits a stage and divides the
+    // page, a tile the boxes that fit.  The tiles of the table's width:
+    auto widest_with = [&](bool alone) {
+        const int slots = stage_slots(row_bytes, mt, alone);
+        p.piece = static_cast<int>(std::min<int64_t>(block, slots)) / 8 * 8;
+        while (block % p.piece != 0)
+            p.piece -= 8;
+        p.tile = slots / p.piece * p.piece;
+        return (p.cap + static_cast<int64_t>(p.tile) - 1) / p.tile;
+    };
+    int64_t widest = widest_with(true);
+    p.cta_units = per_cta > 1 && widest >= kSharedTiles && widest <= kAloneTiles * per_cta &&
+                  units <= (widest > kWholeTiles ? kRounds : 1) * static_cast<int64_t>(most);
+    if (!p.cta_units)
+        widest = widest_with(false);
+    p.whole_units = !p.cta_units && widest <= kWholeTiles;
+    p.min_tiles = kMinTiles;
+    // Few tiles: a worker on each of as many SMs first.
+    const int64_t want = p.whole_units || p.cta_units ? units
+                                                      : (units * (widest + kUnitCost) - 1) / (kMinTiles + kUnitCost) + 1;
+    p.ctas = static_cast<int>(p.cta_units ? units : std::min<int64_t>(most, std::max<int64_t>(1, want)));
+    p.workers = p.ctas * per_cta;
+
     // ---- The cache as (128 bytes, token, band, group, page): a box is a piece
     // of all bands, landing as [band][token][128 bytes], swizzled.
     EncodeTiledFn encode = encode_fn();
@@ -341,7 +369,7 @@ extern "C" sda_status sparse_decode_paged_attention(const sda_tensor *query, con
     const cuuint64_t gstride[4] = {static_cast<cuuint64_t>(cache->stride[2] * elt), 128u,
                                    static_cast<cuuint64_t>(cache->stride[1] * elt),
                                    static_cast<cuuint64_t>(cache->stride[0] * elt)};
-    const cuuint32_t box[5] = {static_cast<cuuint32_t>(128 / elt), static_cast<cuuint32_t>(piece),
+    const cuuint32_t box[5] = {static_cast<cuuint32_t>(128 / elt), static_cast<cuuint32_t>(p.piece),
                                static_cast<cuuint32_t>(bands), 1, 1};
     const cuuint32_t estride[5] = {1, 1, 1, 1, 1};
     if (encode(&tmap, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
@@ -350,7 +378,6 @@ extern "C" sda_status sparse_decode_paged_attention(const sda_tensor *query, con
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return SDA_ERR_UNSUPPORTED;
 
-    Params p = {};
     p.query = static_cast<const uint16_t *>(query->data);
     p.q_s0 = query->stride[0];
     p.q_s1 = query->stride[1];
@@ -374,7 +401,6 @@ extern "C" sda_status sparse_decode_paged_attention(const sda_tensor *query, con
     p.k_scale = fp8 ? k_scale : nullptr;
     p.v_scale = fp8 ? v_scale : nullptr;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    const int per_cta = workers_of(heads * query_len);
     const size_t parts = static_cast<size_t>(ctas_of(dim, heads * query_len)) * per_cta * 2 * heads * query_len;
     p.flags = reinterpret_cast<unsigned int *>(ws);
     p.items = reinterpret_cast<JoinItem *>(ws + kHeaderBytes);
@@ -387,33 +413,14 @@ extern "C" sda_status sparse_decode_paged_attention(const sda_tensor *query, con
     p.groups = static_cast<int>(groups);
     p.heads = static_cast<int>(heads);
     p.query_len = query_len;
-    p.rows = static_cast<int>(heads) * query_len;
     p.table_cols = static_cast<int>(block_table->shape[1]);
     p.block = static_cast<int>(block);
-    p.cap = static_cast<int>(std::min<int64_t>(block_table->shape[1] * block, INT32_MAX - 4096));
-    p.piece = piece;
-    p.tile = slots / piece * piece;
     auto runs_of_4 = [](const sda_tensor *t) {
         return aligned(t->data, 8) && t->stride[0] % 4 == 0 && t->stride[1] % 4 == 0;
     };
     p.q_vec = runs_of_4(query);
     p.o_vec = runs_of_4(output);
 
-    const int sms = sm_count();
-    if (sms < 1)
-        return SDA_ERR_CUDA;
-    // Tiles a request can have at most, by the table's width.
-    const int64_t units = requests * groups;
-    const int64_t widest = (p.cap + static_cast<int64_t>(p.tile) - 1) / p.tile;
-    const int most = std::min(ctas_of(dim, p.rows), ctas_per_sm(static_cast<int>(dim), tiles_of_rows(p.rows)) * sms);
-    p.min_tiles = kMinTiles;
-    p.cta_units = per_cta > 1 && widest >= kSharedTiles && widest <= kAloneTiles * per_cta &&
-                  units <= (widest > kWholeTiles ? kRounds : 1) * static_cast<int64_t>(most);
-    p.whole_units = !p.cta_units && widest <= kWholeTiles;
-    // Few tiles: a worker on each of as many SMs first.
-    const int64_t want = p.whole_units ? units : (units * (widest + kUnitCost) - 1) / (kMinTiles + kUnitCost) + 1;
-    p.ctas = static_cast<int>(p.cta_units ? units : std::min<int64_t>(most, std::max<int64_t>(1, want)));
-    p.workers = p.ctas * per_cta;
     p.workers_inv = inverse_of(static_cast<unsigned>(p.workers));
     p.tile_inv = inverse_of(static_cast<unsigned>(p.tile));
     p.per_block_inv = inverse_of(static_cast<unsigned>(p.block / p.piece));

@@ -89,14 +89,20 @@ struct Params {
     int q_vec, o_vec;                           // 8-byte loads of q and stores of the output
 };
 
-// Tokens of a stage for a cache row of `row_bytes`: 8 to 12 KB of cache where a
+// Tokens of a stage for a cache row of `row_bytes`: 6 to 12 KB of cache where a
 // worker is one warp (its ring is a quarter of the CTA's 96 KB), twice that for
 // wider rows where warps share a worker's stages: more independent products a
-// step, fewer hand-overs.
-constexpr int stage_slots(int row_bytes, int mt)
+// step, fewer hand-overs (two tiles of bf16, 192 dims: 571 us with 16 tokens, 542
+// with 32).  Smaller stages leave more of them in flight, but the products less
+// at a time: bf16, 192 dims, 306 us with 16 tokens, 322 with 8; E4M3, 128 dims,
+// 59 with 32, 62 with 16.  Rows of 384 bytes lie between: 742 us with 32 tokens
+// (two stages a worker), 713 with 16; a CTA alone with a unit has few of them
+// (700 tokens 13.5 us with 32, 15.1 with 16).
+constexpr int stage_slots(int row_bytes, int mt, bool alone)
 {
-    const int slots = row_bytes <= 128 ? 64 : row_bytes <= 384 ? 32 : row_bytes <= 768 ? 16 : 8;
-    return mt > 1 && row_bytes > 384 ? 2 * slots : slots;
+    const int middle = alone ? 384 : 256;
+    const int slots = row_bytes <= 128 ? 64 : row_bytes <= middle ? 32 : row_bytes <= 768 ? 16 : 8;
+    return mt > 1 && row_bytes > middle ? 2 * slots : slots;
 }
 
 // CTAs that share an SM.  The products of several tiles of 64 dims gain from a
@@ -137,7 +143,7 @@ struct Shape {
     static constexpr int kElt = FP8 ? 1 : 2;
     static constexpr int kRowBytes = 2 * D * kElt;
     static constexpr int kBands = kRowBytes / 128;
-    static constexpr int kSlots = stage_slots(kRowBytes, MT);
+    static constexpr int kSlots = stage_slots(kRowBytes, MT, ALONE);
     static constexpr int kStageBytes = kSlots * kRowBytes;
     static constexpr int kSteps = D / 16;                       // QK k-steps
     static constexpr int kWorkers = kWarps / MT;                // of a CTA
@@ -1304,14 +1310,13 @@ sda_status launch_shape(const CUtensorMap &tmap, const Params &p, void *stream)
 template <bool FP8, int D, int MT>
 sda_status launch_tiles(const CUtensorMap &tmap, const Params &p, void *stream)
 {
-    const bool full = p.piece == Shape<FP8, D, MT, true>::kSlots;
     if constexpr (Shape<FP8, D, MT, true>::kWorkers > 1) {
         if (p.cta_units)
-            return full ? launch_shape<FP8, D, MT, true, true>(tmap, p, stream)
-                        : launch_shape<FP8, D, MT, false, true>(tmap, p, stream);
+            return p.piece == Shape<FP8, D, MT, true, true>::kSlots ? launch_shape<FP8, D, MT, true, true>(tmap, p, stream)
+                                                                    : launch_shape<FP8, D, MT, false, true>(tmap, p, stream);
     }
-    return full ? launch_shape<FP8, D, MT, true, false>(tmap, p, stream)
-                : launch_shape<FP8, D, MT, false, false>(tmap, p, stream);
+    return p.piece == Shape<FP8, D, MT, true>::kSlots ? launch_shape<FP8, D, MT, true, false>(tmap, p, stream)
+                                                      : launch_shape<FP8, D, MT, false, false>(tmap, p, stream);
 }
 
 template <bool FP8, int D>
