@@ -141,6 +141,10 @@ public:
     void *workspace = nullptr, *stream = nullptr;
     size_t bytes = 0;
 
+    Plain() = default;
+    Plain(const Plain &) = delete;
+    ~Plain() { Py_XDECREF(keep_); }
+
     // args: the entry point's address, the default workspaces by (device, stream),
     // the bytes that the call needs, a workspace or None, then n tensors or None.
     // False: not a plain call, or a Python error is set.
@@ -187,6 +191,7 @@ public:
         Py_XDECREF(key);
         if (!have || !PyTuple_Check(have) || PyTuple_GET_SIZE(have) != 3)
             return false;
+        Py_INCREF(keep_ = have);                // another thread may put a larger one in its place meanwhile
         workspace = PyLong_AsVoidPtr(PyTuple_GET_ITEM(have, 1));
         bytes = PyLong_AsSize_t(PyTuple_GET_ITEM(have, 2));
         const size_t need = PyLong_AsSize_t(args[2]);
@@ -211,6 +216,7 @@ public:
 private:
     sda_tensor d_[11];
     int device_ = -1;
+    PyObject *keep_ = nullptr;
 };
 
 bool as_int(PyObject *x, int &out)

