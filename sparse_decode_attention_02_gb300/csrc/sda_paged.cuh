@@ -174,7 +174,8 @@ struct Shape {
     static constexpr int kHdrOff = kBarOff + 16 * kStages;
     static constexpr int kIssuedOff = kHdrOff + 8 * kStages;
     static constexpr int kCtlOff = (kIssuedOff + 4 * kStages + 15) / 16 * 16;
-    static constexpr int kStateOff = kCtlOff + 16 + 8 * (kThreads + kWarps);
+    static constexpr int kStatsOff = kCtlOff + 16 + 8 * (kThreads + kWarps);    // of a merge: maximum and sum of each row
+    static constexpr int kStateOff = kStatsOff + kWarps * 16 * 8;
     static constexpr int kBytes = kStateOff + kWarps * kStateBytes + 1024;         // + the base's alignment
     static_assert(kPerSm * kWorkers <= 2 * kWarps, "join list");
     static_assert(kStageBytes % 1024 == 0 && kRing >= 2 && kBytes <= 232448 / kPerSm - 1024, "ring");
@@ -187,7 +188,7 @@ struct Segment {
 
 struct Walk {
     long long left;                             // line from the unit's start to the part's end
-    int request, group, tile;                   // (whole_units: units still to take; ALONE: 1 + tiles, if there is a unit)
+    int request, group, tile;                   // (whole_units: units still to take)
 
     static __device__ __forceinline__ int length(const Params &p, int q)
     {
@@ -199,47 +200,34 @@ struct Walk {
         return len > 0 ? static_cast<int>(quotient(len - 1, p.tile_inv)) + 1 : 0;
     }
 
-    template <bool ALONE>
     __device__ __forceinline__ bool next(const Params &p, Segment &s)
     {
-        if constexpr (ALONE) {                  // the share may be empty
+        while (left > 0 && request < p.requests) {
+            const int len = length(p, request), tiles = tiles_of(p, len);
             s.request = request;
             s.group = group;
             s.first = tile;
-            s.last = tile + static_cast<int>(left) - 1;
-            s.len = length(p, request);
-            s.tiles = tiles_of(p, s.len);
-            const bool some = left > 0;
-            left = 0;
-            return some;
-        } else {
-            while (left > 0 && request < p.requests) {
-                const int len = length(p, request), tiles = tiles_of(p, len);
-                s.request = request;
-                s.group = group;
-                s.first = tile;
-                s.tiles = tiles;
-                s.len = len;
-                // a unit's cost comes before its tiles
-                s.last = p.whole_units ? tiles
-                                       : static_cast<int>(max(min(left - kUnitCost, static_cast<long long>(tiles)),
-                                                              static_cast<long long>(tile)));
-                const bool some = s.last > s.first;
-                if (s.last == tiles) {
-                    left -= p.whole_units ? 1 : tiles > 0 ? tiles + kUnitCost : 0;
-                    tile = 0;
-                    if (++group == p.groups || (tiles == 0 && !p.whole_units)) {
-                        group = 0;
-                        ++request;
-                    }
-                } else {
-                    left = 0;
+            s.tiles = tiles;
+            s.len = len;
+            // a unit's cost comes before its tiles
+            s.last = p.whole_units ? tiles
+                                   : static_cast<int>(max(min(left - kUnitCost, static_cast<long long>(tiles)),
+                                                          static_cast<long long>(tile)));
+            const bool some = s.last > s.first;
+            if (s.last == tiles) {
+                left -= p.whole_units ? 1 : tiles > 0 ? tiles + kUnitCost : 0;
+                tile = 0;
+                if (++group == p.groups || (tiles == 0 && !p.whole_units)) {
+                    group = 0;
+                    ++request;
                 }
-                if (some)
-                    return true;
+            } else {
+                left = 0;
             }
-            return false;
+            if (some)
+                return true;
         }
+        return false;
     }
 };
 
@@ -446,18 +434,11 @@ __device__ __forceinline__ long long boundary(const Params &p, long long total, 
 // w * CTAs + CTA, which spreads them over the SMs.  Every thread of the block
 // calls it; a worker's warps look for its part together.
 // `sums`: kThreads + kWarps values of shared memory.
-template <int WORKERS, bool ALONE>
+template <int WORKERS>
 __device__ __forceinline__ Part find_part(const Params &p, long long *sums, int w, long long &total, int &used, int &v)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int spread = w * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
-    if constexpr (ALONE) {
-        const int q = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.groups));
-        const int tiles = Walk::tiles_of(p, Walk::length(p, q));
-        const int first = tiles * w / WORKERS, last = tiles * (w + 1) / WORKERS;
-        total = used = v = 0;
-        return {tiles > 0 ? 1 + last - first : 0, 0, q, static_cast<int>(blockIdx.x) - q * p.groups, first};
-    }
     if (p.whole_units) {
         total = static_cast<long long>(p.requests) * p.groups;
         used = p.workers;
@@ -548,13 +529,12 @@ struct Place {
     long long unit;                             // where the segment's unit begins on the line
 
     // The next segment into seg; a copy of it in `s`.
-    template <bool ALONE>
     __device__ __forceinline__ bool next(const Params &p, long long part_end, Segment &s)
     {
         Walk w = walk;
         __syncwarp();                           // every lane has read it
         unit = part_end - w.left;
-        const bool some = w.next<ALONE>(p, s);
+        const bool some = w.next(p, s);
         walk = w;
         seg = s;
         __syncwarp();
@@ -612,7 +592,10 @@ struct Feed {
         page2 = left2 > 0 && col < p.table_cols ? p.block_table[seg.request * p.bt_s0 + col] : -1;
         tile += n2;
         if (tile >= seg.last) {
-            more = at_line->template next<S::kAlone>(p, 0, seg);
+            if constexpr (S::kAlone)
+                more = false;
+            else
+                more = at_line->next(p, 0, seg);
             tile = seg.first;
         }
     }
@@ -626,7 +609,12 @@ struct Feed {
         lane_stage = lane / per_stage;
         lane_piece = lane - lane_stage * per_stage;
         Segment seg;
-        more = at_line->template next<S::kAlone>(p, 0, seg);
+        if constexpr (S::kAlone) {              // the one that is there; it may be empty
+            seg = at_line->seg;
+            more = seg.last > seg.first;
+        } else {
+            more = at_line->next(p, 0, seg);
+        }
         tile = seg.first;
         n2 = 0;
         look_up(p);                             // the first batch's table entries are on their way
@@ -727,24 +715,34 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL, ALONE>::kPer
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap)) : "memory");
     }
     pdl_launch_dependents();
-    pdl_wait();
     __syncthreads();
+    pdl_wait();
 
-    long long total;
-    int used, v;
-    const Part part = find_part<S::kWorkers, ALONE>(p, sums, worker, total, used, v);
     // What is needed between units only: this warp's place, its feed's, the line.
     WarpState *state = reinterpret_cast<WarpState *>(smem + S::kStateOff) + warp;
-    state->here.walk = state->ahead.walk = {part.left, part.request, part.group, part.tile};
-    state->part_end = part.start + part.left;
-    state->total = total;
-    state->used = used;
-    state->number = v;
+    if constexpr (ALONE) {
+        Segment &seg = state->here.seg;
+        seg.request = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.groups));
+        seg.group = static_cast<int>(blockIdx.x) - seg.request * p.groups;
+        seg.len = Walk::length(p, seg.request);
+        seg.tiles = Walk::tiles_of(p, seg.len);
+        seg.first = seg.tiles * worker / S::kWorkers;
+        seg.last = seg.tiles * (worker + 1) / S::kWorkers;
+    } else {
+        long long total;
+        int used, v;
+        const Part part = find_part<S::kWorkers>(p, sums, worker, total, used, v);
+        state->here.walk = state->ahead.walk = {part.left, part.request, part.group, part.tile};
+        state->part_end = part.start + part.left;
+        state->total = total;
+        state->used = used;
+        state->number = v;
+    }
     __syncwarp();
     Feed<S> feed;
     const Ring place = {sbase, full_bar, hdr, issued};
     if (mt == 0)
-        feed.start(p, &state->ahead, lane);
+        feed.start(p, ALONE ? &state->here : &state->ahead, lane);
 
     const int g = lane >> 2, t = lane & 3;      // fragment row and column pair
     const int H = p.heads, R = p.rows;
@@ -773,13 +771,19 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL, ALONE>::kPer
     uint32_t parity = 0;
     bool dead = false, started = false;
 
-    for (;;) {
+    for (bool more = true; more; more = !ALONE) {
         int common, left;                       // tokens that every row sees, from the segment's first on; its stages
         const uint16_t *q_rows;                 // the unit's first query row
         {
             Segment seg;
-            if (!state->here.template next<ALONE>(p, state->part_end, seg))
-                break;
+            if constexpr (ALONE) {
+                seg = state->here.seg;
+                if (seg.tiles == 0)
+                    break;
+            } else {
+                if (!state->here.next(p, state->part_end, seg))
+                    break;
+            }
             common = seg.len - p.query_len + 1 - seg.first * p.tile;
             left = seg.last - seg.first;
             q_rows = p.query + (static_cast<int64_t>(seg.request) * p.query_len * p.groups + seg.group) * p.q_s0;
@@ -1129,50 +1133,33 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL, ALONE>::kPer
             from_start = x0 <= u0 + kUnitCost;                  // the first worker's piece begins the unit
         }
         if (merged) {
-            // The workers' stages are used up, so the ring can hold their outputs.
-            constexpr int kStride = D + 4;
-            float *outs = reinterpret_cast<float *>(smem), *stats = outs + kWarps * 16 * kStride;
-            static_assert((kWarps * 16 * kStride + kWarps * 32) * 4 <= S::kBarOff, "merge buffer");
-            __syncthreads();
-            if (t == 0) {
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    stats[(warp * 16 + g + 8 * k) * 2] = m_run[k];
-                    stats[(warp * 16 + g + 8 * k) * 2 + 1] = l_run[k];
-                }
-            }
-            __syncthreads();
+            // A worker's stages are used up, so its part of the ring can hold its output.
+            constexpr int kRows = 16 * MT, kOut = S::kRing * S::kStageBytes / 4;       // of a worker
+            constexpr int kStride = kRows * (D + 4) <= kOut ? D + 4 : D;
+            static_assert(kRows * kStride <= kOut, "merge buffer");
+            float *outs = reinterpret_cast<float *>(smem), *stats = reinterpret_cast<float *>(smem + S::kStatsOff);
+            if constexpr (MT > 1)
+                __syncthreads();                // all of the worker's warps are through its last stage
+            else
+                __syncwarp();
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const float *st = stats + (mt * 16 + g + 8 * k) * 2;
-                float M = -INFINITY, L = 0.0f;
-#pragma unroll
-                for (int w = 0; w < S::kWorkers; ++w)
-                    M = fmaxf(M, st[w * MT * 32]);
-#pragma unroll
-                for (int w = 0; w < S::kWorkers; ++w)
-                    L += st[w * MT * 32 + 1] * (st[w * MT * 32] == -INFINITY ? 1.0f : fast_exp2(st[w * MT * 32] - M));
-                const bool empty = M == -INFINITY && L == 0.0f;
-                const int r = k ? r1 : r0;
-                const float lse2 = empty ? -INFINITY : M + log2f(L);
-                if (!ALONE && t == 0 && r < R)
-                    p.part_lse[piece * R + r] = worker > 0 ? -INFINITY : lse2;
-                if (ALONE && t == 0 && r < R && worker == 0 && p.lse)
-                    p.lse[row_of(r) * p.l_s0 + (r % H) * p.l_s1] = lse2 * kLn2;
-                // all of a warp that saw nothing is 0 (or not a number, and stays that)
-                const float f = empty ? 0.0f : (m_run[k] == -INFINITY ? 1.0f : fast_exp2(m_run[k] - M)) / L;
-                float *dst = outs + (warp * 16 + g + 8 * k) * kStride;
+                const int r = 16 * mt + g + 8 * k;              // of the worker
+                // one piece of the CTA's for the join: the first worker's
+                if (!ALONE && worker > 0 && t == 0 && r < R)
+                    p.part_lse[piece * R + r] = -INFINITY;
+                if (t == 0)
+                    *reinterpret_cast<float2 *>(stats + (worker * kRows + r) * 2) = make_float2(m_run[k], l_run[k]);
+                float *dst = outs + worker * kOut + r * kStride;
 #pragma unroll
                 for (int c = 0; c < D / 16; ++c) {
                     if constexpr (FP8) {
                         *reinterpret_cast<float4 *>(dst + 16 * c + 4 * t) =
-                            make_float4(o[2 * c][2 * k] * f, o[2 * c + 1][2 * k] * f, o[2 * c][2 * k + 1] * f,
-                                        o[2 * c + 1][2 * k + 1] * f);
+                            make_float4(o[2 * c][2 * k], o[2 * c + 1][2 * k], o[2 * c][2 * k + 1], o[2 * c + 1][2 * k + 1]);
                     } else {
-                        *reinterpret_cast<float2 *>(dst + 16 * c + 2 * t) =
-                            make_float2(o[2 * c][2 * k] * f, o[2 * c][2 * k + 1] * f);
+                        *reinterpret_cast<float2 *>(dst + 16 * c + 2 * t) = make_float2(o[2 * c][2 * k], o[2 * c][2 * k + 1]);
                         *reinterpret_cast<float2 *>(dst + 16 * c + 8 + 2 * t) =
-                            make_float2(o[2 * c + 1][2 * k] * f, o[2 * c + 1][2 * k + 1] * f);
+                            make_float2(o[2 * c + 1][2 * k], o[2 * c + 1][2 * k + 1]);
                     }
                 }
             }
@@ -1180,16 +1167,35 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL, ALONE>::kPer
             const int64_t first = static_cast<int64_t>(v - worker) * 2 + (from_start ? 1 : 0);
             for (int e = threadIdx.x; e < R * (D / 4); e += kThreads) {
                 const int r = e / (D / 4), d = 4 * (e - r * (D / 4));
-                const float *src = outs + r * kStride + d;      // row r of worker 0: tile r / 16 is warp r / 16
-                float4 x = *reinterpret_cast<const float4 *>(src);
+                float2 st[S::kWorkers];
+                float M = -INFINITY, L = 0.0f;
 #pragma unroll
-                for (int w = 1; w < S::kWorkers; ++w) {
-                    const float4 y = *reinterpret_cast<const float4 *>(src + w * MT * 16 * kStride);
-                    x.x += y.x;
-                    x.y += y.y;
-                    x.z += y.z;
-                    x.w += y.w;
+                for (int w = 0; w < S::kWorkers; ++w) {
+                    st[w] = *reinterpret_cast<const float2 *>(stats + (w * kRows + r) * 2);
+                    M = fmaxf(M, st[w].x);
                 }
+#pragma unroll
+                for (int w = 0; w < S::kWorkers; ++w) {         // all of a worker that saw nothing is 0 (or not a number)
+                    st[w].x = st[w].x == -INFINITY ? 1.0f : fast_exp2(st[w].x - M);
+                    L += st[w].y * st[w].x;
+                }
+                const bool empty = M == -INFINITY && L == 0.0f;
+                const float inv = empty ? 0.0f : 1.0f / L;
+                float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int w = 0; w < S::kWorkers; ++w) {
+                    const float4 y = *reinterpret_cast<const float4 *>(outs + w * kOut + r * kStride + d);
+                    const float f = st[w].x * inv;
+                    x.x += f * y.x;
+                    x.y += f * y.y;
+                    x.z += f * y.z;
+                    x.w += f * y.w;
+                }
+                const float lse2 = empty ? -INFINITY : M + log2f(L);
+                if (!ALONE && d == 0)
+                    p.part_lse[first * R + r] = lse2;
+                if (ALONE && d == 0 && p.lse)
+                    p.lse[row_of(r) * p.l_s0 + (r % H) * p.l_s1] = lse2 * kLn2;
                 if constexpr (!ALONE) {
                     *reinterpret_cast<float4 *>(p.partial + (first * R + r) * D + d) = x;
                     continue;
