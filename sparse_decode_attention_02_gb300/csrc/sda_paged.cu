@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kJoinThreads) sda_paged_join_kernel(const __gr
         auto place = [&](int k) {
             return ((static_cast<int64_t>(item.first) + k) * 2 + (k == 0 ? 1 : 0)) * p.rows + r;
         };
-        const int j = r / H, h = r - j * H;
+        const int j = (r * p.head_inv) >> 16, h = r - j * H;
         const int64_t token = static_cast<int64_t>(item.request) * p.query_len + j;
         const uint16_t *gate = p.gate ? p.gate + token * p.g_s0 + static_cast<int64_t>(item.group * H + h) * p.g_s1 : nullptr;
         const uint16_t gate_bits = gate ? *gate : 0;            // beside what follows
@@ -415,6 +415,7 @@ extern "C" sda_status sparse_decode_paged_attention(const sda_tensor *query, con
     p.requests = static_cast<int>(requests);
     p.groups = static_cast<int>(groups);
     p.heads = static_cast<int>(heads);
+    p.head_inv = (65536 + p.heads - 1) / p.heads;
     p.query_len = query_len;
     p.table_cols = static_cast<int>(block_table->shape[1]);
     p.block = static_cast<int>(block);

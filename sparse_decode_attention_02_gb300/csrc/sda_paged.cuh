@@ -96,6 +96,7 @@ struct Params {
     unsigned long long wait_ns;
     float scale;
     int requests, groups, heads, query_len, rows;   // rows: query_len * heads
+    int head_inv;                               // ceil(2^16 / heads): r * head_inv >> 16 is r / heads for r < 64
     int table_cols, block, cap;                 // cap: tokens the table's width can hold
     int piece, tile;                            // tokens of a TMA box and of a stage
     int ctas, workers, min_tiles, whole_units, cta_units;   // cta_units: ALONE
@@ -243,6 +244,14 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *map
         " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
         : "memory");
+}
+
+// A load that stays where it is written, long before its use.
+__device__ __forceinline__ float load_now(const float *at)
+{
+    float v;
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(at));
+    return v;
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr)
@@ -746,11 +755,12 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL, ALONE>::kPer
 
     const int g = lane >> 2, t = lane & 3;      // fragment row and column pair
     const int H = p.heads, R = p.rows;
-    const float ks = FP8 ? __ldg(p.k_scale) : 1.0f, vs = FP8 ? __ldg(p.v_scale) : 1.0f;
+    const float ks = FP8 ? load_now(p.k_scale) : 1.0f, vs = FP8 ? load_now(p.v_scale) : 1.0f;
+    auto token_of = [&](int r) { return (r * p.head_inv) >> 16; };      // of a query row
 
     const int r0 = 16 * mt + g, r1 = r0 + 8;    // this thread's query rows
     // query token of each row; rows past R repeat the last token's limits
-    const int j0 = min(r0 / H, p.query_len - 1), j1 = min(r1 / H, p.query_len - 1);
+    const int j0 = min(token_of(r0), p.query_len - 1), j1 = min(token_of(r1), p.query_len - 1);
 
     // Shared-memory offsets of this lane's K rows and V rows in a stage.  A
     // stage holds its pieces one after another, each [band][token][128 bytes].
@@ -797,7 +807,8 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL, ALONE>::kPer
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const int r = k ? r1 : r0, rq = r < R ? r : 0;      // rows past R read row 0: zeros in the end
-            const uint16_t *q = q_rows + static_cast<int64_t>(rq / H) * p.groups * p.q_s0 + (rq % H) * p.q_s1 +
+            const int jq = token_of(rq);
+            const uint16_t *q = q_rows + static_cast<int64_t>(jq) * p.groups * p.q_s0 + (rq - jq * H) * p.q_s1 +
                                 (FP8 ? 16 : 8) * t;
             auto dim = [](int kk) { return FP8 ? 64 * (kk >> 2) + 4 * (kk & 3) : 32 * (kk >> 1) + 4 * (kk & 1); };
             if (p.q_vec) {
@@ -1110,7 +1121,7 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL, ALONE>::kPer
         const Segment seg = {at.request, at.group, at.first, at.last, at.tiles, at.len};
         const int v = static_cast<const volatile WarpState *>(state)->number;
         const int64_t out_row0 = static_cast<int64_t>(seg.request) * p.query_len * p.groups + seg.group;
-        auto row_of = [&](int r) { return out_row0 + static_cast<int64_t>(r / H) * p.groups; };
+        auto row_of = [&](int r) { return out_row0 + static_cast<int64_t>(token_of(r)) * p.groups; };
         const bool begins = seg.first == 0, ends = seg.last == seg.tiles;
         const bool whole = begins && ends;
         const int64_t piece = static_cast<int64_t>(v) * 2 + (begins ? 1 : 0);
@@ -1165,8 +1176,10 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL, ALONE>::kPer
             }
             __syncthreads();
             const int64_t first = static_cast<int64_t>(v - worker) * 2 + (from_start ? 1 : 0);
-            for (int e = threadIdx.x; e < R * (D / 4); e += kThreads) {
-                const int r = e / (D / 4), d = 4 * (e - r * (D / 4));
+            // As many threads for a row as there are for 16, or 8, of each tile.
+            const int lg = (MT == 1 ? 3 : 2) + (R <= 8 * MT ? 1 : 0);
+            const int r = static_cast<int>(threadIdx.x) >> lg, c0 = static_cast<int>(threadIdx.x) & ((1 << lg) - 1);
+            if (r < R) {
                 float2 st[S::kWorkers];
                 float M = -INFINITY, L = 0.0f;
 #pragma unroll
@@ -1181,39 +1194,49 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL, ALONE>::kPer
                 }
                 const bool empty = M == -INFINITY && L == 0.0f;
                 const float inv = empty ? 0.0f : 1.0f / L;
-                float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                const int h = r - token_of(r) * H;
+                uint16_t *out = nullptr;
+                float f = 1.0f;
+                if constexpr (ALONE) {
+                    f = vs;
+                    if (p.gate)
+                        f *= gate_factor(p.gate[(static_cast<int64_t>(seg.request) * p.query_len + token_of(r)) * p.g_s0 +
+                                                static_cast<int64_t>(seg.group * H + h) * p.g_s1]);
+                    out = p.output + row_of(r) * p.o_s0 + h * p.o_s1;
+                }
+                float *part = p.partial + (first * R + r) * D;
+#pragma unroll 2
+                for (int d = 4 * c0; d < D; d += 4 << lg) {
+                    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-                for (int w = 0; w < S::kWorkers; ++w) {
-                    const float4 y = *reinterpret_cast<const float4 *>(outs + w * kOut + r * kStride + d);
-                    const float f = st[w].x * inv;
-                    x.x += f * y.x;
-                    x.y += f * y.y;
-                    x.z += f * y.z;
-                    x.w += f * y.w;
+                    for (int w = 0; w < S::kWorkers; ++w) {
+                        const float4 y = *reinterpret_cast<const float4 *>(outs + w * kOut + r * kStride + d);
+                        const float of = st[w].x * inv;
+                        x.x += of * y.x;
+                        x.y += of * y.y;
+                        x.z += of * y.z;
+                        x.w += of * y.w;
+                    }
+                    if constexpr (!ALONE) {
+                        *reinterpret_cast<float4 *>(part + d) = x;
+                    } else {
+                        const uint2 w = make_uint2(pack_bf16(x.x * f, x.y * f), pack_bf16(x.z * f, x.w * f));
+                        if (p.o_vec) {
+                            *reinterpret_cast<uint2 *>(out + d) = w;
+                        } else {
+                            out[d] = static_cast<uint16_t>(w.x);
+                            out[d + 1] = static_cast<uint16_t>(w.x >> 16);
+                            out[d + 2] = static_cast<uint16_t>(w.y);
+                            out[d + 3] = static_cast<uint16_t>(w.y >> 16);
+                        }
+                    }
                 }
-                const float lse2 = empty ? -INFINITY : M + log2f(L);
-                if (!ALONE && d == 0)
-                    p.part_lse[first * R + r] = lse2;
-                if (ALONE && d == 0 && p.lse)
-                    p.lse[row_of(r) * p.l_s0 + (r % H) * p.l_s1] = lse2 * kLn2;
-                if constexpr (!ALONE) {
-                    *reinterpret_cast<float4 *>(p.partial + (first * R + r) * D + d) = x;
-                    continue;
-                }
-                const int h = r % H;
-                float f = vs;
-                if (p.gate)
-                    f *= gate_factor(p.gate[(static_cast<int64_t>(seg.request) * p.query_len + r / H) * p.g_s0 +
-                                            static_cast<int64_t>(seg.group * H + h) * p.g_s1]);
-                uint16_t *out = p.output + row_of(r) * p.o_s0 + h * p.o_s1 + d;
-                const uint2 w = make_uint2(pack_bf16(x.x * f, x.y * f), pack_bf16(x.z * f, x.w * f));
-                if (p.o_vec) {
-                    *reinterpret_cast<uint2 *>(out) = w;
-                } else {
-                    out[0] = static_cast<uint16_t>(w.x);
-                    out[1] = static_cast<uint16_t>(w.x >> 16);
-                    out[2] = static_cast<uint16_t>(w.y);
-                    out[3] = static_cast<uint16_t>(w.y >> 16);
+                if (c0 == 0) {
+                    const float lse2 = empty ? -INFINITY : M + log2f(L);
+                    if (!ALONE)
+                        p.part_lse[first * R + r] = lse2;
+                    else if (p.lse)
+                        p.lse[row_of(r) * p.l_s0 + h * p.l_s1] = lse2 * kLn2;
                 }
             }
         }
@@ -1226,13 +1249,13 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL, ALONE>::kPer
             // only a row that saw nothing is empty: a sum that is not a number goes on
             const bool empty = m_run[k] == -INFINITY && L == 0.0f;
             const float lse2 = empty ? -INFINITY : m_run[k] + log2f(L);
-            const int h = r % H;
+            const int h = r - token_of(r) * H;
             const int64_t row = row_of(r);
             float f = empty ? 0.0f : 1.0f / L;
             if (whole) {
                 f *= vs;
                 if (p.gate)
-                    f *= gate_factor(p.gate[(static_cast<int64_t>(seg.request) * p.query_len + r / H) * p.g_s0 +
+                    f *= gate_factor(p.gate[(static_cast<int64_t>(seg.request) * p.query_len + token_of(r)) * p.g_s0 +
                                             static_cast<int64_t>(seg.group * H + h) * p.g_s1]);
                 if (t == 0 && p.lse)
                     p.lse[row * p.l_s0 + h * p.l_s1] = lse2 * kLn2;
