@@ -1311,22 +1311,24 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL, ALONE>::kPer
         }
     }
 
-    // Requests without tokens: zeros.
-    for (int q = blockIdx.x; q < p.requests; q += gridDim.x) {
-        const int len = Walk::length(p, q);
-        if (threadIdx.x == 0 && p.seq_lens[q * p.len_s] > p.cap)
+    // Requests without tokens: zeros.  A CTA alone with a unit knows its own.
+    for (int q = blockIdx.x; q < (ALONE ? p.requests * p.groups : p.requests); q += gridDim.x) {
+        const int request = ALONE ? state->here.seg.request : q, g0 = ALONE ? state->here.seg.group : 0;
+        const int len = ALONE ? state->here.seg.len : Walk::length(p, q);
+        if (threadIdx.x == 0 && (!ALONE || len == p.cap) && p.seq_lens[request * p.len_s] > p.cap)
             atomicOr(p.flags, SDA_FLAG_BOUNDS);
         if (len != 0)
             continue;
-        for (int gr = warp; gr < p.groups * R; gr += kWarps) {  // [token][group][head]
-            const int h = gr % H;
-            const int64_t row = static_cast<int64_t>(q) * p.query_len * p.groups + gr / H;
-            uint16_t *out = p.output + row * p.o_s0 + h * p.o_s1;
-            for (int d = lane; d < D; d += 32)
-                out[d] = 0;
-            if (lane == 0 && p.lse)
-                p.lse[row * p.l_s0 + h * p.l_s1] = -INFINITY;
-        }
+        for (int gr = warp + g0 * H; gr < (ALONE ? (g0 + 1) * H : p.groups * H); gr += kWarps)          // [group][head]
+            for (int j = 0; j < p.query_len; ++j) {
+                const int h = gr % H;
+                const int64_t row = (static_cast<int64_t>(request) * p.query_len + j) * p.groups + gr / H;
+                uint16_t *out = p.output + row * p.o_s0 + h * p.o_s1;
+                for (int d = lane; d < D; d += 32)
+                    out[d] = 0;
+                if (lane == 0 && p.lse)
+                    p.lse[row * p.l_s0 + h * p.l_s1] = -INFINITY;
+            }
     }
 
     // After a wait that ran out, copies may be in flight: they land before the
