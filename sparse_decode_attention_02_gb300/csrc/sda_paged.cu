@@ -38,10 +38,10 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
-template <int D>
+template <int D, int UNROLL>                    // pieces loaded at a time
 __global__ void __launch_bounds__(kJoinThreads) sda_paged_join_kernel(const __grid_constant__ Params p)
 {
-    constexpr int kVecs = D / 64, kUnroll = 4;  // pairs of dims a lane has; pieces loaded at a time
+    constexpr int kVecs = D / 64;               // pairs of dims a lane has
     __shared__ float2 sums[kJoinWarps][D / 2];
     __shared__ int list_piece[kMaxWorkers], counts[kJoinWarps];
     __shared__ float list_lse[kMaxWorkers];
@@ -118,10 +118,10 @@ __global__ void __launch_bounds__(kJoinThreads) sda_paged_join_kernel(const __gr
             acc[i] = make_float2(0.0f, 0.0f);
         int at = warp;                          // of the list
         while (have != 0 || at < live) {
-            float2 x[kUnroll][kVecs];
-            float w[kUnroll];
+            float2 x[UNROLL][kVecs];
+            float w[UNROLL];
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
+            for (int u = 0; u < UNROLL; ++u) {
                 const bool some = shared ? at < live : have != 0;
                 const int k = !some ? 0 : shared ? list_piece[at] : __ffs(have) - 1;
                 w[u] = shared ? (some ? list_lse[at] : 0.0f) : __shfl_sync(~0u, l, k);
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kJoinThreads) sda_paged_join_kernel(const __gr
                 at += kJoinWarps;
             }
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
+            for (int u = 0; u < UNROLL; ++u) {
                 const float f = exp2f(w[u] - ref);
 #pragma unroll
                 for (int i = 0; i < kVecs; ++i) {
@@ -221,9 +221,9 @@ size_t align256(size_t n)
     return (n + 255) & ~static_cast<size_t>(255);
 }
 
-// A worker takes at least this many tiles before the line is cut finer (one and four:
-// within 5 % either way).
-constexpr int kMinTiles = 2;
+// A worker takes at least this many tiles before the line is cut finer (one request
+// of 1198 tokens x 4 groups: 14.5 us, with two 14.9).
+constexpr int kMinTiles = 1;
 // Units of at most kWholeTiles tiles (by the table's width) are never cut: a worker
 // takes them whole.  A CTA takes a unit alone instead
 //   * from kSharedTiles tiles on (two of E4M3, 128 dims, 32 rows, 64 requests x 2
@@ -440,9 +440,14 @@ extern "C" sda_status sparse_decode_paged_attention(const sda_tensor *query, con
     const int64_t items = units * ((p.rows + kJoinWarps - 1) / kJoinWarps);
     const int64_t rows_to_join = units <= p.workers / kManyPieces ? units * p.rows : items;
     const dim3 grid(static_cast<unsigned>(std::min<int64_t>(4 * sms, rows_to_join)));
-    auto join = dim == 64    ? sda_paged_join_kernel<64>
-                : dim == 128 ? sda_paged_join_kernel<128>
-                : dim == 192 ? sda_paged_join_kernel<192>
-                             : sda_paged_join_kernel<256>;
+    // Eight pieces at a time where each SM has a row at most (one request of 261,001
+    // tokens: 78.7 us with four, 77.4 with eight), four where registers decide how
+    // many rows there are at a time (188 requests of up to 2500: 56.3, 59.9; 256 dims,
+    // 96 rows: 51.1, 52.3).
+    const bool few = units * p.rows <= sms;
+    auto join = dim == 64    ? (few ? sda_paged_join_kernel<64, 8> : sda_paged_join_kernel<64, 4>)
+                : dim == 128 ? (few ? sda_paged_join_kernel<128, 8> : sda_paged_join_kernel<128, 4>)
+                : dim == 192 ? (few ? sda_paged_join_kernel<192, 8> : sda_paged_join_kernel<192, 4>)
+                             : sda_paged_join_kernel<256, 4>;
     return launch_pdl(join, grid, dim3(kJoinThreads), 0, stream, p);
 }
