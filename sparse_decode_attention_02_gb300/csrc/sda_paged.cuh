@@ -25,17 +25,18 @@
 //     and runs ahead over unit boundaries.
 //   * Short units (a table of few tiles) are not put on the line: a worker takes
 //     each whole, or where they are few a CTA does (ALONE), its workers a share of
-//     the tiles each, and merges them itself; nothing is left for the join.
+//     the tiles each, and merges them itself; nothing is left for the join (46
+//     requests of 211 tokens, E4M3: 16.7 us cut and joined, 8.4 alone).
 // Two CTAs of four warps an SM: eight warps leave each thread the registers for
 // a tile's whole Q and output (at 168 registers, with a producer warp, they spilled:
 // the third case below 1296 us).
 //
 // Measured, with a copy at 6.68 TB/s: 64 chats of 8K to 32K tokens (bf16, 192 dims,
-// 2 groups) 305 us, 6.6 TB/s; 12 requests of 64K to 128K with two new tokens (bf16,
-// 192, 4 groups, 32 rows) 534 us, 6.9 TB/s; 16 documents of 128K to 256K (E4M3, 192,
-// 4 groups) 713 us, 7.0 TB/s; one of 261,001 alone 78 us, 5.2 TB/s; 188 of up to 2500
-// tokens over pages of 16 (E4M3, 128, 4 groups) 59 us, 4.3 TB/s, where the start and
-// the join are a third; one of 40 tokens 7.1 us, latency.  E4M3 with 32 rows (192
+// 2 groups) 302 to 308 us, 6.6 TB/s; 12 requests of 64K to 128K with two new tokens (bf16,
+// 192, 4 groups, 32 rows) 534 to 543 us, 6.9 TB/s; 16 documents of 128K to 256K (E4M3, 192,
+// 4 groups) 713 to 724 us, 7.0 TB/s; one of 261,001 alone 78 us, 5.2 TB/s; 188 of up to 2500
+// tokens over pages of 16 (E4M3, 128, 4 groups) 56 us, 4.5 TB/s, where the start and
+// the join are a third; one of 40 tokens 5.0 to 5.6 us, latency.  E4M3 with 32 rows (192
 // dims) reaches 0.6 of the copy rate, with 64 rows 0.34: there the bound is the chain
 // of scores, softmax and products that two warps a scheduler overlap (tensor pipe
 // 49 %).  Halving the conversions there, with weights exchanged between two warps,
@@ -55,8 +56,8 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kMaxRows = 64;                    // query_len * heads
 constexpr int kSms = 152;
 constexpr int kMaxWorkers = kSms * 2 * kWarps;  // two CTAs of them on each SM (or three of two)
-// Tiles that a unit's end is worth on the line (188 requests of up to 2500 tokens: none
-// 76 us, four 59, eight 61).
+// Tiles that a unit's end is worth on the line (188 requests of up to 2500 tokens, then
+// at 59 us with four: none 76, eight 61).
 constexpr int kUnitCost = 4;
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;

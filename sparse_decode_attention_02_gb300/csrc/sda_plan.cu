@@ -12,7 +12,7 @@
 // all lanes, a lane's own only between those two.  Where there is at most a row a
 // thread, each thread finds its own, so that all pages are looked up at once.
 //
-// A decode step is bound by latency: 256 requests 5.1 us in one CTA, of which about
+// A decode step is bound by latency: 256 requests 5.0 us in one CTA, of which about
 // 1 us each the lengths, the sums and the grants (the sums are 32-bit and saturate,
 // divisions by B are multiplications).  Prompts are bound by the 16 bytes written
 // per token row: 4096 of them, 4.2 M rows, 22 us, of which 10 the sums in every CTA
