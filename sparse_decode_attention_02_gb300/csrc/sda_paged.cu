@@ -226,15 +226,15 @@ size_t align256(size_t n)
 constexpr int kMinTiles = 1;
 // Units of at most kWholeTiles tiles (by the table's width) are never cut: a worker
 // takes them whole.  A CTA takes a unit alone instead
-//   * from kSharedTiles tiles on (two of E4M3, 128 dims, 32 rows, 64 requests x 2
-//     groups: 9.0 us shared, 8.4 not);
-//   * up to kAloneTiles tiles a worker (bf16, 192 dims, 2 groups; cut and joined
-//     against alone: 44 tiles, 1 request 15.7, 15.9 us, 76 requests 26.1, 21.0;
-//     94 tiles, 1 request 17.4, 26.9, 76 requests 40.3, 35.0, which lengths that
-//     differ would lose);
-//   * in at most kRounds rounds of CTAs, or one where a worker could take it whole
-//     (10 tiles of E4M3, 128 dims: 1200 units 38.5, 38.5 us, 2400 units 53.5, 71.3).
-constexpr int kWholeTiles = 8, kSharedTiles = 3, kAloneTiles = 12;
+//   * up to kAloneTiles tiles a worker (2 groups; cut and joined against alone: bf16,
+//     192 dims, 63 tiles, 1 request 14.6, 17.6 us, 76 requests 31.9, 24.3; 80 E4M3
+//     requests of 100 to 2300 tokens, 72 tiles, 27.5, 35.5: lengths that differ lose
+//     what equal ones gain);
+//   * in at most kRounds rounds of CTAs (1500 E4M3 requests of up to 900 tokens x 2
+//     groups: 105 us cut, 126 alone), or one where a worker could take it whole (600
+//     bf16 requests of 96 tokens, 192 dims: 21 us whole, 29 alone; 8 of 16 tokens,
+//     in one round: 7.4, 5.8).
+constexpr int kWholeTiles = 8, kAloneTiles = 12;
 constexpr int kRounds = 4;
 
 // CTAs of a launch, at most.
@@ -347,7 +347,7 @@ extern "C" sda_status sparse_decode_paged_attention(const sda_tensor *query, con
         return (p.cap + static_cast<int64_t>(p.tile) - 1) / p.tile;
     };
     int64_t widest = widest_with(true);
-    p.cta_units = per_cta > 1 && widest >= kSharedTiles && widest <= kAloneTiles * per_cta &&
+    p.cta_units = per_cta > 1 && widest <= kAloneTiles * per_cta &&
                   units <= (widest > kWholeTiles ? kRounds : 1) * static_cast<int64_t>(most);
     if (!p.cta_units)
         widest = widest_with(false);
