@@ -347,7 +347,7 @@ extern "C" sda_status sparse_decode_paged_attention(const sda_tensor *query, con
         return (p.cap + static_cast<int64_t>(p.tile) - 1) / p.tile;
     };
     int64_t widest = widest_with(true);
-    p.cta_units = per_cta > 1 && widest <= kAloneTiles * per_cta &&
+    p.cta_units = widest <= kAloneTiles * per_cta &&
                   units <= (widest > kWholeTiles ? kRounds : 1) * static_cast<int64_t>(most);
     if (!p.cta_units)
         widest = widest_with(false);

@@ -1135,7 +1135,8 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL, ALONE>::kPer
         // they are all that its workers have: one piece for the join, not four.
         // The CTA's part of the line lies in the unit, and its first worker has a
         // tile (so every worker comes here once, with this segment).
-        bool merged = ALONE, from_start = false;
+        constexpr bool kShares = ALONE && S::kWorkers > 1;
+        bool merged = kShares, from_start = false;
         if (S::kWorkers > 1 && !ALONE && !whole && state->used == p.workers) {
             const long long n = state->total, u0 = state->here.unit;
             const int w0 = static_cast<int>(blockIdx.x) * S::kWorkers;
@@ -1245,7 +1246,7 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL, ALONE>::kPer
         for (int k = 0; k < 2; ++k) {
             const int r = k ? r1 : r0;
             const float L = l_run[k];
-            if (ALONE || merged || r >= R)
+            if (kShares || merged || r >= R)
                 continue;
             // only a row that saw nothing is empty: a sum that is not a number goes on
             const bool empty = m_run[k] == -INFINITY && L == 0.0f;
@@ -1356,11 +1357,9 @@ sda_status launch_shape(const CUtensorMap &tmap, const Params &p, void *stream)
 template <bool FP8, int D, int MT>
 sda_status launch_tiles(const CUtensorMap &tmap, const Params &p, void *stream)
 {
-    if constexpr (Shape<FP8, D, MT, true>::kWorkers > 1) {
-        if (p.cta_units)
-            return p.piece == Shape<FP8, D, MT, true, true>::kSlots ? launch_shape<FP8, D, MT, true, true>(tmap, p, stream)
-                                                                    : launch_shape<FP8, D, MT, false, true>(tmap, p, stream);
-    }
+    if (p.cta_units)
+        return p.piece == Shape<FP8, D, MT, true, true>::kSlots ? launch_shape<FP8, D, MT, true, true>(tmap, p, stream)
+                                                                : launch_shape<FP8, D, MT, false, true>(tmap, p, stream);
     return p.piece == Shape<FP8, D, MT, true>::kSlots ? launch_shape<FP8, D, MT, true, false>(tmap, p, stream)
                                                       : launch_shape<FP8, D, MT, false, false>(tmap, p, stream);
 }
