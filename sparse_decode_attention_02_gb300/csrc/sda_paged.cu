@@ -229,7 +229,9 @@ constexpr int kMinTiles = 1;
 //   * up to kAloneTiles tiles a worker (2 groups; cut and joined against alone: bf16,
 //     192 dims, 63 tiles, 1 request 14.6, 17.6 us, 76 requests 31.9, 24.3; 80 E4M3
 //     requests of 100 to 2300 tokens, 72 tiles, 27.5, 35.5: lengths that differ lose
-//     what equal ones gain);
+//     what equal ones gain), or twice that with more than 16 query rows, whose
+//     pieces are large, and units for every CTA (E4M3, 192 dims, 64 rows: 400
+//     requests of up to 700 tokens 113.6, 88.9; 80 of 100 to 700 33.6, 41.0);
 //   * in at most kRounds rounds of CTAs (1500 E4M3 requests of up to 900 tokens x 2
 //     groups: 105 us cut, 126 alone), or one where a worker could take it whole (600
 //     bf16 requests of 96 tokens, 192 dims: 21 us whole, 29 alone; 8 of 16 tokens,
@@ -347,7 +349,7 @@ extern "C" sda_status sparse_decode_paged_attention(const sda_tensor *query, con
         return (p.cap + static_cast<int64_t>(p.tile) - 1) / p.tile;
     };
     int64_t widest = widest_with(true);
-    p.cta_units = widest <= kAloneTiles * per_cta &&
+    p.cta_units = widest <= (per_cta < kWarps && units >= most ? 2 : 1) * kAloneTiles * per_cta &&
                   units <= (widest > kWholeTiles ? kRounds : 1) * static_cast<int64_t>(most);
     if (!p.cta_units)
         widest = widest_with(false);

@@ -72,3 +72,14 @@ def test_no_lse_and_unaligned_outputs():
     assert torch.equal(out, want)
     out.fill_(9.0)
     assert (raw == 9.0).all()
+
+
+@pytest.mark.parametrize("n", [303, 304])
+@pytest.mark.parametrize("tiles", [12, 13, 24, 25])
+@pytest.mark.parametrize("ql,workers", [(4, 1), (2, 2)])
+def test_many_query_rows_around_the_rules(n, tiles, ql, workers):
+    """Twice the tiles where there is a unit for every CTA."""
+    r = random.Random(n + tiles)
+    top = tiles * workers * 32
+    lens = [r.choice([0, 1, 33, r.randint(1, 200)]) for _ in range(n - 2)] + [top, top - 1]
+    check(lens, D=128, H=16, ql=ql, G=1, block=32)
