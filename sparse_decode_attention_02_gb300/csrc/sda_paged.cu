@@ -18,7 +18,7 @@ using namespace sda::paged;
 // the batch.  A row of few pieces is one warp's; one of many (a request alone on
 // the GPU leaves a piece per worker) is shared by a block's warps, which add up
 // through shared memory in a fixed order.  It reads each partial once (some MB, in
-// L2) and is bound by latency: about 6 us of the 78 of one long request, 2 of them
+// L2) and is bound by latency: about 6 us of the 77 of one long request, 2 of them
 // the launch.
 // ---------------------------------------------------------------------------
 
@@ -82,9 +82,11 @@ __global__ void __launch_bounds__(kJoinThreads) sda_paged_join_kernel(const __gr
             l = lane < n ? p.part_lse[place(lane)] : -INFINITY;
             have = __ballot_sync(~0u, l != -INFINITY);
         } else {
-            for (int k0 = 0; k0 < n; k0 += kJoinThreads) {
-                const int k = k0 + threadIdx.x;
-                const float x = k < n ? p.part_lse[place(k)] : -INFINITY;
+            auto lse_of = [&](int k) { return k < n ? p.part_lse[place(k)] : -INFINITY; };
+            const int k1 = static_cast<int>(threadIdx.x);
+            float next_x = lse_of(k1 + kJoinThreads), x = lse_of(k1);     // a turn ahead
+            for (int k0 = 0; k0 < n; k0 += kJoinThreads, x = next_x, next_x = lse_of(k1 + k0 + kJoinThreads)) {
+                const int k = k0 + k1;
                 const unsigned some = __ballot_sync(~0u, x != -INFINITY);
                 __syncthreads();                // the list and counts of the last round, or item, have been read
                 if (lane == 0)
