@@ -457,16 +457,15 @@ __device__ __forceinline__ Part find_part(const Params &p, long long *sums, int 
         const unsigned q = static_cast<unsigned>(u0) / static_cast<unsigned>(p.groups);
         return {boundary(p, total, v + 1) - u0, 0, static_cast<int>(q), static_cast<int>(u0 - q * p.groups), 0};
     }
-    // Spans of the requests on the line, of one group each; a thread sums a run of them.
+    // Spans of the requests on the line, of one group each; a thread sums a run of
+    // them, or a lane has one where a warp has them all and needs no other.
+    const bool few = p.requests <= 32;
     const int per = (p.requests + kThreads - 1) / kThreads;
     const int q0 = min(p.requests, static_cast<int>(threadIdx.x) * per), q1 = min(p.requests, q0 + per);
     auto span = [&](int q) -> long long {
         const int tiles = Walk::tiles_of(p, Walk::length(p, q));
         return tiles > 0 ? tiles + kUnitCost : 0;
     };
-    long long mine = 0;
-    for (int q = q0; q < q1; ++q)
-        mine += span(q);
     auto scan = [&](long long x) {              // inclusive, over the warp
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -475,16 +474,24 @@ __device__ __forceinline__ Part find_part(const Params &p, long long *sums, int 
         }
         return x;
     };
-    const long long inc = scan(mine);
-    sums[threadIdx.x] = inc - mine;             // before the thread's run, in its warp
-    if (lane == 31)
-        sums[kThreads + warp] = inc;
-    __syncthreads();
-    long long warp_sum[kWarps], all = 0;
+    long long mine = 0, inc, warp_sum[kWarps] = {}, all = 0;
+    if (few) {
+        mine = lane < p.requests ? span(lane) : 0;
+        inc = scan(mine);
+        all = __shfl_sync(~0u, inc, 31);
+    } else {
+        for (int q = q0; q < q1; ++q)
+            mine += span(q);
+        inc = scan(mine);
+        sums[threadIdx.x] = inc - mine;         // before the thread's run, in its warp
+        if (lane == 31)
+            sums[kThreads + warp] = inc;
+        __syncthreads();
 #pragma unroll
-    for (int k = 0; k < kWarps; ++k) {
-        warp_sum[k] = all;
-        all += sums[kThreads + k];
+        for (int k = 0; k < kWarps; ++k) {
+            warp_sum[k] = all;
+            all += sums[kThreads + k];
+        }
     }
     total = all * p.groups;
     const int least = p.min_tiles + kUnitCost;
@@ -497,33 +504,41 @@ __device__ __forceinline__ Part find_part(const Params &p, long long *sums, int 
     const long long x = used == p.workers ? boundary(p, total, v) : shorter * static_cast<unsigned>(v) / used;
     const long long x1 = used == p.workers ? boundary(p, total, v + 1) : shorter * static_cast<unsigned>(v + 1) / used;
 
-    // The run that x lies in: the last that begins at or before it.
-    int run = -1;
+    int q = 0;
+    long long at = 0, len = 0;
+    if (few) {
+        const int l = __ffs(__ballot_sync(~0u, inc * p.groups > x)) - 1;        // x is on the line
+        len = __shfl_sync(~0u, mine, l);
+        at = __shfl_sync(~0u, (inc - mine) * p.groups, l);
+        q = l;
+    } else {
+        // The run that x lies in: the last that begins at or before it.
+        int run = -1;
 #pragma unroll
-    for (int k = 0; k < kWarps; ++k)
-        run += __popc(__ballot_sync(~0u, (warp_sum[k] + sums[32 * k + lane]) * p.groups <= x));
-    // The request in the run, 32 at a time; requests without tokens span nothing.
-    long long at = warp_sum[0];
+        for (int k = 0; k < kWarps; ++k)
+            run += __popc(__ballot_sync(~0u, (warp_sum[k] + sums[32 * k + lane]) * p.groups <= x));
+        // The request in the run, 32 at a time; requests without tokens span nothing.
+        at = warp_sum[0];
 #pragma unroll
-    for (int k = 1; k < kWarps; ++k)
-        at = run >= 32 * k ? warp_sum[k] : at;
-    at = (at + sums[run]) * p.groups;
-    int q = run * per;
-    long long len = 0;
-    for (;; q += 32) {
-        const long long s = q + lane < p.requests ? span(q + lane) : 0;
-        const long long to = scan(s) * p.groups;                        // past each request
-        const unsigned past = __ballot_sync(~0u, at + to > x);
-        if (past) {
-            const int l = __ffs(past) - 1;
-            len = __shfl_sync(~0u, s, l);
-            at += __shfl_sync(~0u, to, l) - len * p.groups;
-            q += l;
-            break;
+        for (int k = 1; k < kWarps; ++k)
+            at = run >= 32 * k ? warp_sum[k] : at;
+        at = (at + sums[run]) * p.groups;
+        q = run * per;
+        for (;; q += 32) {
+            const long long s = q + lane < p.requests ? span(q + lane) : 0;
+            const long long to = scan(s) * p.groups;                        // past each request
+            const unsigned past = __ballot_sync(~0u, at + to > x);
+            if (past) {
+                const int l = __ffs(past) - 1;
+                len = __shfl_sync(~0u, s, l);
+                at += __shfl_sync(~0u, to, l) - len * p.groups;
+                q += l;
+                break;
+            }
+            if (q + 32 >= p.requests)                                       // not reached: x is on the line
+                return {0, 0, 0, 0, 0};
+            at += __shfl_sync(~0u, to, 31);
         }
-        if (q + 32 >= p.requests)                                       // not reached: x is on the line
-            return {0, 0, 0, 0, 0};
-        at += __shfl_sync(~0u, to, 31);
     }
     const unsigned long long in = x - at;
     const int g = static_cast<int>(in >> 32 || len >> 32 ? in / len : static_cast<unsigned>(in) / static_cast<unsigned>(len));
