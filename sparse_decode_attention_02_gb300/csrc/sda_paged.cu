@@ -18,7 +18,7 @@ using namespace sda::paged;
 // the batch.  A row of few pieces is one warp's; one of many (a request alone on
 // the GPU leaves a piece per worker) is shared by a block's warps, which add up
 // through shared memory in a fixed order.  It reads each partial once (some MB, in
-// L2) and is bound by latency: about 6 us of the 77 of one long request, 2 of them
+// L2) and is bound by latency: about 6 us of the 76 of one long request, 2 of them
 // the launch.
 // ---------------------------------------------------------------------------
 

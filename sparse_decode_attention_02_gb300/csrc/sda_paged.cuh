@@ -34,8 +34,8 @@
 // Measured, with a copy at 6.68 TB/s: 64 chats of 8K to 32K tokens (bf16, 192 dims,
 // 2 groups) 302 to 308 us, 6.6 TB/s; 12 requests of 64K to 128K with two new tokens (bf16,
 // 192, 4 groups, 32 rows) 534 to 543 us, 6.9 TB/s; 16 documents of 128K to 256K (E4M3, 192,
-// 4 groups) 713 to 724 us, 7.0 TB/s; one of 261,001 alone 77 us, 5.2 TB/s; 188 of up to 2500
-// tokens over pages of 16 (E4M3, 128, 4 groups) 56 us, 4.5 TB/s, where the start and
+// 4 groups) 713 to 724 us, 7.0 TB/s; one of 261,001 alone 76 us, 5.3 TB/s; 188 of up to 2500
+// tokens over pages of 16 (E4M3, 128, 4 groups) 57 us, 4.5 TB/s, where the start and
 // the join are a third; one of 40 tokens 5.0 to 5.6 us, latency.  E4M3 with 32 rows (192
 // dims) reaches 0.6 of the copy rate, with 64 rows 0.34: there the bound is the chain
 // of scores, softmax and products that two warps a scheduler overlap (tensor pipe
