@@ -29,6 +29,8 @@ constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxRequests = 8192;              // six int32 arrays of them in shared memory: 192 KB
 constexpr int kArrays = 6;
+constexpr size_t kOwnShared = 1024;             // at least the kernel's other shared memory (784 bytes)
+constexpr size_t kUsualShared = 48 * 1024;      // what a kernel may use in all before its limit is raised
 constexpr int kQuad = 4;                        // consecutive token rows a thread writes at a time
 constexpr int kWarpRows = 32 * kQuad;           // rows of a warp's turn
 constexpr uint32_t kMostSum = 0x7FFFFFFFu;      // sums stay here: beyond any count of pages or rows
@@ -143,6 +145,7 @@ __global__ void __launch_bounds__(kThreads) sda_plan_kernel(const __grid_constan
     __shared__ Sums warp_sums[2][kWarps];
     __shared__ int granted[3];                  // token rows, pages taken, pages returned
     __shared__ int is_last;
+    static_assert(sizeof warp_sums + sizeof granted + sizeof is_last <= kOwnShared, "shared memory");
 
     pdl_launch_dependents();
     pdl_wait();
@@ -490,7 +493,7 @@ extern "C" sda_status sparse_decode_plan_step(const sda_tensor *context_lens, co
 
     const size_t smem = kArrays * sizeof(int32_t) * static_cast<size_t>(Q);
     static size_t raised[64] = {};
-    if (smem > 48 * 1024 && !raise_smem(sda_plan_kernel, kArrays * sizeof(int32_t) * kMaxRequests, raised))
+    if (smem + kOwnShared > kUsualShared && !raise_smem(sda_plan_kernel, kArrays * sizeof(int32_t) * kMaxRequests, raised))
         return SDA_ERR_CUDA;
     const int sms = sm_count();
     if (sms < 1)
