@@ -463,8 +463,9 @@ def sparse_decode_rope_append(query, key, value, positions, inv_freq, slots, cac
     pairs of each axis.  `k_scale` / `v_scale`: as in sparse_decode_attention.
     Returns `query_out`."""
     lib = _lib or load()
-    if query is not None and query_out is None:
-        query_out = torch.zeros_like(query) if slots is not None else torch.empty_like(query)
+    if query is not None and query_out is None:             # padding rows of it are zeros
+        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+            query_out = torch.zeros_like(query) if slots is not None else torch.empty_like(query)
     if key is None:
         cache = None
     if sections is not None and (positions is None or len(sections) != positions.shape[0] or len(sections) > 4):
