@@ -47,6 +47,7 @@
 #include <cstdint>
 #include <mutex>
 
+#include "sda_context.cuh"
 #include "sdattn.h"
 
 // The process-wide limit of the kernels' pipeline waits (set with
@@ -1170,9 +1171,10 @@ sda_status launch_tc(const sda_tensor *query, const sda_tensor *summaries, const
         const cuuint64_t gstride[4] = {static_cast<cuuint64_t>(ip.m_s0), 128u, static_cast<cuuint64_t>(kIdxDim),
                                        static_cast<cuuint64_t>(ip.m_s0) * static_cast<cuuint64_t>(per_page)};
         const cuuint32_t box[5] = {128u, 8u, 2u, static_cast<cuuint32_t>(gblock), 1u};
-        if (encode(&smap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void *>(summaries->data), gdim, gstride,
-                   box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        if (sda::with_context(encode, &smap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void *>(summaries->data),
+                              gdim, gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return SDA_ERR_UNSUPPORTED;
     }
     // queries as (128-byte K chunk, K half, head, group, token): one box per K half
@@ -1184,9 +1186,9 @@ sda_status launch_tc(const sda_tensor *query, const sda_tensor *summaries, const
                                        static_cast<cuuint64_t>(ip.q_s0)};
         const cuuint32_t box[5] = {128u, 1u, static_cast<cuuint32_t>(kIdxHeads), static_cast<cuuint32_t>(gblock),
                                    static_cast<cuuint32_t>(query_len)};
-        if (encode(&qmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void *>(query->data), gdim, gstride, box,
-                   estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        if (sda::with_context(encode, &qmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void *>(query->data), gdim,
+                              gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return SDA_ERR_UNSUPPORTED;
     }
     IndexTcParams tp;

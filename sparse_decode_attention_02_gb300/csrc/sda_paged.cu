@@ -1,5 +1,6 @@
 // Host side of the paged attention, and the kernel that joins the pieces of a
 // request that several CTAs computed.
+#include "sda_context.cuh"
 #include "sda_paged.cuh"
 
 #include <cmath>
@@ -379,10 +380,10 @@ extern "C" sda_status sparse_decode_paged_attention(const sda_tensor *query, con
     const cuuint32_t box[5] = {static_cast<cuuint32_t>(128 / elt), static_cast<cuuint32_t>(p.piece),
                                static_cast<cuuint32_t>(bands), 1, 1};
     const cuuint32_t estride[5] = {1, 1, 1, 1, 1};
-    if (encode(&tmap, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
-               const_cast<void *>(cache->data), gdim, gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    if (with_context(encode, &tmap, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
+                     const_cast<void *>(cache->data), gdim, gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return SDA_ERR_UNSUPPORTED;
 
     p.query = static_cast<const uint16_t *>(query->data);
