@@ -9,11 +9,14 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <mutex>
 
 #include "sdattn.h"
 
-// Defined in sdattn.cu: the limit set by sparse_decode_set_wait_limit_ns.
+// Defined in sdattn.cu: the limit set by sparse_decode_set_wait_limit_ns, and what
+// keeps a call's launches on one workspace together.
 uint64_t sda_wait_limit_ns();
+std::mutex &sda_launch_mutex(const void *workspace);
 
 namespace sda {
 

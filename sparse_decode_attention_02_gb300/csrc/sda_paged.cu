@@ -438,6 +438,8 @@ extern "C" sda_status sparse_decode_paged_attention(const sda_tensor *query, con
                      : dim == 128 ? (fp8 ? launch_fp8_128 : launch_bf16_128)
                      : dim == 192 ? (fp8 ? launch_fp8_192 : launch_bf16_192)
                                   : (fp8 ? launch_fp8_256 : launch_bf16_256);
+    // The split kernel leaves its list and pieces in the workspace, the join empties it.
+    const std::lock_guard<std::mutex> together(sda_launch_mutex(workspace));
     const sda_status st = launch(tmap, p, stream);
     if (st != SDA_OK || p.whole_units || p.cta_units)
         return st;

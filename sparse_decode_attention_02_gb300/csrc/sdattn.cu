@@ -1290,6 +1290,16 @@ __attribute__((visibility("hidden"))) uint64_t sda_wait_limit_ns()
     return g_wait_ns.load();
 }
 
+// Held over the launches of one call that pass something on in `workspace`.
+// Calls on one stream may share a workspace, also from several host threads: without
+// it, another call's launches could come between these.  Workspaces that share a
+// mutex wait for one another's launches (some us), no more.
+__attribute__((visibility("hidden"))) std::mutex &sda_launch_mutex(const void *workspace)
+{
+    static std::mutex mutexes[64];
+    return mutexes[reinterpret_cast<uintptr_t>(workspace) / 256 % 64];
+}
+
 extern "C" {
 
 int sparse_decode_splits(int rows)
