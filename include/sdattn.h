@@ -20,6 +20,8 @@
  *     are valid once the stream has reached that point.
  *   - Inputs are read only; only `output` and `workspace` are written, and
  *     neither may overlap an input.
+ *   - Host threads may call at the same time.  On one stream they may also pass
+ *     the same workspace: the launches of a call stay together.
  */
 #ifndef SDATTN_H
 #define SDATTN_H

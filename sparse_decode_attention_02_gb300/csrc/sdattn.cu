@@ -1563,6 +1563,10 @@ sda_status run_call(const Call &c, bool check_only = false)
 
     cudaStream_t s = static_cast<cudaStream_t>(c.stream);
     const int nr = windowed ? 0 : prm.num_regions;
+    // With splits the combine kernel reads what the split kernel leaves in the workspace.
+    std::unique_lock<std::mutex> together;
+    if (c.splits > 1)
+        together = std::unique_lock<std::mutex>(sda_launch_mutex(c.workspace));
     const bool full = piece == stage_tokens;
     // Window rows come in token pairs of one request (query_len even): one CTA
     // streams (its split's share of) the pair's union window once.
