@@ -187,6 +187,12 @@ def _current(dev: torch.device):
     return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
 
 
+def _on(stream: torch.cuda.Stream | None):
+    """Makes `stream` the current one, if given: what a call allocates and fills belongs to
+    the stream that it runs on."""
+    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+
+
 def sparse_decode_splits(rows: int) -> int:
     return load().sparse_decode_splits(int(rows))
 
@@ -206,16 +212,18 @@ def default_workspace(device: torch.device, nbytes: int, stream: torch.cuda.Stre
     key = (device, handle)
     ws = _workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
-        ws = torch.zeros(max(nbytes, 1 << 12), dtype=torch.uint8, device=device)
+        with _on(stream):
+            ws = torch.zeros(max(nbytes, 1 << 12), dtype=torch.uint8, device=device)
         _workspaces[key] = ws
     return ws
 
 
-def _scale_ptr(x, device):
+def _scale_ptr(x, device, stream):
     if x is None:
         return None, None
     if not isinstance(x, torch.Tensor):
-        x = torch.tensor([float(x)], dtype=torch.float32, device=device)
+        with _on(stream):
+            x = torch.tensor([float(x)], dtype=torch.float32, device=device)
     if x.dtype != torch.float32 or x.device != device or x.numel() != 1:
         raise ValueError("k_scale / v_scale must be one-element float32 tensors on the query's device")
     return x.data_ptr(), x
@@ -239,8 +247,8 @@ def sparse_decode_attention(query, cache, regions, block_table, positions, activ
     need = lib.sparse_decode_workspace_bytes(rows, heads, splits)
     if workspace is None:
         workspace = default_workspace(dev, need, stream)
-    ks, _keep_k = _scale_ptr(k_scale, dev)
-    vs, _keep_v = _scale_ptr(v_scale, dev)
+    ks, _keep_k = _scale_ptr(k_scale, dev, stream)
+    vs, _keep_v = _scale_ptr(v_scale, dev, stream)
     descs = [describe(x) for x in (query, cache, regions, block_table, positions, active, output)]
     gd = describe(gate)
     s = stream if stream is not None else torch.cuda.current_stream(dev)
@@ -273,8 +281,8 @@ def sparse_decode_swa_attention(query, cache, block_table, seq_lens, output, *, 
     need = lib.sparse_decode_workspace_bytes(rows, heads, splits)
     if workspace is None:
         workspace = default_workspace(dev, need, stream)
-    ks, _keep_k = _scale_ptr(k_scale, dev)
-    vs, _keep_v = _scale_ptr(v_scale, dev)
+    ks, _keep_k = _scale_ptr(k_scale, dev, stream)
+    vs, _keep_v = _scale_ptr(v_scale, dev, stream)
     descs = [describe(x) for x in (query, cache, block_table, seq_lens, output)]
     gd = describe(gate)
     s = stream if stream is not None else torch.cuda.current_stream(dev)
@@ -293,7 +301,8 @@ def sparse_decode_select_regions(scores, current, topk: int, regions=None, *, to
     lib = load()
     dev = _device_of(scores, current, topk_lengths, regions, stream=stream)
     if regions is None:
-        regions = torch.empty((scores.shape[0], int(topk)), dtype=torch.int32, device=dev)
+        with _on(stream):
+            regions = torch.empty((scores.shape[0], int(topk)), dtype=torch.int32, device=dev)
     s = stream if stream is not None else torch.cuda.current_stream(dev)
     d = [describe(x) for x in (scores, current, topk_lengths, regions)]
     with _current(dev):
@@ -319,7 +328,8 @@ def sparse_decode_summary_scores(query, weights, summaries, block_table, seq_len
     if scores is None:
         if n_cols is None:
             n_cols = block_table.shape[1] * int(block_size) // 8
-        scores = torch.empty((rows, int(n_cols)), dtype=torch.float32, device=dev)
+        with _on(stream):
+            scores = torch.empty((rows, int(n_cols)), dtype=torch.float32, device=dev)
     s = stream if stream is not None else torch.cuda.current_stream(dev)
     d = [describe(x) for x in (query, weights, summaries, block_table, seq_lens, scores, current, lengths)]
     ws = workspace.data_ptr() if workspace is not None else None
@@ -430,7 +440,7 @@ def sparse_decode_plan_step(context_lens, new_lens, free_pages, free_state, bloc
     requests, free_next)."""
     lib = _lib or load()
     if positions is None or requests is None or seq_lens is None or token_starts is None or free_next is None:
-        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+        with _on(stream):
             new = lambda t, n: torch.empty(n, dtype=torch.int32, device=slots.device) if t is None else t
             positions, requests = new(positions, slots.shape[0]), new(requests, slots.shape[0])
             seq_lens, token_starts = new(seq_lens, context_lens.shape[0]), new(token_starts, context_lens.shape[0] + 1)
@@ -464,7 +474,7 @@ def sparse_decode_rope_append(query, key, value, positions, inv_freq, slots, cac
     Returns `query_out`."""
     lib = _lib or load()
     if query is not None and query_out is None:             # padding rows of it are zeros
-        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+        with _on(stream):
             query_out = torch.zeros_like(query) if slots is not None else torch.empty_like(query)
     if key is None:
         cache = None
@@ -563,8 +573,8 @@ def sparse_decode_attention_no_alloc(query, cache, regions, block_table, positio
     rows = query.shape[0]
     if splits is None:
         splits = lib.sparse_decode_splits(rows)
-    ks, _keep_k = _scale_ptr(k_scale, dev)
-    vs, _keep_v = _scale_ptr(v_scale, dev)
+    ks, _keep_k = _scale_ptr(k_scale, dev, stream)
+    vs, _keep_v = _scale_ptr(v_scale, dev, stream)
     descs = [describe(x) for x in (query, cache, regions, block_table, positions, active, output)]
     gd = describe(gate)
     s = stream if stream is not None else torch.cuda.current_stream(dev)

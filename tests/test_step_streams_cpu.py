@@ -57,3 +57,50 @@ def test_step_tables_are_made_on_the_calls_stream(made):
     stream = Stream()
     sda.sparse_decode_plan_step(n, n, n, n, n[None], block_size=16, slots=slots, stream=stream)
     assert made and all(s is stream for _, s in made), made
+
+
+def on_the_gpu(monkeypatch, lib_calls):
+    """Lets host tensors through the older entries up to the library, whose entries `lib_calls` succeed."""
+    class Lib:
+        def __getattr__(self, name):
+            return (lambda *a: 0) if name in lib_calls else getattr(B._lib, name)
+
+    lib = Lib()
+    monkeypatch.setattr(B, "load", lambda: lib)
+    monkeypatch.setattr(B, "_device_of", lambda *t, stream=None: torch.device("cpu"))
+    monkeypatch.setattr(B, "_current", lambda dev: contextlib.nullcontext())
+
+
+def test_default_workspaces_are_made_on_their_stream(made, monkeypatch):
+    monkeypatch.setattr(B, "_workspaces", {})
+    made.clear()
+    stream = Stream()
+    ws = B.default_workspace("cpu", 300, stream)
+    assert ws.numel() >= 300 and not ws.any() and made and all(s is stream for _, s in made), made
+
+
+@pytest.mark.parametrize("name,call", [
+    ("sparse_decode_select_regions", lambda s: sda.sparse_decode_select_regions(torch.ones(2, 9), torch.ones(2), 4, stream=s)),
+    ("sparse_decode_summary_scores",
+     lambda s: sda.sparse_decode_summary_scores(torch.ones(2, 1, 8, 256, dtype=torch.uint8), torch.ones(2, 1, 8),
+                                                torch.ones(2, 1, 256, dtype=torch.uint8), torch.ones(2, 3, dtype=torch.int32),
+                                                torch.ones(2, dtype=torch.int32), block_size=16, stream=s))])
+def test_outputs_of_the_selection_are_made_on_the_calls_stream(made, monkeypatch, name, call):
+    on_the_gpu(monkeypatch, {name})
+    plain = torch.ones
+    made.clear()
+    stream = Stream()
+    call(stream)
+    assert plain is torch.ones and made and all(s is stream for _, s in made), made
+
+
+def test_uploaded_scales_belong_to_the_calls_stream(made, monkeypatch):
+    on_the_gpu(monkeypatch, {"sparse_decode_attention"})
+    q, i32 = torch.ones(1, 1, 192, dtype=torch.bfloat16), torch.ones(1, 1, dtype=torch.int32)
+    cache = torch.ones(1, 1, 16, 384, dtype=torch.uint8)
+    ws = torch.ones(1 << 12, dtype=torch.uint8)
+    made.clear()
+    stream = Stream()
+    sda.sparse_decode_attention(q, cache, i32, i32, i32[0], i32[0] > 0, q.clone(), scale=0.1, splits=1, k_scale=0.5,
+                                v_scale=0.25, workspace=ws, stream=stream)
+    assert len(made) == 2 and all(s is stream for _, s in made), made
