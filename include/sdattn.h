@@ -409,7 +409,9 @@ size_t sparse_decode_paged_workspace_bytes(int heads, int query_len, int head_di
  * the lengths, on the device, so the call can be captured in a graph; the
  * pieces of a request are joined by their log-sum-exps in a fixed order, so
  * equal inputs give equal bits.  What masked or unused cache places hold (NaN
- * included) does not reach the output.  A length past the table (W * B) or a
+ * included) does not reach the output.  An infinite value in V gives the rows
+ * that see it an infinity of its sign, NaN where they see both signs or where
+ * its weight underflows.  A length past the table (W * B) or a
  * table entry outside the cache raises SDA_FLAG_BOUNDS and is left out.
  * Errors as for sparse_decode_attention.
  */

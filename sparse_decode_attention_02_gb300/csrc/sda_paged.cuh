@@ -318,16 +318,23 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t sel)
     return r;
 }
 
-template <bool FP8>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+// Two fp32 values to packed fp16 (round to nearest even), `lo` in the low half.
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
 {
-    if constexpr (FP8) {
-        uint32_t r;
-        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-        return r;
-    } else {
-        return pack_bf16(lo, hi);
-    }
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Two weights, >= 0, as the sum of two bf16 values each: the largest bf16 below the
+// weight, and the rest, rounded (16 bits in all).  Both are above 0 unless the
+// weight is 0, so that an infinite V keeps its sign in both products (a rest of 0 or
+// of the other sign would make it NaN).
+__device__ __forceinline__ void split_bf16(float lo, float hi, uint32_t &most, uint32_t &rest)
+{
+    const uint32_t a = max(__float_as_uint(lo), 1u) - 1u, b = max(__float_as_uint(hi), 1u) - 1u;
+    asm("prmt.b32 %0, %1, %2, 0x7632;" : "=r"(most) : "r"(a), "r"(b));
+    rest = pack_bf16(lo - __uint_as_float(a & 0xFFFF0000u), hi - __uint_as_float(b & 0xFFFF0000u));
 }
 
 __device__ __forceinline__ float fast_exp2(float x)
@@ -359,8 +366,8 @@ __device__ __forceinline__ uint64_t low_bits(int n)
 
 // O[16 x D] += P[16 x 16 slots] V[16 slots x D].  `vrow`: this lane's V row for
 // ldmatrix (k-slot (mi & 1) * 8 + lane % 8, of the chunk pair's chunk mi >> 1),
-// `vsw` its swizzle phase.  bf16: P comes as a rounded part and the rest, so
-// that its products carry 16 bits of it.  MASKED zeroes V of slots out of the
+// `vsw` its swizzle phase.  bf16: P comes in two parts (split_bf16), so that its
+// products carry 16 bits of it.  MASKED zeroes V of slots out of the
 // mask (vm0: k-slots 2t, 2t + 1; vm1: 8 + 2t, 9 + 2t), whatever they hold.
 template <bool FP8, int D, bool MASKED>
 __device__ __forceinline__ void pv_accumulate(float (&o)[D / 8][4], const uint32_t (&pa)[4],
@@ -875,8 +882,8 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL, ALONE>::kPer
                 for (int kk = 0; kk < S::kSteps; ++kk)
 #pragma unroll
                     for (int i = k; i < 4; i += 2)
-                        qf[kk][i] = pack2<true>(__uint_as_float(qf[kk][i] << 16) * up,
-                                                __uint_as_float(qf[kk][i] & 0xFFFF0000u) * up);
+                        qf[kk][i] = pack_f16(__uint_as_float(qf[kk][i] << 16) * up,
+                                             __uint_as_float(qf[kk][i] & 0xFFFF0000u) * up);
             }
         }
 
@@ -1010,9 +1017,8 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL, ALONE>::kPer
                     l_run[1] += sc[i][2] + sc[i][3];
                 }
 
-                // ---- O += P V.  P in 11 bits (fp16, next to E4M3 values' 4), or
-                // bf16 twice: rounded, and what the rounding left.  Tokens that
-                // only some rows see come below.
+                // ---- O += P V.  P in 11 bits (fp16, next to E4M3 values' 4), or in
+                // two bf16 parts.  Tokens that only some rows see come below.
                 const uint64_t seen = kPlain ? kAll : loaded & low_bits(common);
                 auto both = [&](uint32_t km, int s) {           // V words of slots s, s + 4
                     return (((km >> s) & 1u) ? 0x0000FFFFu : 0u) | (((km >> (s + 4)) & 1u) ? 0xFFFF0000u : 0u);
@@ -1027,8 +1033,7 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL, ALONE>::kPer
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
                             const float lo = weight(0, 2 * k, km, 0), hi = weight(0, 2 * k + 1, km, 0);
-                            pa[k] = pack_bf16(lo, hi);
-                            pb[k] = pack_bf16(lo - __uint_as_float(pa[k] << 16), hi - __uint_as_float(pa[k] & 0xFFFF0000u));
+                            split_bf16(lo, hi, pa[k], pb[k]);
                         }
                         pv_accumulate8<D, !kPlain>(o, pa, pb, sb + vsw * 128u, bstride, mi, vsw, both(km, t));
                     }
@@ -1043,9 +1048,10 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL, ALONE>::kPer
                     for (int k = 0; k < 4; ++k) {
                         const int i = 2 * k2 + (k >> 1), c = 2 * (k & 1);
                         const float lo = weight(i, c, km, 8 * (k >> 1)), hi = weight(i, c + 1, km, 8 * (k >> 1));
-                        pa[k] = pack2<FP8>(lo, hi);
-                        if constexpr (!FP8)
-                            pb[k] = pack_bf16(lo - __uint_as_float(pa[k] << 16), hi - __uint_as_float(pa[k] & 0xFFFF0000u));
+                        if constexpr (FP8)
+                            pa[k] = pack_f16(lo, hi);
+                        else
+                            split_bf16(lo, hi, pa[k], pb[k]);
                     }
                     const uint32_t vrow = sb + ((mi & 1) ? tile_off[2 * k2 + 1] : tile_off[2 * k2]) + vsw * 128u;
                     pv_accumulate<FP8, D, !kPlain>(o, pa, pb, vrow, bstride, mi, vsw, both(km, t), both(km, t + 8));
