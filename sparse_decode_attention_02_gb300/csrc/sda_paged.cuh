@@ -67,7 +67,6 @@ constexpr int kMaxItems = kMaxWorkers * (kMaxRows / kJoinWarps);
 constexpr int kItemWord = 16, kTicketWord = 17; // of the workspace header: items listed, join blocks done
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kRescaleSlack = 8.0f;           // log2 units a running max may lag the true max
 
 struct JoinItem {
     int pieces, request, group, first;          // the unit, and the worker with its first piece
@@ -162,6 +161,13 @@ struct Shape {
     static constexpr int kSlots = stage_slots(kRowBytes, MT, ALONE);
     static constexpr int kStageBytes = kSlots * kRowBytes;
     static constexpr int kSteps = D / 16;                       // QK k-steps
+    // Log2 units that the running maximum may lag behind the true one, and that the
+    // weights are lifted by.  bf16 weights have fp32's range.  E4M3 caches take fp16
+    // weights: lifted by 13 and at most four times the running maximum's they reach
+    // 2^15 (fp16 ends at 2^16) and keep 11 bits down to 2^-27 of the largest, beyond
+    // that 2^-38 of it.  Without the lift tokens 10 nats below one that takes nearly
+    // all of the weight lost bits, and those 17 below it were lost, however many.
+    static constexpr float kRescaleSlack = FP8 ? 2.0f : 8.0f, kLift = FP8 ? 13.0f : 0.0f;
     static constexpr int kWorkers = kWarps / MT;                // of a CTA
     // Q fragments stay in registers, beside the output's D / 2, but for 256 dims:
     // there they take a third of the ring's place (each lane its own words).
@@ -984,12 +990,12 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL, ALONE>::kPer
                 }
 
                 // ---- Running maximum and sum.  The maximum may lag by
-                // kRescaleSlack, so that outputs are seldom rescaled; p <= 2^8.
+                // kRescaleSlack, so that outputs are seldom rescaled.
                 mx0 = fmaxf(mx0, __shfl_xor_sync(~0u, mx0, 1));
                 mx0 = fmaxf(mx0, __shfl_xor_sync(~0u, mx0, 2));
                 mx1 = fmaxf(mx1, __shfl_xor_sync(~0u, mx1, 1));
                 mx1 = fmaxf(mx1, __shfl_xor_sync(~0u, mx1, 2));
-                if (__any_sync(~0u, mx0 > m_run[0] + kRescaleSlack || mx1 > m_run[1] + kRescaleSlack)) {
+                if (__any_sync(~0u, mx0 > m_run[0] + S::kRescaleSlack || mx1 > m_run[1] + S::kRescaleSlack)) {
                     const float n0 = fmaxf(m_run[0], mx0), n1 = fmaxf(m_run[1], mx1);
                     const float a0 = n0 == -INFINITY ? 1.0f : fast_exp2(m_run[0] - n0);
                     const float a1 = n1 == -INFINITY ? 1.0f : fast_exp2(m_run[1] - n1);
@@ -1005,8 +1011,8 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL, ALONE>::kPer
                         o[n][3] *= a1;
                     }
                 }
-                const float ref0 = m_run[0] == -INFINITY ? 0.0f : m_run[0];
-                const float ref1 = m_run[1] == -INFINITY ? 0.0f : m_run[1];
+                const float ref0 = m_run[0] == -INFINITY ? 0.0f : m_run[0] - S::kLift;
+                const float ref1 = m_run[1] == -INFINITY ? 0.0f : m_run[1] - S::kLift;
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
                     sc[i][0] = fast_exp2(sc[i][0] - ref0);      // -inf gives 0
@@ -1151,6 +1157,7 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL, ALONE>::kPer
         for (int k = 0; k < 2; ++k) {
             l_run[k] += __shfl_xor_sync(~0u, l_run[k], 1);
             l_run[k] += __shfl_xor_sync(~0u, l_run[k], 2);
+            m_run[k] -= S::kLift;               // what sums and outputs are relative to
         }
         // A long unit's pieces of neighbouring workers are merged by the CTA where
         // they are all that its workers have: one piece for the join, not four.
