@@ -28,6 +28,7 @@ from ._binding import (  # noqa: F401
     sparse_decode_swa_attention,
     sparse_decode_swa_splits,
     status_string,
+    step_workspace,
     timeline_buffer,
     use_library,
     workspace_bytes,

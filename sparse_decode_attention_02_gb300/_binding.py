@@ -348,23 +348,39 @@ _NO_SCALE = (None, None)
 _step_workspaces: dict = {}
 
 
+_step_lock = threading.Lock()
+
+
 def _new_step_workspace(index: int, handle: int, nbytes: int, stream):
     """The serving-step entries' default workspace, its header zeroed on the call's stream: kept per
-    (device, stream) and grown on demand like `default_workspace`'s, but a capture gets one
-    of its own, zeroed in the graph, that no other graph or eager call shares.  Returns
-    (tensor, address, bytes)."""
+    (device, stream) and grown on demand like `default_workspace`'s, with the flags raised so
+    far, but a capture gets one of its own, zeroed in the graph, that no other graph or eager
+    call shares.  Returns (tensor, address, bytes)."""
     dev = torch.device("cuda", index)
-    with torch.cuda.stream(stream) if stream is not None else _current(dev):
+    with _step_lock, torch.cuda.stream(stream) if stream is not None else _current(dev):
         capturing = torch.cuda.is_current_stream_capturing()
-        have = _step_workspaces.get((index, handle))
-        if have is not None and have[2] >= nbytes and not capturing:
-            return have
+        old = _step_workspaces.get((index, handle))
+        if old is not None and old[2] >= nbytes and not capturing:
+            return old
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         ws[:256].zero_()                        # the header: all that has to be zero
-        have = ws, ws.data_ptr(), nbytes
+        if old is not None and not capturing:
+            ws[:4].copy_(old[0][:4])            # its first word: the flags
+        new = ws, ws.data_ptr(), nbytes
         if not capturing:
-            _step_workspaces[index, handle] = have
-        return have
+            _step_workspaces[index, handle] = new
+        return new
+
+
+def step_workspace(device=None, nbytes: int = 256, stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """The workspace that serving-step calls (plan_step, rope_append, paged_attention) use where none
+    is passed: one per (device, stream), grown on demand.  `read_errors(step_workspace())` tells
+    what they have flagged on the current stream since the flags were cleared.  A captured
+    call has one of its own; pass it a workspace to read its flags after a replay."""
+    device = torch.device("cuda" if device is None else device)
+    index = device.index if device.index is not None else torch.cuda.current_device()
+    handle = (stream if stream is not None else torch.cuda.current_stream(index)).cuda_stream
+    return _new_step_workspace(index, handle, max(int(nbytes), 256), stream)[0]
 
 
 def _scale_address(x, index: int, stream):
