@@ -201,6 +201,13 @@ def workspace_bytes(rows: int, heads: int, splits: int) -> int:
     return load().sparse_decode_workspace_bytes(int(rows), int(heads), int(splits))
 
 
+def _memory(workspace: torch.Tensor):
+    """(address, bytes) of a workspace, whose bytes have to be as many as it says."""
+    if not workspace.is_contiguous():
+        raise ValueError("sparse_decode: a workspace must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 _workspaces: dict = {}
 
 
@@ -249,14 +256,14 @@ def sparse_decode_attention(query, cache, regions, block_table, positions, activ
         workspace = default_workspace(dev, need, stream)
     ks, _keep_k = _scale_ptr(k_scale, dev, stream)
     vs, _keep_v = _scale_ptr(v_scale, dev, stream)
+    where, nbytes = _memory(workspace)
     descs = [describe(x) for x in (query, cache, regions, block_table, positions, active, output)]
     gd = describe(gate)
     s = stream if stream is not None else torch.cuda.current_stream(dev)
     with _current(dev):
         rc = lib.sparse_decode_attention(*[_ref(d) for d in descs], float(scale), int(query_len),
                                          int(splits), ks, vs, _ref(gd), int(bool(clear_inactive)),
-                                         int(region_tokens), workspace.data_ptr(),
-                                         workspace.numel() * workspace.element_size(), s.cuda_stream)
+                                         int(region_tokens), where, nbytes, s.cuda_stream)
     if rc != SDA_OK:
         raise SdaError(rc, lib.sparse_decode_status_string(rc).decode())
 
@@ -283,13 +290,14 @@ def sparse_decode_swa_attention(query, cache, block_table, seq_lens, output, *, 
         workspace = default_workspace(dev, need, stream)
     ks, _keep_k = _scale_ptr(k_scale, dev, stream)
     vs, _keep_v = _scale_ptr(v_scale, dev, stream)
+    where, nbytes = _memory(workspace)
     descs = [describe(x) for x in (query, cache, block_table, seq_lens, output)]
     gd = describe(gate)
     s = stream if stream is not None else torch.cuda.current_stream(dev)
     with _current(dev):
         rc = lib.sparse_decode_swa_attention(*[_ref(d) for d in descs], float(scale), int(window),
-                                             int(query_len), int(splits), ks, vs, _ref(gd), workspace.data_ptr(),
-                                             workspace.numel() * workspace.element_size(), s.cuda_stream)
+                                             int(query_len), int(splits), ks, vs, _ref(gd), where, nbytes,
+                                             s.cuda_stream)
     if rc != SDA_OK:
         raise SdaError(rc, lib.sparse_decode_status_string(rc).decode())
 
@@ -332,8 +340,7 @@ def sparse_decode_summary_scores(query, weights, summaries, block_table, seq_len
             scores = torch.empty((rows, int(n_cols)), dtype=torch.float32, device=dev)
     s = stream if stream is not None else torch.cuda.current_stream(dev)
     d = [describe(x) for x in (query, weights, summaries, block_table, seq_lens, scores, current, lengths)]
-    ws = workspace.data_ptr() if workspace is not None else None
-    wsb = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    ws, wsb = _memory(workspace) if workspace is not None else (None, 0)
     with _current(dev):
         rc = lib.sparse_decode_summary_scores(_ref(d[0]), _ref(d[1]), _ref(d[2]), _ref(d[3]), _ref(d[4]),
                                               int(block_size), int(query_len), _ref(d[5]), _ref(d[6]),
@@ -431,7 +438,7 @@ def _call(fn, tensors, arguments, need: int, workspace, stream, scales=()):
         if have is None or have[2] < need or capturing or stream is not None:
             have = _new_step_workspace(index, handle, need, stream)
     else:
-        have = workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        have = workspace, *_memory(workspace)
     pointers = [_scale_address(x, index, stream) for x in scales]
     if current:
         rc = fn(*arguments(where, pointers), have[1], have[2], handle)

@@ -177,8 +177,8 @@ public:
                 return false;
             }
             const at::Tensor &w = THPVariable_Unpack(args[3]);
-            if (!w.is_cuda() || w.get_device() != device_)
-                return false;
+            if (!w.is_cuda() || w.get_device() != device_ || !w.is_contiguous())
+                return false;                   // the binding refuses it
             workspace = w.data_ptr();
             bytes = w.nbytes();
             return true;

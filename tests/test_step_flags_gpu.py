@@ -70,3 +70,10 @@ def test_a_captured_step_shows_its_flags_in_the_workspace_it_was_given():
     assert sda.read_errors(ws) == 0
     g.replay()
     assert sda.read_errors(ws, clear=True) == sda.FLAG_FULL
+
+
+def test_a_workspace_with_gaps_is_refused():
+    for ws in (torch.zeros(1, dtype=torch.uint8, device="cuda").expand(256), torch.zeros(512, dtype=torch.uint8, device="cuda")[::2]):
+        for kw in ({}, dict(stream=torch.cuda.current_stream())):
+            with pytest.raises(ValueError, match="contiguous"):
+                out_of_pages(workspace=ws, **kw)
