@@ -331,8 +331,9 @@ sda_status sparse_decode_plan_step(const sda_tensor *context_lens, const sda_ten
  * t = positions[axis(i), token] * inv_freq[i]:
  *     a' = amplitude * (a cos t - b sin t),  b' = amplitude * (b cos t + a sin t)
  * over the first 2 * len(inv_freq) dims; the others pass through.  The angle
- * is reduced exactly (in 64-bit fixed point), so far positions lose nothing;
- * the products are fp32, each output is rounded once.
+ * is reduced in 64-bit fixed point: at any position it is off by less than
+ * max(1, |inv_freq|) * 2^-32 of a turn, beside the rounding of its fp32 sine
+ * and cosine.  The products are fp32, each output is rounded once.
  *
  *   query       [T, Hq, D] bf16 or NULL; query_out (written) the same shape;
  *               query_out may be query itself, else they must not overlap.
@@ -411,8 +412,16 @@ size_t sparse_decode_paged_workspace_bytes(int heads, int query_len, int head_di
  * equal inputs give equal bits.  What masked or unused cache places hold (NaN
  * included) does not reach the output.  An infinite value in V gives the rows
  * that see it an infinity of its sign, NaN where they see both signs or where
- * its weight underflows.  A length past the table (W * B) or a
- * table entry outside the cache raises SDA_FLAG_BOUNDS and is left out.
+ * its weight underflows.  A length past the table counts as W * B, and the
+ * piece of a table entry outside the cache is left out; both raise
+ * SDA_FLAG_BOUNDS.
+ * Logits, sums and outputs are fp32.  The weights that multiply V have 16 bits
+ * beside a bf16 cache; beside FP8 they have 11 down to 2^-27 of the row's
+ * largest, and below that are off by 2^-38 of it at most.
+ * How the work is split follows the width W, which the host knows, and not the
+ * lengths: where a table is wider than this step's longest request, a view of
+ * its first columns is the faster call (block_table with a smaller shape[1] and
+ * the same strides).
  * Errors as for sparse_decode_attention.
  */
 sda_status sparse_decode_paged_attention(const sda_tensor *query, const sda_tensor *cache,
