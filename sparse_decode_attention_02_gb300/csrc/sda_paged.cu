@@ -224,9 +224,6 @@ size_t align256(size_t n)
     return (n + 255) & ~static_cast<size_t>(255);
 }
 
-// A worker takes at least this many tiles before the line is cut finer (one request
-// of 1198 tokens x 4 groups: 14.5 us, with two 14.9).
-constexpr int kMinTiles = 1;
 // Units of at most kWholeTiles tiles (by the table's width) are never cut: a worker
 // takes them whole.  A CTA takes a unit alone instead
 //   * up to kAloneTiles tiles a worker (2 groups; cut and joined against alone: bf16,
@@ -357,7 +354,6 @@ extern "C" sda_status sparse_decode_paged_attention(const sda_tensor *query, con
     if (!p.cta_units)
         widest = widest_with(false);
     p.whole_units = !p.cta_units && widest <= kWholeTiles;
-    p.min_tiles = kMinTiles;
     // Few tiles: a worker on each of as many SMs first.
     const int64_t want = p.whole_units || p.cta_units ? units
                                                       : (units * (widest + kUnitCost) - 1) / (kMinTiles + kUnitCost) + 1;
