@@ -153,10 +153,10 @@ __device__ __forceinline__ uint32_t quotient(uint32_t x, unsigned long long inve
 constexpr int kStateBytes = 136;                // WarpState
 
 // FULL: a piece fills a stage (pages of at least a stage's tokens, in whole
-// stages), so the offsets in a stage are constants: 1 to 16 % of the time for 32
+// stages), so the offsets in a stage are constants: up to 16 % of the time for 32
 // requests of 16K tokens (most with 32 and 64 query rows), 1 to 12 % for 60 of up to
-// 500, at 64, 192 and 256 dims.  ALONE: each CTA has one unit,
-// its workers a share of the unit's tiles each.
+// 500, at 64, 192 and 256 dims.  ALONE: each CTA has one unit, its workers a share of
+// the unit's tiles each.
 template <bool FP8, int D, int MT, bool FULL, bool ALONE = false>
 struct Shape {
     static constexpr bool kFull = FULL, kAlone = ALONE;

@@ -21,7 +21,7 @@ def test_rotated_queries_while_the_current_stream_is_busy(fp8):
     busy = torch.empty(1 << 28, device="cuda")
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
-    for _ in range(100):                                      # tens of milliseconds
+    for _ in range(400):                                      # some 100 milliseconds
         busy.add_(1.0)
     got = sda.sparse_decode_rope_append(q, k, v, pos, inv, slots, cache, stream=side, **kw)
     side.synchronize()
@@ -47,7 +47,7 @@ def test_split_attention_and_selection_while_the_current_stream_is_busy():
     busy = torch.empty(1 << 28, device="cuda")
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
-    for _ in range(100):
+    for _ in range(400):
         busy.add_(1.0)
     sda.sparse_decode_attention(*args, got, stream=side, **kw)
     ids = sda.sparse_decode_select_regions(scores, current, 100, stream=side)
