@@ -1297,7 +1297,8 @@ __attribute__((visibility("hidden"))) uint64_t sda_wait_limit_ns()
 __attribute__((visibility("hidden"))) std::mutex &sda_launch_mutex(const void *workspace)
 {
     static std::mutex mutexes[64];
-    return mutexes[reinterpret_cast<uintptr_t>(workspace) / 256 % 64];
+    // large allocations lie 2 MB apart: all bits of the address have to count
+    return mutexes[reinterpret_cast<uintptr_t>(workspace) * 0x9E3779B97F4A7C15ull >> 58];
 }
 
 extern "C" {
