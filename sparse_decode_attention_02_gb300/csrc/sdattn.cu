@@ -497,8 +497,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         __syncwarp();
     }
-    pdl_launch_dependents();
     pdl_wait();   // inputs may be written by the previous kernel on the stream
+    // Only now: the combine kernel reads inputs before its own wait, and a previous
+    // kernel that lets its dependents start early could still be writing them.
+    pdl_launch_dependents();
     SDA_STAMP(threadIdx.x == 0 && blockIdx.x < kTimelineUnits, blockIdx.x * 8ull + 0);
 
     // Sparse mode: the row's selected regions, its position and active flag.
@@ -1129,7 +1131,8 @@ __global__ void __launch_bounds__(kCombineThreads) sda_combine_kernel(const __gr
     const int h = mine ? item / (kDim / 4) : 0;
     const int d = 4 * (item - h * (kDim / 4));
     // Inputs the split kernel does not write (activity, gate) are read while it
-    // still runs; its partials and LSEs only after the wait.
+    // still runs (what came before it is done: it waits before it lets this kernel
+    // start); its partials and LSEs only after the wait.
     bool act = false;
     float gam = 1.0f;
     if (mine) {
