@@ -50,7 +50,8 @@ typedef enum {
     SDA_DTYPE_INT32 = 4,
     SDA_DTYPE_BOOL = 5,       /* one byte, nonzero = true                              */
     SDA_DTYPE_FP32 = 6,
-    SDA_DTYPE_INT64 = 7
+    SDA_DTYPE_INT64 = 7,
+    SDA_DTYPE_INT8 = 8        /* elements of a quantised cache, -127..127              */
 } sda_dtype;
 
 /* A strided view of device memory.  Unused trailing shape/stride entries are
@@ -69,6 +70,7 @@ typedef struct {
 #define SDA_FLAG_TIMEOUT 0x2u  /* a pipeline wait exceeded its limit; the row's output is invalid */
 #define SDA_FLAG_FULL    0x4u  /* sparse_decode_plan_step: free pages or token rows ran out, some
                                   requests got nothing this step */
+#define SDA_FLAG_NONFINITE 0x8u /* sparse_decode_quantised_append: a key or value was not finite */
 
 /*
  * Split count per row: start at 1 and double while below 32 and
@@ -430,6 +432,74 @@ sda_status sparse_decode_paged_attention(const sda_tensor *query, const sda_tens
                                          int query_len, const float *k_scale, const float *v_scale,
                                          const sda_tensor *gate, void *workspace, size_t workspace_bytes,
                                          void *stream);
+
+/*
+ * Keys and values into a quantised cache: one byte an element, and a scale for
+ * each block of tokens of a head, for its keys and for its values, that follows
+ * what is written.  No counterpart on the pages, whose 8-bit cache has one pair
+ * of scales that the caller chooses (sparse_decode_rope_append writes that).
+ *
+ *   key, value  [T, G, D] bf16 (keys as they are to be stored: turned already,
+ *               as sparse_decode_rope_append does in place with them as `query`).
+ *   slots       [T] int64, stride 1: page * B + offset; -1 marks a padding row.
+ *   cache       [pages, G, B, 2D] FP8_E4M3, UINT8 (E4M3 bytes) or INT8, K first
+ *               then V (written at the slots, and see below).
+ *   scales      [pages, G, B / S, 2] fp32, stride[3] == 1: of the keys and of the
+ *               values of S places of a page (read and written).  S is a multiple
+ *               of 8.  Element e stands for e * scale.
+ *   workspace   NULL, or >= 256 bytes, 256-byte aligned: receives the flags.
+ * The least scale that holds the rows that a call writes into a block, a being
+ * their largest finite |x|, is for E4M3 the smallest power of two s with
+ * a <= 448 s, for INT8 fp32(a / 127), and at least 2^-126.  Where the rows begin
+ * at the block's first place that is the block's scale, whatever it held; else
+ * the scale is the larger of it and the one that is there.  A new element is
+ * e4m3(x / scale) or rint(x / scale), the quotient in fp32, to nearest even and
+ * saturated at 448 or 127.
+ * If the scale of a block in use grows, the places before the rows are rounded
+ * again: e4m3(f e) or rint(f e) with f = fp32(old / new) and the product in fp32.
+ * (A power of two leaves all but E4M3's smallest elements their value; an INT8
+ * element is off by half a step of the new scale more for each such call.)  Places
+ * behind the rows are left as they were and stand for nothing.
+ * An infinity is stored as the largest element of its sign, a NaN as E4M3's NaN or
+ * INT8's 0; both raise SDA_FLAG_NONFINITE.
+ * The rows of a block stand next to each other, in the order of their places and
+ * with no place between them left out, as sparse_decode_plan_step gives them: from
+ * the first that does not on, a block's rows are left out with SDA_FLAG_BOUNDS.  So
+ * is a slot outside the cache.  Rows of one block in two places of `slots` make its
+ * contents a mix of the two.
+ * D is a multiple of 16 up to 512.  stride[2] == 1 (cache: stride[3] == 1); bases
+ * and the other byte strides of key, value and cache are multiples of 16, those of
+ * scales of 8, else SDA_ERR_UNSUPPORTED.  Returns SDA_ERR_INVALID for shapes,
+ * dtypes or strides outside this contract, SDA_ERR_WORKSPACE for a bad workspace,
+ * SDA_ERR_CUDA if the launch failed; T == 0 returns SDA_OK with no launch.
+ */
+sda_status sparse_decode_quantised_append(const sda_tensor *key, const sda_tensor *value,
+                                          const sda_tensor *slots, const sda_tensor *cache,
+                                          const sda_tensor *scales, void *workspace,
+                                          size_t workspace_bytes, void *stream);
+
+/*
+ * Tokens of a quantised cache in bf16, request after request: what a prompt's
+ * attention over an earlier part reads.
+ *
+ *   cache, scales  as in sparse_decode_quantised_append.
+ *   block_table    [>= Q, W] int32, stride[1] == 1.
+ *   token_starts   [Q + 1] int32, stride 1, ascending: the row of each request's
+ *                  first token, and the row after the last.
+ *   first_tokens   [Q] int32 or NULL (0): the token that each request is read from.
+ *   key, value     [T, G, D] bf16 (written), either may be NULL: row
+ *                  token_starts[q] + i holds bf16(element * scale) of token
+ *                  first_tokens[q] + i.  Other rows are left as they were.
+ *   workspace      as in sparse_decode_quantised_append.
+ * A token whose table column is past the width or whose page is outside the cache
+ * leaves its row as it was, with SDA_FLAG_BOUNDS.  Limits and errors as for
+ * sparse_decode_quantised_append.
+ */
+sda_status sparse_decode_quantised_read(const sda_tensor *cache, const sda_tensor *scales,
+                                        const sda_tensor *block_table, const sda_tensor *token_starts,
+                                        const sda_tensor *first_tokens, const sda_tensor *key,
+                                        const sda_tensor *value, void *workspace, size_t workspace_bytes,
+                                        void *stream);
 
 /*
  * Reads the device error flags (SDA_FLAG_*) from a workspace into *flags,

@@ -8,6 +8,7 @@ load the library; the first call does, and raises if it is not built.
 from ._binding import (  # noqa: F401
     FLAG_BOUNDS,
     FLAG_FULL,
+    FLAG_NONFINITE,
     FLAG_TIMEOUT,
     SdaError,
     declared_functions,
@@ -21,6 +22,8 @@ from ._binding import (  # noqa: F401
     sparse_decode_attention_no_alloc,
     sparse_decode_paged_attention,
     sparse_decode_plan_step,
+    sparse_decode_quantised_append,
+    sparse_decode_quantised_read,
     sparse_decode_rope_append,
     sparse_decode_select_regions,
     sparse_decode_splits,

@@ -26,6 +26,7 @@ SDA_OK, SDA_ERR_INVALID, SDA_ERR_UNSUPPORTED, SDA_ERR_WORKSPACE, SDA_ERR_CUDA, S
 FLAG_BOUNDS = 0x1
 FLAG_TIMEOUT = 0x2
 FLAG_FULL = 0x4
+FLAG_NONFINITE = 0x8
 
 _DTYPES = {
     torch.bfloat16: 1,
@@ -35,6 +36,7 @@ _DTYPES = {
     torch.bool: 5,
     torch.float32: 6,
     torch.int64: 7,
+    torch.int8: 8,
 }
 
 
@@ -85,6 +87,10 @@ def _declare(lib):
     lib.sparse_decode_paged_workspace_bytes.restype = Z
     lib.sparse_decode_paged_attention.argtypes = 6 * [V] + [F, I] + 4 * [V] + [Z, V]
     lib.sparse_decode_paged_attention.restype = I
+    lib.sparse_decode_quantised_append.argtypes = 6 * [V] + [Z, V]
+    lib.sparse_decode_quantised_append.restype = I
+    lib.sparse_decode_quantised_read.argtypes = 8 * [V] + [Z, V]
+    lib.sparse_decode_quantised_read.restype = I
     lib.sparse_decode_read_errors.argtypes = [ctypes.c_void_p, ctypes.POINTER(ctypes.c_uint32),
                                               ctypes.c_int, ctypes.c_void_p]
     lib.sparse_decode_read_errors.restype = ctypes.c_int
@@ -103,7 +109,8 @@ def _declare(lib):
     lib.sparse_decode_status_string.restype = ctypes.c_char_p
     # of the entry points that csrc/sda_marshal.cpp calls
     lib.addresses = {f: ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
-                     for f in ("sparse_decode_plan_step", "sparse_decode_rope_append", "sparse_decode_paged_attention")}
+                     for f in ("sparse_decode_plan_step", "sparse_decode_rope_append", "sparse_decode_paged_attention",
+                               "sparse_decode_quantised_append", "sparse_decode_quantised_read")}
     return lib
 
 
@@ -380,8 +387,8 @@ def _new_step_workspace(index: int, handle: int, nbytes: int, stream):
 
 
 def step_workspace(device=None, nbytes: int = 256, stream: torch.cuda.Stream | None = None) -> torch.Tensor:
-    """The workspace that serving-step calls (plan_step, rope_append, paged_attention) use where none
-    is passed: one per (device, stream), grown on demand.  `read_errors(step_workspace())` tells
+    """The workspace that serving-step calls (plan_step, rope_append, paged_attention and those of the
+    quantised cache) use where none is passed: one per (device, stream), grown on demand.  `read_errors(step_workspace())` tells
     what they have flagged on the current stream since the flags were cleared.  A captured
     call has one of its own; pass it a workspace to read its flags after a replay."""
     device = torch.device("cuda" if device is None else device)
@@ -554,9 +561,44 @@ def sparse_decode_paged_attention(query, cache, block_table, seq_lens, output, *
         raise SdaError(rc, lib.sparse_decode_status_string(rc).decode())
 
 
+def sparse_decode_quantised_append(key, value, slots, cache, scales, *, workspace: torch.Tensor | None = None,
+                                   stream: torch.cuda.Stream | None = None) -> None:
+    """Keys and values quantised into their slots of a paged `cache` (E4M3, as uint8 too, or int8
+    elements) whose `scales` ([pages, G, block / span, 2] fp32: of the keys and the values of each
+    `span` tokens of a head) follow what is written; see include/sdattn.h for the contract."""
+    lib = _lib or load()
+    tensors = key, value, slots, cache, scales
+    rc = None
+    if stream is None:
+        rc = (_marshal or load_marshal()).quantised_append(lib.addresses["sparse_decode_quantised_append"], _step_workspaces,
+                                                           256, workspace, *tensors)
+    if rc is None:
+        rc = _call(lib.sparse_decode_quantised_append, tensors, lambda d, _: d, 256, workspace, stream)
+    if rc:
+        raise SdaError(rc, lib.sparse_decode_status_string(rc).decode())
+
+
+def sparse_decode_quantised_read(cache, scales, block_table, token_starts, key, value, *, first_tokens=None,
+                                 workspace: torch.Tensor | None = None,
+                                 stream: torch.cuda.Stream | None = None) -> None:
+    """Tokens of a quantised cache in bf16 into the rows of `key` and `value` ([T, G, D]; either may
+    be None): those of request q from `first_tokens[q]` (0 without it) on, into rows
+    `token_starts[q]` to `token_starts[q + 1]`; see include/sdattn.h for the contract."""
+    lib = _lib or load()
+    tensors = cache, scales, block_table, token_starts, first_tokens, key, value
+    rc = None
+    if stream is None:
+        rc = (_marshal or load_marshal()).quantised_read(lib.addresses["sparse_decode_quantised_read"], _step_workspaces,
+                                                         256, workspace, *tensors)
+    if rc is None:
+        rc = _call(lib.sparse_decode_quantised_read, tensors, lambda d, _: d, 256, workspace, stream)
+    if rc:
+        raise SdaError(rc, lib.sparse_decode_status_string(rc).decode())
+
+
 def read_errors(workspace: torch.Tensor, clear: bool = False,
                 stream: torch.cuda.Stream | None = None) -> int:
-    """Device error flags (FLAG_BOUNDS | FLAG_TIMEOUT) recorded in a workspace; synchronises."""
+    """Device error flags (FLAG_BOUNDS, FLAG_TIMEOUT, ...) recorded in a workspace; synchronises."""
     lib = load()
     dev = _device_of(workspace, stream=stream)
     s = stream if stream is not None else torch.cuda.current_stream(dev)

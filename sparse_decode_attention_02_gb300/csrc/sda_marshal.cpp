@@ -1,7 +1,7 @@
 // Argument marshalling of the Python binding, natively: tensors to the C ABI's
 // descriptors, their common device, and the stream a call goes to.  No
-// computation happens here.  plan_step, rope_append and paged_attention make the
-// plain calls from here (all on the current device, a workspace at hand); where
+// computation happens here.  The serving-step entries (plan_step and those below it) make
+// the plain calls from here (all on the current device, a workspace at hand); where
 // the binding has to see to something first they answer None, and the call goes
 // through ctypes.
 #define PY_SSIZE_T_CLEAN
@@ -30,6 +30,7 @@ int code_of(c10::ScalarType t)
     case c10::ScalarType::Bool: return SDA_DTYPE_BOOL;
     case c10::ScalarType::Float: return SDA_DTYPE_FP32;
     case c10::ScalarType::Long: return SDA_DTYPE_INT64;
+    case c10::ScalarType::Char: return SDA_DTYPE_INT8;
     default: return 0;
     }
 }
@@ -342,12 +343,40 @@ PyObject *paged_attention(PyObject *, PyObject *const *args, Py_ssize_t n)
     });
 }
 
+// tensors: key, value, slots, cache, scales
+PyObject *quantised_append(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    return plain_call(args, n, 9, [&](void *entry, sda_status &status) {
+        Plain c;
+        if (!c.read(args, 5))
+            return false;
+        status = call<decltype(sparse_decode_quantised_append)>(entry, c.at[0], c.at[1], c.at[2], c.at[3], c.at[4], c.workspace,
+                      c.bytes, c.stream);
+        return true;
+    });
+}
+
+// tensors: cache, scales, block_table, token_starts, first_tokens, key, value
+PyObject *quantised_read(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    return plain_call(args, n, 11, [&](void *entry, sda_status &status) {
+        Plain c;
+        if (!c.read(args, 7))
+            return false;
+        status = call<decltype(sparse_decode_quantised_read)>(entry, c.at[0], c.at[1], c.at[2], c.at[3], c.at[4], c.at[5], c.at[6],
+                      c.workspace, c.bytes, c.stream);
+        return true;
+    });
+}
+
 PyMethodDef methods[] = {
     {"pack", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(pack)), METH_FASTCALL, nullptr},
     {"scalar", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(scalar)), METH_FASTCALL, nullptr},
     {"plan_step", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(plan_step)), METH_FASTCALL, nullptr},
     {"rope_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rope_append)), METH_FASTCALL, nullptr},
     {"paged_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(paged_attention)), METH_FASTCALL, nullptr},
+    {"quantised_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(quantised_append)), METH_FASTCALL, nullptr},
+    {"quantised_read", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(quantised_read)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
