@@ -502,6 +502,58 @@ sda_status sparse_decode_quantised_read(const sda_tensor *cache, const sda_tenso
                                         void *stream);
 
 /*
+ * sparse_decode_paged_attention over a quantised cache.
+ *
+ *   cache, scales  as in sparse_decode_quantised_append; finite scales >= 0.
+ *   query, block_table, seq_lens, output, lse, scale, query_len, gate, workspace,
+ *   stream         as in sparse_decode_paged_attention (the workspace of
+ *                  sparse_decode_paged_workspace_bytes).
+ * The scales enter in fp32: a block's key scale multiplies its logits, its value
+ * scale its weights.  Weights times value scales have 11 bits down to 2^-27 of the
+ * product of the row's largest weight and the largest value scale that is met, and
+ * below that are off by 2^-38 of it at most.  Scales of blocks that no visible token
+ * lies in may hold anything.
+ */
+sda_status sparse_decode_quantised_paged_attention(const sda_tensor *query, const sda_tensor *cache,
+                                                   const sda_tensor *scales,
+                                                   const sda_tensor *block_table,
+                                                   const sda_tensor *seq_lens, const sda_tensor *output,
+                                                   const sda_tensor *lse, float scale, int query_len,
+                                                   const sda_tensor *gate, void *workspace,
+                                                   size_t workspace_bytes, void *stream);
+
+/*
+ * sparse_decode_attention over a quantised cache, for the head sizes of
+ * sparse_decode_paged_attention.
+ *
+ *   query          [rows, H, D] bf16, H in 1..16, D in {64, 128, 192, 256}.
+ *   cache, scales  as in sparse_decode_quantised_append; finite scales >= 0.
+ *   regions, block_table, positions, active, output, scale, query_len, gate,
+ *   clear_inactive, region_tokens, stream  as in sparse_decode_attention, but that
+ *                  any region_tokens and B will do whose greatest common divisor is a
+ *                  multiple of 8.
+ *   lse            NULL, or [rows, H] fp32 (written): natural log-sum-exp of the
+ *                  row's scaled logits; -inf for a row that sees nothing, as it was
+ *                  where the output is left as it was.
+ *   workspace      >= sparse_decode_paged_workspace_bytes(H, 1, D) bytes, 256-byte
+ *                  aligned, its header zeroed once before first use.  Calls that
+ *                  overlap on the GPU must not share one.
+ * The regions of all active rows are dealt out evenly over the GPU on the device;
+ * there is no split count.  An active row that sees no token is +0.0.  Equal inputs
+ * give equal bits.  A region id below -1, a table column past the width or an entry
+ * outside the cache leaves its tokens out with SDA_FLAG_BOUNDS.  rows must be tokens
+ * * G; requests = ceil(rows / (G * query_len)).
+ */
+sda_status sparse_decode_quantised_attention(const sda_tensor *query, const sda_tensor *cache,
+                                             const sda_tensor *scales, const sda_tensor *regions,
+                                             const sda_tensor *block_table, const sda_tensor *positions,
+                                             const sda_tensor *active, const sda_tensor *output,
+                                             const sda_tensor *lse, float scale, int query_len,
+                                             const sda_tensor *gate, int clear_inactive,
+                                             int region_tokens, void *workspace, size_t workspace_bytes,
+                                             void *stream);
+
+/*
  * Reads the device error flags (SDA_FLAG_*) from a workspace into *flags,
  * optionally clearing them.  Synchronises `stream` (it must be the stream the
  * calls ran on).  Returns SDA_ERR_CUDA if a CUDA call failed.

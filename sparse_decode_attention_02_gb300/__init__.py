@@ -23,6 +23,8 @@ from ._binding import (  # noqa: F401
     sparse_decode_paged_attention,
     sparse_decode_plan_step,
     sparse_decode_quantised_append,
+    sparse_decode_quantised_attention,
+    sparse_decode_quantised_paged_attention,
     sparse_decode_quantised_read,
     sparse_decode_rope_append,
     sparse_decode_select_regions,

@@ -91,6 +91,10 @@ def _declare(lib):
     lib.sparse_decode_quantised_append.restype = I
     lib.sparse_decode_quantised_read.argtypes = 8 * [V] + [Z, V]
     lib.sparse_decode_quantised_read.restype = I
+    lib.sparse_decode_quantised_paged_attention.argtypes = 7 * [V] + [F, I, V, V, Z, V]
+    lib.sparse_decode_quantised_paged_attention.restype = I
+    lib.sparse_decode_quantised_attention.argtypes = 9 * [V] + [F, I, V, I, I, V, Z, V]
+    lib.sparse_decode_quantised_attention.restype = I
     lib.sparse_decode_read_errors.argtypes = [ctypes.c_void_p, ctypes.POINTER(ctypes.c_uint32),
                                               ctypes.c_int, ctypes.c_void_p]
     lib.sparse_decode_read_errors.restype = ctypes.c_int
@@ -110,7 +114,8 @@ def _declare(lib):
     # of the entry points that csrc/sda_marshal.cpp calls
     lib.addresses = {f: ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
                      for f in ("sparse_decode_plan_step", "sparse_decode_rope_append", "sparse_decode_paged_attention",
-                               "sparse_decode_quantised_append", "sparse_decode_quantised_read")}
+                               "sparse_decode_quantised_append", "sparse_decode_quantised_read",
+                               "sparse_decode_quantised_paged_attention", "sparse_decode_quantised_attention")}
     return lib
 
 
@@ -533,6 +538,14 @@ def paged_workspace_bytes(heads: int, query_len: int = 1, head_dim: int = 192) -
     return load().sparse_decode_paged_workspace_bytes(_int32(heads), _int32(query_len), _int32(head_dim))
 
 
+def _paged_need(query, query_len: int) -> int:
+    shape = query.shape[1], int(query_len), query.shape[-1]
+    need = _paged_bytes.get(shape)
+    if need is None:
+        need = _paged_bytes[shape] = paged_workspace_bytes(*shape) or 256
+    return need
+
+
 def sparse_decode_paged_attention(query, cache, block_table, seq_lens, output, *, scale: float,
                                   query_len: int = 1, k_scale=None, v_scale=None, gate=None, lse=None,
                                   workspace: torch.Tensor | None = None,
@@ -541,12 +554,7 @@ def sparse_decode_paged_attention(query, cache, block_table, seq_lens, output, *
     cache into `output`, and the rows' log-sum-exps into `lse` if given; see
     include/sdattn.h for the contract."""
     lib = _lib or load()
-    need = 0
-    if workspace is None:
-        shape = query.shape[1], int(query_len), query.shape[-1]
-        need = _paged_bytes.get(shape)
-        if need is None:
-            need = _paged_bytes[shape] = paged_workspace_bytes(*shape) or 256
+    need = _paged_need(query, query_len) if workspace is None else 0
     tensors = query, cache, block_table, seq_lens, output, lse, gate
     rc = None
     if stream is None:
@@ -592,6 +600,50 @@ def sparse_decode_quantised_read(cache, scales, block_table, token_starts, key, 
                                                          256, workspace, *tensors)
     if rc is None:
         rc = _call(lib.sparse_decode_quantised_read, tensors, lambda d, _: d, 256, workspace, stream)
+    if rc:
+        raise SdaError(rc, lib.sparse_decode_status_string(rc).decode())
+
+
+def sparse_decode_quantised_paged_attention(query, cache, scales, block_table, seq_lens, output, *, scale: float,
+                                            query_len: int = 1, gate=None, lse=None,
+                                            workspace: torch.Tensor | None = None,
+                                            stream: torch.cuda.Stream | None = None) -> None:
+    """`sparse_decode_paged_attention` over a quantised `cache` with its `scales`; see
+    include/sdattn.h for the contract."""
+    lib = _lib or load()
+    need = _paged_need(query, query_len) if workspace is None else 0
+    tensors = query, cache, scales, block_table, seq_lens, output, lse, gate
+    rc = None
+    if stream is None:
+        rc = (_marshal or load_marshal()).quantised_paged_attention(lib.addresses["sparse_decode_quantised_paged_attention"],
+                                                                    _step_workspaces, need, workspace, *tensors, scale,
+                                                                    query_len)
+    if rc is None:
+        rc = _call(lib.sparse_decode_quantised_paged_attention, tensors,
+                   lambda d, _: (*d[:7], float(scale), _int32(query_len), d[7]), need, workspace, stream)
+    if rc:
+        raise SdaError(rc, lib.sparse_decode_status_string(rc).decode())
+
+
+def sparse_decode_quantised_attention(query, cache, scales, regions, block_table, positions, active, output, *,
+                                      scale: float, query_len: int = 1, clear_inactive: bool = True, gate=None,
+                                      lse=None, region_tokens: int = 0, workspace: torch.Tensor | None = None,
+                                      stream: torch.cuda.Stream | None = None) -> None:
+    """`sparse_decode_attention` over the selected regions of a quantised `cache` with its `scales`,
+    for head sizes 64, 128, 192 and 256, and the rows' log-sum-exps into `lse` if given; see
+    include/sdattn.h for the contract."""
+    lib = _lib or load()
+    need = _paged_need(query, 1) if workspace is None else 0
+    tensors = query, cache, scales, regions, block_table, positions, active, output, lse, gate
+    rc = None
+    if stream is None:
+        rc = (_marshal or load_marshal()).quantised_attention(lib.addresses["sparse_decode_quantised_attention"],
+                                                              _step_workspaces, need, workspace, *tensors, scale, query_len,
+                                                              clear_inactive, region_tokens)
+    if rc is None:
+        rc = _call(lib.sparse_decode_quantised_attention, tensors,
+                   lambda d, _: (*d[:9], float(scale), _int32(query_len), d[9], bool(clear_inactive), _int32(region_tokens)),
+                   need, workspace, stream)
     if rc:
         raise SdaError(rc, lib.sparse_decode_status_string(rc).decode())
 

@@ -11,7 +11,7 @@ ROOT = os.path.dirname(HERE)
 SOURCES = [os.path.join(HERE, "csrc", name) for name in (
     "sdattn.cu", "sda_select.cu", "sda_index.cu", "sda_plan.cu", "sda_rope.cu", "sda_quant.cu",
     "sda_paged.cu",
-    *(f"sda_paged_{kind}_{dim}.cu" for kind in ("bf16", "fp8") for dim in (64, 128, 192, 256)))]
+    *(f"sda_paged_{kind}_{dim}.cu" for kind in ("bf16", "fp8", "qe4m3", "qint8") for dim in (64, 128, 192, 256)))]
 INCLUDES = [os.path.join(HERE, "csrc", name) for name in ("sda_common.cuh", "sda_context.cuh", "sda_quant.cuh",
                                                            "sda_paged.cuh")]
 HEADER = os.path.join(ROOT, "include", "sdattn.h")

@@ -369,6 +369,40 @@ PyObject *quantised_read(PyObject *, PyObject *const *args, Py_ssize_t n)
     });
 }
 
+// tensors: query, cache, scales, block_table, seq_lens, output, lse, gate; scale, query_len
+PyObject *quantised_paged_attention(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    return plain_call(args, n, 14, [&](void *entry, sda_status &status) {
+        Plain c;
+        float scale;
+        int query_len;
+        if (!c.read(args, 8) || !as_float(args[12], scale) || !as_int(args[13], query_len))
+            return false;
+        status = call<decltype(sparse_decode_quantised_paged_attention)>(entry, c.at[0], c.at[1], c.at[2], c.at[3], c.at[4],
+                      c.at[5], c.at[6], scale, query_len, c.at[7], c.workspace, c.bytes, c.stream);
+        return true;
+    });
+}
+
+// tensors: query, cache, scales, regions, block_table, positions, active, output, lse, gate;
+// scale, query_len, clear_inactive, region_tokens
+PyObject *quantised_attention(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    return plain_call(args, n, 18, [&](void *entry, sda_status &status) {
+        Plain c;
+        float scale;
+        int query_len, region_tokens;
+        if (!c.read(args, 10) || !as_float(args[14], scale) || !as_int(args[15], query_len) || !as_int(args[17], region_tokens))
+            return false;
+        const int clear = PyObject_IsTrue(args[16]);
+        if (clear < 0)
+            return false;
+        status = call<decltype(sparse_decode_quantised_attention)>(entry, c.at[0], c.at[1], c.at[2], c.at[3], c.at[4], c.at[5],
+                      c.at[6], c.at[7], c.at[8], scale, query_len, c.at[9], clear, region_tokens, c.workspace, c.bytes, c.stream);
+        return true;
+    });
+}
+
 PyMethodDef methods[] = {
     {"pack", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(pack)), METH_FASTCALL, nullptr},
     {"scalar", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(scalar)), METH_FASTCALL, nullptr},
@@ -377,6 +411,10 @@ PyMethodDef methods[] = {
     {"paged_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(paged_attention)), METH_FASTCALL, nullptr},
     {"quantised_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(quantised_append)), METH_FASTCALL, nullptr},
     {"quantised_read", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(quantised_read)), METH_FASTCALL, nullptr},
+    {"quantised_paged_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(quantised_paged_attention)),
+     METH_FASTCALL, nullptr},
+    {"quantised_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(quantised_attention)), METH_FASTCALL,
+     nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -6,6 +6,7 @@
 #include <cmath>
 #include <cstring>
 #include <mutex>
+#include <numeric>
 
 namespace {
 
@@ -70,7 +71,11 @@ __global__ void __launch_bounds__(kJoinThreads) sda_paged_join_kernel(const __gr
         };
         const int j = (r * p.head_inv) >> 16, h = r - j * H;
         const int64_t token = static_cast<int64_t>(item.request) * p.query_len + j;
-        const uint16_t *gate = p.gate ? p.gate + token * p.g_s0 + static_cast<int64_t>(item.group * H + h) * p.g_s1 : nullptr;
+        // regions: an item's request is a row
+        const int64_t gate_token = p.region_groups ? item.request / p.region_groups : token;
+        const int gate_group = p.region_groups ? item.request % p.region_groups : item.group;
+        const uint16_t *gate =
+            p.gate ? p.gate + gate_token * p.g_s0 + static_cast<int64_t>(gate_group * H + h) * p.g_s1 : nullptr;
         const uint16_t gate_bits = gate ? *gate : 0;            // beside what follows
         const float vs = p.v_scale ? *p.v_scale : 1.0f;
 
@@ -263,55 +268,92 @@ extern "C" size_t sparse_decode_paged_workspace_bytes(int heads, int query_len, 
     return kHeaderBytes + align256(kItemBytes) + rows * head_dim * sizeof(float) + align256(rows * sizeof(float));
 }
 
-extern "C" sda_status sparse_decode_paged_attention(const sda_tensor *query, const sda_tensor *cache,
-                                                    const sda_tensor *block_table, const sda_tensor *seq_lens,
-                                                    const sda_tensor *output, const sda_tensor *lse, float scale,
-                                                    int query_len, const float *k_scale, const float *v_scale,
-                                                    const sda_tensor *gate, void *workspace,
-                                                    size_t workspace_bytes, void *stream)
+namespace {
+
+// One call of the entry points below after argument unpacking: whole caches
+// (seq_lens) or regions (regions, positions, active), plain caches (k_scale and
+// v_scale beside E4M3) or quantised ones (scales).
+struct Call {
+    const sda_tensor *query, *cache, *scales, *block_table, *seq_lens, *output, *lse, *gate;
+    const sda_tensor *regions, *positions, *active;
+    float scale;
+    int query_len, clear_inactive, region_tokens;
+    const float *k_scale, *v_scale;
+    void *workspace;
+    size_t workspace_bytes;
+    void *stream;
+};
+
+sda_status run_call(const Call &c)
 {
+    const sda_tensor *query = c.query, *cache = c.cache, *block_table = c.block_table, *output = c.output;
+    const bool by_region = c.regions != nullptr;
     // ---- Contract.
-    if (!dims_ok(query, 3) || !dims_ok(cache, 4) || !dims_ok(block_table, 2) || !dims_ok(seq_lens, 1) ||
-        !dims_ok(output, 3))
+    if (!dims_ok(query, 3) || !dims_ok(cache, 4) || !dims_ok(block_table, 2) || !dims_ok(output, 3) ||
+        (by_region ? !dims_ok(c.regions, 2) || !dims_ok(c.positions, 1) || !dims_ok(c.active, 1) : !dims_ok(c.seq_lens, 1)))
         return SDA_ERR_INVALID;
     const int64_t rows = query->shape[0], heads = query->shape[1], dim = query->shape[2];
-    if (query->dtype != SDA_DTYPE_BF16 || output->dtype != SDA_DTYPE_BF16 ||
-        block_table->dtype != SDA_DTYPE_INT32 || seq_lens->dtype != SDA_DTYPE_INT32)
+    if (query->dtype != SDA_DTYPE_BF16 || output->dtype != SDA_DTYPE_BF16 || block_table->dtype != SDA_DTYPE_INT32)
         return SDA_ERR_INVALID;
-    const bool fp8 = is_fp8(cache);
-    if (!fp8 && cache->dtype != SDA_DTYPE_BF16)
+    if (by_region ? c.regions->dtype != SDA_DTYPE_INT32 || c.positions->dtype != SDA_DTYPE_INT32 ||
+                        (c.active->dtype != SDA_DTYPE_BOOL && c.active->dtype != SDA_DTYPE_UINT8)
+                  : c.seq_lens->dtype != SDA_DTYPE_INT32)
+        return SDA_ERR_INVALID;
+    const bool fp8 = !c.scales && is_fp8(cache);
+    if (!c.scales && !fp8 && cache->dtype != SDA_DTYPE_BF16)
         return SDA_ERR_INVALID;
     if (cache->shape[3] != 2 * dim || output->shape[0] != rows || output->shape[1] != heads ||
         output->shape[2] != dim)
         return SDA_ERR_INVALID;
-    if (query->stride[2] != 1 || output->stride[2] != 1 || cache->stride[3] != 1 || block_table->stride[1] != 1)
+    if (query->stride[2] != 1 || output->stride[2] != 1 || cache->stride[3] != 1 ||
+        (block_table->shape[1] > 1 && block_table->stride[1] != 1))
         return SDA_ERR_INVALID;
-    if (!dim_ok(dim) || heads < 1 || heads > kMaxRows)
+    if (!dim_ok(dim) || heads < 1 || heads > (by_region ? kMaxRegionHeads : kMaxRows))
         return SDA_ERR_UNSUPPORTED;
-    if (query_len < 1 || !std::isfinite(scale) || (fp8 && (!k_scale || !v_scale)))
+    if (c.query_len < 1 || !std::isfinite(c.scale) || (fp8 && (!c.k_scale || !c.v_scale)))
         return SDA_ERR_INVALID;
+    // Query rows of a unit: a request's tokens, or one row of regions.
+    const int query_len = by_region ? 1 : c.query_len;
     if (heads * query_len > kMaxRows)
         return SDA_ERR_UNSUPPORTED;
+    QuantisedCache quantised = {};
+    if (c.scales) {
+        const sda_status st = check_quantised(cache, c.scales, dim, quantised);
+        if (st != SDA_OK)
+            return st;
+    }
     const int64_t pages = cache->shape[0], groups = cache->shape[1], block = cache->shape[2];
-    const int64_t requests = seq_lens->shape[0];
-    if (groups < 1 || block < 1 || pages < 1 || rows % (groups * query_len) != 0 ||
-        rows / (groups * query_len) != requests || block_table->shape[0] < requests)
+    if (groups < 1 || block < 1 || pages < 1)
         return SDA_ERR_INVALID;
-    const bool gated = given(gate);
-    if (gated && (!dims_ok(gate, 2) || gate->dtype != SDA_DTYPE_BF16 || gate->shape[0] != rows / groups ||
-                  gate->shape[1] != groups * heads))
+    int64_t requests, units;                    // lines of the table; units that the kernel is to cut
+    if (by_region) {
+        requests = (rows + groups * c.query_len - 1) / (groups * c.query_len);
+        units = rows;
+        if (rows % groups != 0 || block_table->shape[0] < requests || c.regions->shape[0] != rows ||
+            c.positions->shape[0] != rows || c.active->shape[0] != rows ||
+            (c.regions->shape[1] > 1 && c.regions->stride[1] != 1) || c.region_tokens < 0)
+            return SDA_ERR_INVALID;
+    } else {
+        requests = c.seq_lens->shape[0];
+        units = requests * groups;
+        if (rows % (groups * query_len) != 0 || rows / (groups * query_len) != requests || block_table->shape[0] < requests)
+            return SDA_ERR_INVALID;
+    }
+    const bool gated = given(c.gate);
+    if (gated && (!dims_ok(c.gate, 2) || c.gate->dtype != SDA_DTYPE_BF16 || c.gate->shape[0] != rows / groups ||
+                  c.gate->shape[1] != groups * heads))
         return SDA_ERR_INVALID;
-    const bool with_lse = given(lse);
-    if (with_lse && (!dims_ok(lse, 2) || lse->dtype != SDA_DTYPE_FP32 || lse->shape[0] != rows ||
-                     lse->shape[1] != heads || (rows > 1 && lse->stride[0] == 0) ||
-                     (heads > 1 && lse->stride[1] == 0)))
+    const bool with_lse = given(c.lse);
+    if (with_lse && (!dims_ok(c.lse, 2) || c.lse->dtype != SDA_DTYPE_FP32 || c.lse->shape[0] != rows ||
+                     c.lse->shape[1] != heads || (rows > 1 && c.lse->stride[0] == 0) ||
+                     (heads > 1 && c.lse->stride[1] == 0)))
         return SDA_ERR_INVALID;
     if ((rows > 1 && output->stride[0] == 0) || (heads > 1 && output->stride[1] == 0))
         return SDA_ERR_INVALID;
     if (pages > INT32_MAX || rows > INT32_MAX / kMaxRows || block_table->shape[1] > INT32_MAX ||
         block > (1 << 24) || groups > (1 << 16))
         return SDA_ERR_UNSUPPORTED;
-    const int elt = fp8 ? 1 : 2, row_bytes = static_cast<int>(2 * dim) * elt;
+    const int elt = cache->dtype == SDA_DTYPE_BF16 ? 2 : 1, row_bytes = static_cast<int>(2 * dim) * elt;
     if (block % 8 != 0)
         return SDA_ERR_UNSUPPORTED;
     if (!aligned(cache->data, 16))
@@ -319,13 +361,23 @@ extern "C" sda_status sparse_decode_paged_attention(const sda_tensor *query, con
     for (int i = 0; i < 3; ++i)
         if (cache->stride[i] <= 0 || (cache->stride[i] * elt) % 16 != 0)
             return SDA_ERR_UNSUPPORTED;
+    // Pieces divide pages, and regions.
+    const int64_t region = by_region ? (c.region_tokens ? c.region_tokens : block) : 0;
+    const int64_t whole = by_region ? std::gcd(region, block) : block;
+    if (by_region && (whole % 8 != 0 || region > (1 << 24) || c.regions->shape[1] > (1 << 20) ||
+                      c.regions->shape[1] * region > INT32_MAX - 4096))
+        return SDA_ERR_UNSUPPORTED;
+    const int64_t held = by_region ? c.regions->shape[1] * region : block_table->shape[1] * block;
     const size_t need = sparse_decode_paged_workspace_bytes(static_cast<int>(heads), query_len, static_cast<int>(dim));
-    if (!workspace || !aligned(workspace, 256) || workspace_bytes < need)
+    if (!c.workspace || !aligned(c.workspace, 256) || c.workspace_bytes < need)
         return SDA_ERR_WORKSPACE;
     if (rows == 0)
         return SDA_OK;
-    if (!query->data || !cache->data || !seq_lens->data || !output->data ||
-        (!block_table->data && block_table->shape[1] > 0))
+    if (!query->data || !cache->data || !output->data || (!block_table->data && block_table->shape[1] > 0) ||
+        (c.scales && !c.scales->data))
+        return SDA_ERR_INVALID;
+    if (by_region ? !c.positions->data || !c.active->data || (!c.regions->data && c.regions->shape[1] > 0)
+                  : !c.seq_lens->data)
         return SDA_ERR_INVALID;
 
     // ---- How the work is split, by the tiles that a request can have at most.
@@ -334,16 +386,15 @@ extern "C" sda_status sparse_decode_paged_attention(const sda_tensor *query, con
         return SDA_ERR_CUDA;
     Params p = {};
     p.rows = static_cast<int>(heads) * query_len;
-    p.cap = static_cast<int>(std::min<int64_t>(block_table->shape[1] * block, INT32_MAX - 4096));
-    const int64_t units = requests * groups;
+    p.cap = static_cast<int>(std::min<int64_t>(held, INT32_MAX - 4096));
     const int mt = tiles_of_rows(p.rows), per_cta = workers_of(p.rows);
     const int most = std::min(ctas_of(dim, p.rows), ctas_per_sm(static_cast<int>(dim), mt) * sms);
     // A TMA box holds the longest run of tokens that fits a stage and divides the
     // page, a tile the boxes that fit.  The tiles of the table's width:
     auto widest_with = [&](bool alone) {
         const int slots = stage_slots(row_bytes, mt, alone);
-        p.piece = static_cast<int>(std::min<int64_t>(block, slots)) / 8 * 8;
-        while (block % p.piece != 0)
+        p.piece = static_cast<int>(std::min<int64_t>(whole, slots)) / 8 * 8;
+        while (whole % p.piece != 0)
             p.piece -= 8;
         p.tile = slots / p.piece * p.piece;
         return (p.cap + static_cast<int64_t>(p.tile) - 1) / p.tile;
@@ -376,7 +427,7 @@ extern "C" sda_status sparse_decode_paged_attention(const sda_tensor *query, con
     const cuuint32_t box[5] = {static_cast<cuuint32_t>(128 / elt), static_cast<cuuint32_t>(p.piece),
                                static_cast<cuuint32_t>(bands), 1, 1};
     const cuuint32_t estride[5] = {1, 1, 1, 1, 1};
-    if (with_context(encode, &tmap, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
+    if (with_context(encode, &tmap, elt == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
                      const_cast<void *>(cache->data), gdim, gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
@@ -387,24 +438,47 @@ extern "C" sda_status sparse_decode_paged_attention(const sda_tensor *query, con
     p.q_s1 = query->stride[1];
     p.block_table = static_cast<const int32_t *>(block_table->data);
     p.bt_s0 = block_table->stride[0];
-    p.seq_lens = static_cast<const int32_t *>(seq_lens->data);
-    p.len_s = seq_lens->stride[0];
+    if (by_region) {
+        p.regions = static_cast<const int32_t *>(c.regions->data);
+        p.reg_s0 = c.regions->stride[0];
+        p.positions = static_cast<const int32_t *>(c.positions->data);
+        p.pos_s = c.positions->stride[0];
+        p.active = static_cast<const uint8_t *>(c.active->data);
+        p.act_s = c.active->stride[0];
+        p.region_tokens = static_cast<int>(region);
+        p.per_region = static_cast<int>(region / p.piece);
+        p.per_region_inv = inverse_of(static_cast<unsigned>(p.per_region));
+        p.region_groups = static_cast<int>(groups);
+        p.region_groups_inv = inverse_of(static_cast<unsigned>(groups));
+        // a line of the table for all rows where a request has as many as there are
+        p.request_rows = static_cast<int>(std::min<int64_t>(groups * c.query_len, INT32_MAX));
+        p.request_rows_inv = inverse_of(static_cast<unsigned>(p.request_rows));
+        p.clear_inactive = c.clear_inactive ? 1 : 0;
+    } else {
+        p.seq_lens = static_cast<const int32_t *>(c.seq_lens->data);
+        p.len_s = c.seq_lens->stride[0];
+    }
+    if (c.scales) {
+        p.scales = static_cast<const float *>(c.scales->data);
+        p.s_s0 = c.scales->stride[0], p.s_s1 = c.scales->stride[1], p.s_s2 = c.scales->stride[2];
+        p.span_inv = inverse_of(static_cast<unsigned>(quantised.span));
+    }
     p.output = static_cast<uint16_t *>(const_cast<void *>(output->data));
     p.o_s0 = output->stride[0];
     p.o_s1 = output->stride[1];
     if (with_lse) {
-        p.lse = static_cast<float *>(const_cast<void *>(lse->data));
-        p.l_s0 = lse->stride[0];
-        p.l_s1 = lse->stride[1];
+        p.lse = static_cast<float *>(const_cast<void *>(c.lse->data));
+        p.l_s0 = c.lse->stride[0];
+        p.l_s1 = c.lse->stride[1];
     }
     if (gated) {
-        p.gate = static_cast<const uint16_t *>(gate->data);
-        p.g_s0 = gate->stride[0];
-        p.g_s1 = gate->stride[1];
+        p.gate = static_cast<const uint16_t *>(c.gate->data);
+        p.g_s0 = c.gate->stride[0];
+        p.g_s1 = c.gate->stride[1];
     }
-    p.k_scale = fp8 ? k_scale : nullptr;
-    p.v_scale = fp8 ? v_scale : nullptr;
-    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    p.k_scale = fp8 ? c.k_scale : nullptr;
+    p.v_scale = fp8 ? c.v_scale : nullptr;
+    uint8_t *ws = static_cast<uint8_t *>(c.workspace);
     const size_t parts = static_cast<size_t>(ctas_of(dim, heads * query_len)) * per_cta * 2 * heads * query_len;
     p.flags = reinterpret_cast<unsigned int *>(ws);
     p.items = reinterpret_cast<JoinItem *>(ws + kHeaderBytes);
@@ -412,9 +486,9 @@ extern "C" sda_status sparse_decode_paged_attention(const sda_tensor *query, con
     p.part_lse = p.partial + parts * dim;
     p.pages = pages;
     p.wait_ns = sda_wait_limit_ns();
-    p.scale = scale;
-    p.requests = static_cast<int>(requests);
-    p.groups = static_cast<int>(groups);
+    p.scale = c.scale;
+    p.requests = static_cast<int>(by_region ? rows : requests);
+    p.groups = static_cast<int>(by_region ? 1 : groups);
     p.heads = static_cast<int>(heads);
     p.head_inv = (65536 + p.heads - 1) / p.heads;
     p.query_len = query_len;
@@ -430,13 +504,18 @@ extern "C" sda_status sparse_decode_paged_attention(const sda_tensor *query, con
     p.tile_inv = inverse_of(static_cast<unsigned>(p.tile));
     p.per_block_inv = inverse_of(static_cast<unsigned>(p.block / p.piece));
 
-    Launch *launch = dim == 64    ? (fp8 ? launch_fp8_64 : launch_bf16_64)
-                     : dim == 128 ? (fp8 ? launch_fp8_128 : launch_bf16_128)
-                     : dim == 192 ? (fp8 ? launch_fp8_192 : launch_bf16_192)
-                                  : (fp8 ? launch_fp8_256 : launch_bf16_256);
+    static Launch *const kLaunches[6][4] = {
+        {launch_bf16_64, launch_bf16_128, launch_bf16_192, launch_bf16_256},
+        {launch_fp8_64, launch_fp8_128, launch_fp8_192, launch_fp8_256},
+        {launch_qe4m3_64, launch_qe4m3_128, launch_qe4m3_192, launch_qe4m3_256},
+        {launch_qint8_64, launch_qint8_128, launch_qint8_192, launch_qint8_256},
+        {regions_qe4m3_64, regions_qe4m3_128, regions_qe4m3_192, regions_qe4m3_256},
+        {regions_qint8_64, regions_qint8_128, regions_qint8_192, regions_qint8_256}};
+    const int kind = c.scales ? 2 + (quantised.int8 ? 1 : 0) + (by_region ? 2 : 0) : fp8 ? 1 : 0;
+    Launch *launch = kLaunches[kind][dim / 64 - 1];
     // The split kernel leaves its list and pieces in the workspace, the join empties it.
-    const std::lock_guard<std::mutex> together(sda_launch_mutex(workspace));
-    const sda_status st = launch(tmap, p, stream);
+    const std::lock_guard<std::mutex> together(sda_launch_mutex(c.workspace));
+    const sda_status st = launch(tmap, p, c.stream);
     if (st != SDA_OK || p.whole_units || p.cta_units)
         return st;
     // A block an item (at most eight rows of a unit) as long as they run together.
@@ -452,5 +531,45 @@ extern "C" sda_status sparse_decode_paged_attention(const sda_tensor *query, con
                 : dim == 128 ? (few ? sda_paged_join_kernel<128, 8> : sda_paged_join_kernel<128, 4>)
                 : dim == 192 ? (few ? sda_paged_join_kernel<192, 8> : sda_paged_join_kernel<192, 4>)
                              : sda_paged_join_kernel<256, 4>;
-    return launch_pdl(join, grid, dim3(kJoinThreads), 0, stream, p);
+    return launch_pdl(join, grid, dim3(kJoinThreads), 0, c.stream, p);
+}
+
+}  // namespace
+
+extern "C" sda_status sparse_decode_paged_attention(const sda_tensor *query, const sda_tensor *cache,
+                                                    const sda_tensor *block_table, const sda_tensor *seq_lens,
+                                                    const sda_tensor *output, const sda_tensor *lse, float scale,
+                                                    int query_len, const float *k_scale, const float *v_scale,
+                                                    const sda_tensor *gate, void *workspace,
+                                                    size_t workspace_bytes, void *stream)
+{
+    return run_call({query, cache, nullptr, block_table, seq_lens, output, lse, gate, nullptr, nullptr, nullptr, scale,
+                     query_len, 0, 0, k_scale, v_scale, workspace, workspace_bytes, stream});
+}
+
+extern "C" sda_status sparse_decode_quantised_paged_attention(const sda_tensor *query, const sda_tensor *cache,
+                                                              const sda_tensor *scales, const sda_tensor *block_table,
+                                                              const sda_tensor *seq_lens, const sda_tensor *output,
+                                                              const sda_tensor *lse, float scale, int query_len,
+                                                              const sda_tensor *gate, void *workspace,
+                                                              size_t workspace_bytes, void *stream)
+{
+    if (!scales)
+        return SDA_ERR_INVALID;
+    return run_call({query, cache, scales, block_table, seq_lens, output, lse, gate, nullptr, nullptr, nullptr, scale,
+                     query_len, 0, 0, nullptr, nullptr, workspace, workspace_bytes, stream});
+}
+
+extern "C" sda_status sparse_decode_quantised_attention(const sda_tensor *query, const sda_tensor *cache,
+                                                        const sda_tensor *scales, const sda_tensor *regions,
+                                                        const sda_tensor *block_table, const sda_tensor *positions,
+                                                        const sda_tensor *active, const sda_tensor *output,
+                                                        const sda_tensor *lse, float scale, int query_len,
+                                                        const sda_tensor *gate, int clear_inactive, int region_tokens,
+                                                        void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!scales || !regions || !positions || !active)
+        return SDA_ERR_INVALID;
+    return run_call({query, cache, scales, block_table, nullptr, output, lse, gate, regions, positions, active, scale,
+                     query_len, clear_inactive, region_tokens, nullptr, nullptr, workspace, workspace_bytes, stream});
 }

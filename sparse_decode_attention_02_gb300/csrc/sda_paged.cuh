@@ -43,7 +43,7 @@
 // lengthened that chain (145 -> 160 us).
 #pragma once
 
-#include "sda_common.cuh"
+#include "sda_quant.cuh"
 
 #include <algorithm>
 #include <type_traits>
@@ -54,6 +54,7 @@ namespace paged {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxRows = 64;                    // query_len * heads
+constexpr int kMaxRegionHeads = 16;             // of a row that attends over regions
 constexpr int kSms = 152;
 constexpr int kMaxWorkers = kSms * 2 * kWarps;  // two CTAs of them on each SM (or three of two)
 // Tiles that a unit's end is worth on the line (188 requests of up to 2500 tokens, then
@@ -70,6 +71,11 @@ constexpr int kMaxItems = kMaxWorkers * (kMaxRows / kJoinWarps);
 constexpr int kItemWord = 16, kTicketWord = 17; // of the workspace header: items listed, join blocks done
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+
+// What the cache holds: bf16; E4M3 with a scale for all keys and one for all values;
+// E4M3 or integers with scales of their own for each block of tokens and head.  All
+// one-byte kinds are multiplied in fp16, which holds them exactly.
+enum Kind { kBf16, kE4m3, kScaledE4m3, kScaledInt8 };
 
 struct JoinItem {
     int pieces, request, group, first;          // the unit, and the worker with its first piece
@@ -91,6 +97,15 @@ struct Params {
     const uint16_t *gate;
     int64_t g_s0, g_s1;
     const float *k_scale, *v_scale;
+    const float *scales;                        // quantised caches: (key, value) pairs
+    int64_t s_s0, s_s1, s_s2;
+    // Regions: a unit is a row, p.requests rows of one group each.
+    const int32_t *regions;
+    int64_t reg_s0;
+    const int32_t *positions;
+    int64_t pos_s;
+    const uint8_t *active;
+    int64_t act_s;
     unsigned int *flags;
     JoinItem *items;
     float *partial;                             // [worker][continued here / goes on][rows][D]
@@ -105,6 +120,10 @@ struct Params {
     int ctas, workers, whole_units, cta_units;   // cta_units: ALONE
     unsigned long long per_block_inv, tile_inv, workers_inv;    // inverse_of the pieces of a page, tile, workers
     int q_vec, o_vec;                           // 8-byte loads of q and stores of the output
+    unsigned long long span_inv, per_region_inv, region_groups_inv, request_rows_inv;
+    int per_region, region_tokens;              // pieces and tokens of a region
+    int region_groups, request_rows;            // KV groups (0: no regions), rows that share a line of the table
+    int clear_inactive;
 };
 
 // Tokens of a stage for a cache row of `row_bytes`: 6 to 12 KB of cache where a
@@ -138,18 +157,6 @@ constexpr int tiles_of_rows(int rows)
     return rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
 }
 
-// x / d as a product: floor(x * inverse_of(d) / 2^64) is exact for x, d < 2^32
-// (d == 1 has no 64-bit inverse: 0 stands for it).
-constexpr unsigned long long inverse_of(unsigned d)
-{
-    return d > 1 ? ~0ull / d + 1 : 0;
-}
-
-__device__ __forceinline__ uint32_t quotient(uint32_t x, unsigned long long inverse)
-{
-    return inverse ? static_cast<uint32_t>(__umul64hi(x, inverse)) : x;
-}
-
 constexpr int kStateBytes = 136;                // WarpState
 
 // FULL: a piece fills a stage (pages of at least a stage's tokens, in whole
@@ -157,9 +164,10 @@ constexpr int kStateBytes = 136;                // WarpState
 // requests of 16K tokens (most with 32 and 64 query rows), 1 to 12 % for 60 of up to
 // 500, at 64, 192 and 256 dims.  ALONE: each CTA has one unit, its workers a share of
 // the unit's tiles each.
-template <bool FP8, int D, int MT, bool FULL, bool ALONE = false>
+template <int KIND, int D, int MT, bool FULL, bool ALONE = false, bool REGIONS = false>
 struct Shape {
-    static constexpr bool kFull = FULL, kAlone = ALONE;
+    static constexpr bool kFull = FULL, kAlone = ALONE, kRegions = REGIONS, kScaled = KIND >= kScaledE4m3;
+    static constexpr bool FP8 = KIND != kBf16;
     static constexpr int kElt = FP8 ? 1 : 2;
     static constexpr int kRowBytes = 2 * D * kElt;
     static constexpr int kBands = kRowBytes / 128;
@@ -189,7 +197,10 @@ struct Shape {
     static constexpr int kCtlOff = (kIssuedOff + 4 * kStages + 15) / 16 * 16;
     static constexpr int kStatsOff = kCtlOff + 16 + 8 * (kThreads + kWarps);    // of a merge: maximum and sum of each row
     static constexpr int kStateOff = kStatsOff + kWarps * 16 * 8;
-    static constexpr int kBytes = kStateOff + kWarps * kStateBytes + 1024;         // + the base's alignment
+    static constexpr int kScaleOff = kStateOff + kWarps * kStateBytes;      // of each stage's eight-token tiles; of a merge
+    static constexpr int kStageScales = kScaled ? kSlots / 8 * 8 : 0;
+    static constexpr int kUnitsOff = kScaleOff + kStages * kStageScales;    // what the workers' outputs are in units of
+    static constexpr int kBytes = kUnitsOff + (kScaled ? 4 * kWarps : 0) + 1024;     // + the base's alignment
     static_assert(kPerSm * kWorkers <= 2 * kWarps, "join list");
     static_assert(kStageBytes % 1024 == 0 && kRing >= 2 && kBytes <= 232448 / kPerSm - 1024, "ring");
 };
@@ -199,13 +210,19 @@ struct Segment {
     int request, group, first, last, tiles, len;   // tiles [first, last) of the unit's `tiles`
 };
 
+template <bool REGIONS>
 struct Walk {
     long long left;                             // line from the unit's start to the part's end
     int request, group, tile;                   // (whole_units: units still to take)
 
+    // Tokens of a unit; of an active row all that its list has room for.  0: a row
+    // of zeros, < 0: left as it was.
     static __device__ __forceinline__ int length(const Params &p, int q)
     {
-        return min(p.seq_lens[q * p.len_s], p.cap);
+        if constexpr (REGIONS)
+            return p.active[q * p.act_s] ? p.cap : p.clear_inactive ? 0 : -1;
+        else
+            return min(p.seq_lens[q * p.len_s], p.cap);
     }
 
     static __device__ __forceinline__ int tiles_of(const Params &p, int len)
@@ -313,15 +330,6 @@ __device__ __forceinline__ void mma1688(float (&c)[4], uint32_t a0, uint32_t a1,
         : "r"(a0), "r"(a1), "r"(b));
 }
 
-// Two E4M3 bytes (low byte -> low half) to two fp16 values, exactly.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two)
-{
-    uint32_t r;
-    const uint16_t v = static_cast<uint16_t>(two);
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(v));
-    return r;
-}
-
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t sel)
 {
     uint32_t r;
@@ -348,11 +356,62 @@ __device__ __forceinline__ void split_bf16(float lo, float hi, uint32_t &most, u
     rest = pack_bf16(lo - __uint_as_float(a & 0xFFFF0000u), hi - __uint_as_float(b & 0xFFFF0000u));
 }
 
+// The four elements of a word of keys: two pairs of fp16 values, in order.
+template <int KIND>
+__device__ __forceinline__ uint2 key_pairs(uint32_t w)
+{
+    if constexpr (KIND == kScaledInt8) {
+        const uint32_t x = w ^ 0x80808080u;
+        return make_uint2(int8x2_to_f16x2<0, 1>(x), int8x2_to_f16x2<2, 3>(x));
+    } else {
+        return make_uint2(e4m3x2_to_f16x2(w), e4m3x2_to_f16x2(w >> 16));
+    }
+}
+
+// A word of two tokens' values (two dims of one, two of the other): the pairs of the
+// first dim and of the second.
+template <int KIND>
+__device__ __forceinline__ uint2 value_pairs(uint32_t w)
+{
+    if constexpr (KIND == kScaledInt8) {
+        const uint32_t x = w ^ 0x80808080u;
+        return make_uint2(int8x2_to_f16x2<0, 2>(x), int8x2_to_f16x2<1, 3>(x));
+    } else {
+        const uint32_t x = prmt(w, 0x3120u);
+        return make_uint2(e4m3x2_to_f16x2(x), e4m3x2_to_f16x2(x >> 16));
+    }
+}
+
+__device__ __forceinline__ float2 lds64(uint32_t addr)
+{
+    float2 v;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
+    return v;
+}
+
+// Eight bytes from global to shared memory, not waited for.
+__device__ __forceinline__ void copy8(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// The barrier's phase is not over before this thread's copies have landed.
+__device__ __forceinline__ void copies_arrive(uint32_t bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 __device__ __forceinline__ float fast_exp2(float x)
 {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// 2^-k of 2^k, -126 <= k <= 126.
+__device__ __forceinline__ float reciprocal_of_power(float x)
+{
+    return __uint_as_float((254u << 23) - __float_as_uint(x));
 }
 
 // The headwise gate: sigmoid in fp32, rounded to bf16.
@@ -380,11 +439,12 @@ __device__ __forceinline__ uint64_t low_bits(int n)
 // `vsw` its swizzle phase.  bf16: P comes in two parts (split_bf16), so that its
 // products carry 16 bits of it.  MASKED zeroes V of slots out of the
 // mask (vm0: k-slots 2t, 2t + 1; vm1: 8 + 2t, 9 + 2t), whatever they hold.
-template <bool FP8, int D, bool MASKED>
+template <int KIND, int D, bool MASKED>
 __device__ __forceinline__ void pv_accumulate(float (&o)[D / 8][4], const uint32_t (&pa)[4],
                                               const uint32_t (&pb)[4], uint32_t vrow, uint32_t bstride, int mi,
                                               int vsw, uint32_t vm0, uint32_t vm1)
 {
+    constexpr bool FP8 = KIND != kBf16;
     constexpr int kFirst = D * (FP8 ? 1 : 2) / 16;              // V's first 16-byte chunk of a row
 #pragma unroll
     for (int c2 = 0; c2 < kFirst / 2; ++c2) {
@@ -402,9 +462,9 @@ __device__ __forceinline__ void pv_accumulate(float (&o)[D / 8][4], const uint32
             // a 16-dim chunk is two n8 tiles: its even dims and its odd ones
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const uint32_t x0 = prmt(r[2 * h], 0x3120u), x1 = prmt(r[2 * h + 1], 0x3120u);
-                mma16816<true>(o[4 * c2 + 2 * h], pa, e4m3x2_to_f16x2(x0), e4m3x2_to_f16x2(x1));
-                mma16816<true>(o[4 * c2 + 2 * h + 1], pa, e4m3x2_to_f16x2(x0 >> 16), e4m3x2_to_f16x2(x1 >> 16));
+                const uint2 x0 = value_pairs<KIND>(r[2 * h]), x1 = value_pairs<KIND>(r[2 * h + 1]);
+                mma16816<true>(o[4 * c2 + 2 * h], pa, x0.x, x1.x);
+                mma16816<true>(o[4 * c2 + 2 * h + 1], pa, x0.y, x1.y);
             }
         } else {
             mma16816<false>(o[2 * c2], pa, r[0], r[1]);
@@ -462,7 +522,7 @@ __device__ __forceinline__ long long boundary(const Params &p, long long total, 
 // w * CTAs + CTA, which spreads them over the SMs.  Every thread of the block
 // calls it; a worker's warps look for its part together.
 // `sums`: kThreads + kWarps values of shared memory.
-template <int WORKERS>
+template <int WORKERS, bool REGIONS>
 __device__ __forceinline__ Part find_part(const Params &p, long long *sums, int w, long long &total, int &used, int &v)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -481,7 +541,7 @@ __device__ __forceinline__ Part find_part(const Params &p, long long *sums, int 
     const int per = (p.requests + kThreads - 1) / kThreads;
     const int q0 = min(p.requests, static_cast<int>(threadIdx.x) * per), q1 = min(p.requests, q0 + per);
     auto span = [&](int q) -> long long {
-        const int tiles = Walk::tiles_of(p, Walk::length(p, q));
+        const int tiles = Walk<REGIONS>::tiles_of(p, Walk<REGIONS>::length(p, q));
         return tiles > 0 ? tiles + kUnitCost : 0;
     };
     auto scan = [&](long long x) {              // inclusive, over the warp
@@ -566,15 +626,16 @@ __device__ __forceinline__ Part find_part(const Params &p, long long *sums, int 
 
 // Where a warp is on the line.  It lies in shared memory (all lanes write the
 // same): between units it is not needed, and registers are short.
+template <bool REGIONS>
 struct Place {
-    Walk walk;
+    Walk<REGIONS> walk;
     Segment seg;
     long long unit;                             // where the segment's unit begins on the line
 
     // The next segment into seg; a copy of it in `s`.
     __device__ __forceinline__ bool next(const Params &p, long long part_end, Segment &s)
     {
-        Walk w = walk;
+        Walk<REGIONS> w = walk;
         __syncwarp();                           // every lane has read it
         unit = part_end - w.left;
         const bool some = w.next(p, s);
@@ -585,18 +646,19 @@ struct Place {
     }
 };
 
+template <bool REGIONS>
 struct WarpState {
-    Place here, ahead;                          // of the warp's products and of its feed
+    Place<REGIONS> here, ahead;                          // of the warp's products and of its feed
     long long part_end, total;                  // on the line; the line's length
     int used, number;                           // workers with a part; this one's number
 };
 
-static_assert(sizeof(WarpState) == kStateBytes, "shared memory of a warp");
+static_assert(sizeof(WarpState<false>) == kStateBytes && sizeof(WarpState<true>) == kStateBytes, "shared memory of a warp");
 
 // A worker's ring of stages: their places, barriers, headers (the slots that
 // hold tokens) and how often each was issued.
 struct Ring {
-    uint32_t stages, full;
+    uint32_t stages, full, scales;
     uint64_t *hdr;
     int *issued;
 };
@@ -606,7 +668,7 @@ struct Ring {
 // in one segment.
 template <class S>
 struct Feed {
-    Place *at_line;                             // of the next segment to look up
+    Place<S::kRegions> *at_line;                // of the next segment to look up
     bool more;
     int tile;                                   // of the segment, the next to look up
     int per_stage, batch, lane_stage, lane_piece;   // pieces of a stage, stages of a batch; the lane's place in one
@@ -629,10 +691,14 @@ struct Feed {
         n2 = min(batch, seg.last - tile);
         group2 = seg.group;
         const int f = (tile + lane_stage) * per_stage + lane_piece;
-        const int col = static_cast<int>(quotient(f, p.per_block_inv));
-        off2 = f * P - col * p.block;
-        left2 = lane_stage < n2 ? seg.len - f * P : 0;          // tokens from the piece's first on
-        page2 = left2 > 0 && col < p.table_cols ? p.block_table[seg.request * p.bt_s0 + col] : -1;
+        if constexpr (S::kRegions) {
+            region_piece(p, seg, f);
+        } else {
+            const int col = static_cast<int>(quotient(f, p.per_block_inv));
+            off2 = f * P - col * p.block;
+            left2 = lane_stage < n2 ? seg.len - f * P : 0;          // tokens from the piece's first on
+            page2 = left2 > 0 && col < p.table_cols ? p.block_table[seg.request * p.bt_s0 + col] : -1;
+        }
         tile += n2;
         if (tile >= seg.last) {
             if constexpr (S::kAlone)
@@ -644,7 +710,7 @@ struct Feed {
     }
 
     // The feed's place is where the worker's part begins.
-    __device__ __forceinline__ void start(const Params &p, Place *place, int lane)
+    __device__ __forceinline__ void start(const Params &p, Place<S::kRegions> *place, int lane)
     {
         at_line = place;
         per_stage = S::kFull ? 1 : p.tile / p.piece;
@@ -691,6 +757,29 @@ struct Feed {
     }
 
 private:
+    // Piece f of a row's regions: its request's table line, the row's group, and how
+    // many of its tokens the row sees.
+    __device__ __forceinline__ void region_piece(const Params &p, const Segment &seg, int f)
+    {
+        const unsigned row = static_cast<unsigned>(seg.request);
+        const unsigned of = quotient(f, p.per_region_inv);
+        const bool some = lane_stage < n2 && f * p.piece < seg.len;
+        const int id = some ? p.regions[row * p.reg_s0 + of] : -1;
+        group2 = static_cast<int>(row - quotient(row, p.region_groups_inv) * p.region_groups);
+        const int64_t token = static_cast<int64_t>(id) * p.region_tokens + (f - static_cast<int>(of) * p.per_region) * p.piece;
+        const int64_t seen = id >= 0 ? p.positions[row * p.pos_s] + 1 - token : 0;
+        left2 = static_cast<int>(max(min(seen, static_cast<int64_t>(p.piece)), static_cast<int64_t>(0)));
+        page2 = -1;
+        if (id < -1)
+            atomicOr(p.flags, SDA_FLAG_BOUNDS);
+        if (left2 > 0) {                        // token <= position: 31 bits
+            const int col = static_cast<int>(static_cast<unsigned>(token) / static_cast<unsigned>(p.block));
+            off2 = static_cast<int>(token) - col * p.block;
+            if (col < p.table_cols)
+                page2 = p.block_table[static_cast<int64_t>(quotient(row, p.request_rows_inv)) * p.bt_s0 + col];
+        }
+    }
+
     // Stages at .. at + count - 1 of the batch into places slot, slot + 1, ...:
     // a stage's first lane announces its bytes and the tokens that it will hold.
     __device__ __forceinline__ void send(const Params &p, const CUtensorMap *tmap, const Ring &r, int slot, int count,
@@ -706,14 +795,20 @@ private:
         const int place = slot + mine;
         const uint32_t full = r.full + 8 * place;
         const bool leads = mine >= 0 && mine < count && lane_piece == 0;
+        uint64_t bits = 0;
+        if constexpr (S::kRegions) {            // each piece has tokens of its own
+            const uint64_t own = copy ? low_bits(left) << (lane_piece * p.piece) : 0;
+            for (int k = 0; k < per_stage; ++k)
+                bits |= __shfl_down_sync(~0u, own, k);          // of use to a stage's first lane
+        }
         if (leads) {
-            uint64_t bits = 0;
             const unsigned of_stage = copies >> lane;           // this lane is the stage's first
             int pieces = 0;
             for (int k = 0; k < per_stage; ++k)
                 if ((of_stage >> k) & 1u) {
                     ++pieces;
-                    bits |= low_bits(min(p.piece, left - k * p.piece)) << (k * p.piece);
+                    if constexpr (!S::kRegions)
+                        bits |= low_bits(min(p.piece, left - k * p.piece)) << (k * p.piece);
                 }
             r.hdr[place] = bits;
             r.issued[place] += 1;
@@ -723,17 +818,29 @@ private:
         __syncwarp();
         if (copy)
             tma_load_5d(r.stages + place * S::kStageBytes + lane_piece * piece_bytes, tmap, 0, off, 0, group, page, full);
+        if constexpr (S::kScaled) {             // the scales of the piece's eight-token tiles
+            if (copy) {
+                const float *src = p.scales + page * p.s_s0 + group * p.s_s1;
+                const uint32_t dst = r.scales + place * S::kStageScales + lane_piece * p.piece;
+                for (int k = 0; k < p.piece; k += 8)
+                    copy8(dst + k, src + quotient(off + k, p.span_inv) * p.s_s2);
+                copies_arrive(full);
+            }
+            __syncwarp();                       // before the stage's own arrival
+        }
         if (leads)
             mbar_arrive(full);
         at += count;
     }
 };
 
-template <bool FP8, int D, int MT, bool FULL, bool ALONE>
-__global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL, ALONE>::kPerSm)
+template <int KIND, int D, int MT, bool FULL, bool ALONE, bool REGIONS>
+__global__ void __launch_bounds__(kThreads, Shape<KIND, D, MT, FULL, ALONE, REGIONS>::kPerSm)
     sda_paged_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_constant__ Params p)
 {
-    using S = Shape<FP8, D, MT, FULL, ALONE>;
+    using S = Shape<KIND, D, MT, FULL, ALONE, REGIONS>;
+    using Line = Walk<REGIONS>;
+    constexpr bool FP8 = S::FP8, SCALED = S::kScaled;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
@@ -762,19 +869,19 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL, ALONE>::kPer
     pdl_wait();
 
     // What is needed between units only: this warp's place, its feed's, the line.
-    WarpState *state = reinterpret_cast<WarpState *>(smem + S::kStateOff) + warp;
+    WarpState<REGIONS> *state = reinterpret_cast<WarpState<REGIONS> *>(smem + S::kStateOff) + warp;
     if constexpr (ALONE) {
         Segment &seg = state->here.seg;
         seg.request = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.groups));
         seg.group = static_cast<int>(blockIdx.x) - seg.request * p.groups;
-        seg.len = Walk::length(p, seg.request);
-        seg.tiles = Walk::tiles_of(p, seg.len);
+        seg.len = Line::length(p, seg.request);
+        seg.tiles = Line::tiles_of(p, seg.len);
         seg.first = seg.tiles * worker / S::kWorkers;
         seg.last = seg.tiles * (worker + 1) / S::kWorkers;
     } else {
         long long total;
         int used, v;
-        const Part part = find_part<S::kWorkers>(p, sums, worker, total, used, v);
+        const Part part = find_part<S::kWorkers, REGIONS>(p, sums, worker, total, used, v);
         state->here.walk = state->ahead.walk = {part.left, part.request, part.group, part.tile};
         state->part_end = part.start + part.left;
         state->total = total;
@@ -783,13 +890,14 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL, ALONE>::kPer
     }
     __syncwarp();
     Feed<S> feed;
-    const Ring place = {sbase, full_bar, hdr, issued};
+    const uint32_t scale_base = smem_u32(smem) + S::kScaleOff + worker * S::kRing * S::kStageScales;
+    const Ring place = {sbase, full_bar, scale_base, hdr, issued};
     if (mt == 0)
         feed.start(p, ALONE ? &state->here : &state->ahead, lane);
 
     const int g = lane >> 2, t = lane & 3;      // fragment row and column pair
     const int H = p.heads, R = p.rows;
-    const float ks = FP8 ? load_now(p.k_scale) : 1.0f, vs = FP8 ? load_now(p.v_scale) : 1.0f;
+    const float ks = KIND == kE4m3 ? load_now(p.k_scale) : 1.0f, vs = KIND == kE4m3 ? load_now(p.v_scale) : 1.0f;
     auto token_of = [&](int r) { return (r * p.head_inv) >> 16; };      // of a query row
 
     const int r0 = 16 * mt + g, r1 = r0 + 8;    // this thread's query rows
@@ -912,6 +1020,9 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL, ALONE>::kPer
         for (int n = 0; n < D / 8; ++n)
             o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
         float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.0f, 0.0f};
+        // Outputs of a quantised cache are in units of a power of two that is at least
+        // the largest value scale so far, so that weights times scales fit fp16.
+        float unit = kSmallestScale;
 
         for (; left > 0; --left, common -= FULL ? S::kSlots : p.tile) {
             if (!dead) {
@@ -968,11 +1079,12 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL, ALONE>::kPer
                             }
 #pragma unroll
                             for (int i = 0; i < kGroup; ++i) {
-                                if constexpr (FP8)
-                                    mma16816<true>(sc[i0 + i], q, e4m3x2_to_f16x2(w[i][k]),
-                                                   e4m3x2_to_f16x2(w[i][k] >> 16));
-                                else
+                                if constexpr (FP8) {
+                                    const uint2 x = key_pairs<KIND>(w[i][k]);
+                                    mma16816<true>(sc[i0 + i], q, x.x, x.y);
+                                } else {
                                     mma16816<false>(sc[i0 + i], q, w[i][2 * k], w[i][2 * k + 1]);
+                                }
                             }
                         }
                     }
@@ -982,13 +1094,24 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL, ALONE>::kPer
                 float mx0 = -INFINITY, mx1 = -INFINITY;
                 const uint64_t s0 = kPlain ? kAll : loaded & low_bits(common + j0);
                 const uint64_t s1 = kPlain ? kAll : loaded & low_bits(common + j1);
+                // The value scales of the tiles, then what their weights are multiplied by.
+                float of_value[SCALED ? NT : 1], top_scale = 0.0f;
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
+                    float sl0 = sl[0], sl1 = sl[1];
+                    if constexpr (SCALED) {
+                        const float2 tile_scales = lds64(scale_base + ring * S::kStageScales + 8 * i);
+                        sl0 *= tile_scales.x;
+                        sl1 *= tile_scales.x;
+                        // where nothing was loaded it may be anything
+                        of_value[i] = kPlain || ((loaded >> (8 * i)) & 0xFFull) ? tile_scales.y : 0.0f;
+                        top_scale = fmaxf(top_scale, of_value[i]);
+                    }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int slot = 8 * i + t + 4 * h;
-                        sc[i][h] = kPlain || ((s0 >> slot) & 1ull) ? sc[i][h] * sl[0] : -INFINITY;
-                        sc[i][2 + h] = kPlain || ((s1 >> slot) & 1ull) ? sc[i][2 + h] * sl[1] : -INFINITY;
+                        sc[i][h] = kPlain || ((s0 >> slot) & 1ull) ? sc[i][h] * sl0 : -INFINITY;
+                        sc[i][2 + h] = kPlain || ((s1 >> slot) & 1ull) ? sc[i][2 + h] * sl1 : -INFINITY;
                     }
                     mx0 = fmaxf(mx0, fmaxf(sc[i][0], sc[i][1]));
                     mx1 = fmaxf(mx1, fmaxf(sc[i][2], sc[i][3]));
@@ -1000,14 +1123,22 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL, ALONE>::kPer
                 mx0 = fmaxf(mx0, __shfl_xor_sync(~0u, mx0, 2));
                 mx1 = fmaxf(mx1, __shfl_xor_sync(~0u, mx1, 1));
                 mx1 = fmaxf(mx1, __shfl_xor_sync(~0u, mx1, 2));
-                if (__any_sync(~0u, mx0 > m_run[0] + S::kRescaleSlack || mx1 > m_run[1] + S::kRescaleSlack)) {
+                if (__any_sync(~0u, mx0 > m_run[0] + S::kRescaleSlack || mx1 > m_run[1] + S::kRescaleSlack) ||
+                    (SCALED && top_scale > unit)) {
                     const float n0 = fmaxf(m_run[0], mx0), n1 = fmaxf(m_run[1], mx1);
-                    const float a0 = n0 == -INFINITY ? 1.0f : fast_exp2(m_run[0] - n0);
-                    const float a1 = n1 == -INFINITY ? 1.0f : fast_exp2(m_run[1] - n1);
+                    float a0 = n0 == -INFINITY ? 1.0f : fast_exp2(m_run[0] - n0);
+                    float a1 = n1 == -INFINITY ? 1.0f : fast_exp2(m_run[1] - n1);
                     m_run[0] = n0;
                     m_run[1] = n1;
                     l_run[0] *= a0;
                     l_run[1] *= a1;
+                    if (SCALED && top_scale > unit) {           // the next power of two, at most 2^126
+                        const float more = __uint_as_float(min((__float_as_uint(top_scale) + 0x7FFFFFu) & 0x7F800000u, 253u << 23));
+                        const float less = unit * reciprocal_of_power(more);
+                        unit = more;
+                        a0 *= less;
+                        a1 *= less;
+                    }
 #pragma unroll
                     for (int n = 0; n < D / 8; ++n) {
                         o[n][0] *= a0;
@@ -1015,6 +1146,12 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL, ALONE>::kPer
                         o[n][2] *= a1;
                         o[n][3] *= a1;
                     }
+                }
+                if constexpr (SCALED) {
+                    const float per_unit = reciprocal_of_power(unit);
+#pragma unroll
+                    for (int i = 0; i < NT; ++i)
+                        of_value[i] *= per_unit;
                 }
                 const float ref0 = m_run[0] == -INFINITY ? 0.0f : m_run[0] - S::kLift;
                 const float ref1 = m_run[1] == -INFINITY ? 0.0f : m_run[1] - S::kLift;
@@ -1059,13 +1196,15 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL, ALONE>::kPer
                     for (int k = 0; k < 4; ++k) {
                         const int i = 2 * k2 + (k >> 1), c = 2 * (k & 1);
                         const float lo = weight(i, c, km, 8 * (k >> 1)), hi = weight(i, c + 1, km, 8 * (k >> 1));
-                        if constexpr (FP8)
+                        if constexpr (SCALED)
+                            pa[k] = pack_f16(lo * of_value[i], hi * of_value[i]);
+                        else if constexpr (FP8)
                             pa[k] = pack_f16(lo, hi);
                         else
                             split_bf16(lo, hi, pa[k], pb[k]);
                     }
                     const uint32_t vrow = sb + ((mi & 1) ? tile_off[2 * k2 + 1] : tile_off[2 * k2]) + vsw * 128u;
-                    pv_accumulate<FP8, D, !kPlain>(o, pa, pb, vrow, bstride, mi, vsw, both(km, t), both(km, t + 8));
+                    pv_accumulate<KIND, D, !kPlain>(o, pa, pb, vrow, bstride, mi, vsw, both(km, t), both(km, t + 8));
                 }
                 // ---- The newest query_len - 1 tokens, which only some rows see:
                 // one at a time in fp32, so that a value that is not a number
@@ -1080,6 +1219,10 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL, ALONE>::kPer
                             if ((s >> 3) == i) {
                                 p0 = (s & 4) ? sc[i][1] : sc[i][0];
                                 p1 = (s & 4) ? sc[i][3] : sc[i][2];
+                                if constexpr (SCALED) {
+                                    p0 *= of_value[i];
+                                    p1 *= of_value[i];
+                                }
                                 off = tile_off[i];
                             }
                         p0 = __shfl_sync(~0u, p0, (lane & ~3) | (s & 3));
@@ -1092,9 +1235,9 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL, ALONE>::kPer
                             const int idx = kFirst + c;
                             const uint32_t w = lds32(vrow + (idx >> 3) * bstride + (((idx & 7) ^ (s & 7)) << 4));
                             if constexpr (FP8) {
-                                const uint32_t a = e4m3x2_to_f16x2(w), b = e4m3x2_to_f16x2(w >> 16);
-                                const float2 va = __half22float2(*reinterpret_cast<const __half2 *>(&a));
-                                const float2 vb = __half22float2(*reinterpret_cast<const __half2 *>(&b));
+                                const uint2 x = key_pairs<KIND>(w);
+                                const float2 va = __half22float2(*reinterpret_cast<const __half2 *>(&x.x));
+                                const float2 vb = __half22float2(*reinterpret_cast<const __half2 *>(&x.y));
                                 if (see0) {
                                     o[2 * c][0] += p0 * va.x;
                                     o[2 * c + 1][0] += p0 * va.y;
@@ -1152,9 +1295,17 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL, ALONE>::kPer
         // ---- The unit's result, or its piece's.
         const volatile Segment &at = state->here.seg;
         const Segment seg = {at.request, at.group, at.first, at.last, at.tiles, at.len};
-        const int v = static_cast<const volatile WarpState *>(state)->number;
+        const int v = static_cast<const volatile WarpState<REGIONS> *>(state)->number;
         const int64_t out_row0 = static_cast<int64_t>(seg.request) * p.query_len * p.groups + seg.group;
         auto row_of = [&](int r) { return out_row0 + static_cast<int64_t>(token_of(r)) * p.groups; };
+        auto gate_of = [&](int r, int h) {      // of query row r, head h
+            const unsigned row = static_cast<unsigned>(seg.request);
+            const unsigned token = REGIONS ? quotient(row, p.region_groups_inv) : 0u;
+            const int group = REGIONS ? static_cast<int>(row - token * p.region_groups) : seg.group;
+            return gate_factor(p.gate[(REGIONS ? static_cast<int64_t>(token)
+                                               : static_cast<int64_t>(seg.request) * p.query_len + token_of(r)) * p.g_s0 +
+                                      static_cast<int64_t>(group * H + h) * p.g_s1]);
+        };
         const bool begins = seg.first == 0, ends = seg.last == seg.tiles;
         const bool whole = begins && ends;
         const int64_t piece = static_cast<int64_t>(v) * 2 + (begins ? 1 : 0);
@@ -1184,6 +1335,9 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL, ALONE>::kPer
             constexpr int kStride = kRows * (D + 4) <= kOut ? D + 4 : D;
             static_assert(kRows * kStride <= kOut, "merge buffer");
             float *outs = reinterpret_cast<float *>(smem), *stats = reinterpret_cast<float *>(smem + S::kStatsOff);
+            float *units = reinterpret_cast<float *>(smem + S::kUnitsOff);
+            if (SCALED && mt == 0 && lane == 0)
+                units[worker] = unit;
             if constexpr (MT > 1)
                 __syncthreads();                // all of the worker's warps are through its last stage
             else
@@ -1232,11 +1386,15 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL, ALONE>::kPer
                 const int h = r - token_of(r) * H;
                 uint16_t *out = nullptr;
                 float f = 1.0f;
+                if constexpr (SCALED) {
+#pragma unroll
+                    for (int w = 0; w < S::kWorkers; ++w)
+                        st[w].x *= units[w];
+                }
                 if constexpr (ALONE) {
                     f = vs;
                     if (p.gate)
-                        f *= gate_factor(p.gate[(static_cast<int64_t>(seg.request) * p.query_len + token_of(r)) * p.g_s0 +
-                                                static_cast<int64_t>(seg.group * H + h) * p.g_s1]);
+                        f *= gate_of(r, h);
                     out = p.output + row_of(r) * p.o_s0 + h * p.o_s1;
                 }
                 float *part = p.partial + (first * R + r) * D;
@@ -1287,11 +1445,12 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL, ALONE>::kPer
             const int h = r - token_of(r) * H;
             const int64_t row = row_of(r);
             float f = empty ? 0.0f : 1.0f / L;
+            if constexpr (SCALED)
+                f *= unit;
             if (whole) {
                 f *= vs;
                 if (p.gate)
-                    f *= gate_factor(p.gate[(static_cast<int64_t>(seg.request) * p.query_len + token_of(r)) * p.g_s0 +
-                                            static_cast<int64_t>(seg.group * H + h) * p.g_s1]);
+                    f *= gate_of(r, h);
                 if (t == 0 && p.lse)
                     p.lse[row * p.l_s0 + h * p.l_s1] = lse2 * kLn2;
             } else if (t == 0) {
@@ -1349,8 +1508,8 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL, ALONE>::kPer
     // Requests without tokens: zeros.  A CTA alone with a unit knows its own.
     for (int q = blockIdx.x; q < (ALONE ? p.requests * p.groups : p.requests); q += gridDim.x) {
         const int request = ALONE ? state->here.seg.request : q, g0 = ALONE ? state->here.seg.group : 0;
-        const int len = ALONE ? state->here.seg.len : Walk::length(p, q);
-        if (threadIdx.x == 0 && (!ALONE || len == p.cap) && p.seq_lens[request * p.len_s] > p.cap)
+        const int len = ALONE ? state->here.seg.len : Line::length(p, q);
+        if (!REGIONS && threadIdx.x == 0 && (!ALONE || len == p.cap) && p.seq_lens[request * p.len_s] > p.cap)
             atomicOr(p.flags, SDA_FLAG_BOUNDS);
         if (len != 0)
             continue;
@@ -1376,40 +1535,51 @@ __global__ void __launch_bounds__(kThreads, Shape<FP8, D, MT, FULL, ALONE>::kPer
     }
 }
 
-template <bool FP8, int D, int MT, bool FULL, bool ALONE>
+template <int KIND, int D, int MT, bool FULL, bool ALONE, bool REGIONS>
 sda_status launch_shape(const CUtensorMap &tmap, const Params &p, void *stream)
 {
-    using S = Shape<FP8, D, MT, FULL, ALONE>;
+    using S = Shape<KIND, D, MT, FULL, ALONE, REGIONS>;
     static size_t raised[64] = {};
-    if (!raise_smem(sda_paged_kernel<FP8, D, MT, FULL, ALONE>, S::kBytes, raised))
+    if (!raise_smem(sda_paged_kernel<KIND, D, MT, FULL, ALONE, REGIONS>, S::kBytes, raised))
         return SDA_ERR_CUDA;
-    return launch_pdl(sda_paged_kernel<FP8, D, MT, FULL, ALONE>, dim3(static_cast<unsigned>(p.ctas)), dim3(kThreads),
+    return launch_pdl(sda_paged_kernel<KIND, D, MT, FULL, ALONE, REGIONS>, dim3(static_cast<unsigned>(p.ctas)), dim3(kThreads),
                       S::kBytes, stream, tmap, p);
 }
 
-template <bool FP8, int D, int MT>
+template <int KIND, int D, int MT, bool REGIONS>
 sda_status launch_tiles(const CUtensorMap &tmap, const Params &p, void *stream)
 {
     if (p.cta_units)
-        return p.piece == Shape<FP8, D, MT, true, true>::kSlots ? launch_shape<FP8, D, MT, true, true>(tmap, p, stream)
-                                                                : launch_shape<FP8, D, MT, false, true>(tmap, p, stream);
-    return p.piece == Shape<FP8, D, MT, true>::kSlots ? launch_shape<FP8, D, MT, true, false>(tmap, p, stream)
-                                                      : launch_shape<FP8, D, MT, false, false>(tmap, p, stream);
+        return p.piece == Shape<KIND, D, MT, true, true>::kSlots ? launch_shape<KIND, D, MT, true, true, REGIONS>(tmap, p, stream)
+                                                                 : launch_shape<KIND, D, MT, false, true, REGIONS>(tmap, p, stream);
+    return p.piece == Shape<KIND, D, MT, true>::kSlots ? launch_shape<KIND, D, MT, true, false, REGIONS>(tmap, p, stream)
+                                                       : launch_shape<KIND, D, MT, false, false, REGIONS>(tmap, p, stream);
 }
 
-template <bool FP8, int D>
+template <int KIND, int D>
 sda_status launch_dim(const CUtensorMap &tmap, const Params &p, void *stream)
 {
     const int tiles = tiles_of_rows(p.rows);
-    return tiles == 1   ? launch_tiles<FP8, D, 1>(tmap, p, stream)
-           : tiles == 2 ? launch_tiles<FP8, D, 2>(tmap, p, stream)
-                        : launch_tiles<FP8, D, 4>(tmap, p, stream);
+    return tiles == 1   ? launch_tiles<KIND, D, 1, false>(tmap, p, stream)
+           : tiles == 2 ? launch_tiles<KIND, D, 2, false>(tmap, p, stream)
+                        : launch_tiles<KIND, D, 4, false>(tmap, p, stream);
+}
+
+// Regions: a row of at most 16 heads is one tile.
+template <int KIND, int D>
+sda_status launch_regions(const CUtensorMap &tmap, const Params &p, void *stream)
+{
+    return launch_tiles<KIND, D, 1, true>(tmap, p, stream);
 }
 
 // One translation unit per head size and cache type.
 using Launch = sda_status(const CUtensorMap &tmap, const Params &p, void *stream);
 Launch launch_bf16_64, launch_bf16_128, launch_bf16_192, launch_bf16_256;
 Launch launch_fp8_64, launch_fp8_128, launch_fp8_192, launch_fp8_256;
+Launch launch_qe4m3_64, launch_qe4m3_128, launch_qe4m3_192, launch_qe4m3_256;
+Launch launch_qint8_64, launch_qint8_128, launch_qint8_192, launch_qint8_256;
+Launch regions_qe4m3_64, regions_qe4m3_128, regions_qe4m3_192, regions_qe4m3_256;
+Launch regions_qint8_64, regions_qint8_128, regions_qint8_192, regions_qint8_256;
 
 }  // namespace paged
 }  // namespace sda

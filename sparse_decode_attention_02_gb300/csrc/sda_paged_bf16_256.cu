@@ -6,7 +6,7 @@ namespace paged {
 
 __attribute__((visibility("hidden"))) sda_status launch_bf16_256(const CUtensorMap &tmap, const Params &p, void *stream)
 {
-    return launch_dim<false, 256>(tmap, p, stream);
+    return launch_dim<kBf16, 256>(tmap, p, stream);
 }
 
 }  // namespace paged

@@ -6,7 +6,7 @@ namespace paged {
 
 __attribute__((visibility("hidden"))) sda_status launch_fp8_64(const CUtensorMap &tmap, const Params &p, void *stream)
 {
-    return launch_dim<true, 64>(tmap, p, stream);
+    return launch_dim<kE4m3, 64>(tmap, p, stream);
 }
 
 }  // namespace paged

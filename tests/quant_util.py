@@ -97,3 +97,26 @@ def read(elements, scales, table, starts, first, rows):
             s = np.repeat(scales[page, :, t % B // S], D2 // 2, -1)
             out[r] = torch.from_numpy(elements[page, :, t % B].astype(np.float32) * s).bfloat16()
     return out, flags
+
+
+def attend(x, k, v, scale):
+    """Float64 attention of query rows x [H, D] over tokens: (output, lse, spread, slack) as step_util.paged_attention
+    gives them.  k and v are decoded: 2^-22 more for the key scale's two roundings."""
+    H, D = x.shape
+    if not len(k):
+        return torch.zeros(H, D, dtype=torch.float64), torch.full((H,), -np.inf, dtype=torch.float64), \
+            torch.zeros(H, D, dtype=torch.float64), torch.zeros(H, dtype=torch.float64)
+    s = x @ k.T * scale
+    lse = torch.logsumexp(s, -1)
+    w = torch.exp(s - lse[:, None])
+    slack = (x.abs() @ k.abs().T * abs(scale)).amax(-1) * (D / 16 + 5) * 2.0 ** -22
+    return w @ v, lse, w @ v.abs(), slack
+
+
+def attention_bound(o, spread, slack, most, tokens, gated=False):
+    """|kernel - exact| <= one bf16 rounding of the output (half a step: 2^-8), the weights' rounding to fp16
+    (2^-11; twice, for the scale's product in fp32 and the exponential: 2^-20), the logits' error in numerator and
+    sum; `most`: what an element of the largest value scale can stand for, whose weights below 2^-27 of the largest are
+    off by 2^-38 of it; with a gate one bf16 step more where the two sigmoids round apart."""
+    weights = 2.0 ** -11 + 2.0 ** -19 + 2 * slack[..., None]
+    return o.abs() * (2.0 ** -8 + (2.0 ** -7 if gated else 0.0)) * 1.01 + spread * weights + most * tokens * 2.0 ** -38 + 1e-37

@@ -108,12 +108,90 @@ def test_read_refusals(lib):
     assert read(lib, T=0, key=None) == OK
 
 
+def paged(lib, reqs=3, ql=2, G=2, H=8, D=64, W=5, scale=0.1, ws=1 << 24, wsb=None, like=None, **change):
+    rows = reqs * ql * G
+    like = cache_and_scales(G=G, D=D, **(like or {}))
+    d = dict(q=t(BF16, (rows, H, D))) | like | dict(table=t(I32, (reqs, W)), lens=t(I32, (reqs,)), out=t(BF16, (rows, H, D)),
+                                                    lse=t(F32, (rows, H)), gate=None) | change
+    a = [ref(x) for x in d.values()]
+    need = lib.sparse_decode_paged_workspace_bytes(H, ql, D)
+    return lib.sparse_decode_quantised_paged_attention(*a[:7], scale, ql, a[7], ws, need if wsb is None else wsb, None)
+
+
+def regions(lib, toks=6, ql=2, G=2, H=8, D=64, R=4, W=5, rt=0, scale=0.1, ws=1 << 24, wsb=None, like=None, **change):
+    rows = toks * G
+    like = cache_and_scales(G=G, D=D, **(like or {}))
+    d = dict(q=t(BF16, (rows, H, D))) | like | dict(ids=t(I32, (rows, R)), table=t(I32, (toks // ql, W)), pos=t(I32, (rows,)),
+                                                    act=t(5, (rows,)), out=t(BF16, (rows, H, D)), lse=t(F32, (rows, H)),
+                                                    gate=None) | change
+    a = [ref(x) for x in d.values()]
+    need = lib.sparse_decode_paged_workspace_bytes(H, 1, D)
+    return lib.sparse_decode_quantised_attention(*a[:9], scale, ql, a[9], 1, rt, ws, need if wsb is None else wsb, None)
+
+
+@pytest.mark.parametrize("entry", [paged, regions])
+@pytest.mark.parametrize("which", range(len(CACHES)))
+def test_cache_refusals_of_attention(lib, entry, which):
+    status, change = CACHES[which]
+    assert entry(lib, **change) == status
+
+
+@pytest.mark.parametrize("entry", [paged, regions])
+def test_attention_refusals(lib, entry):
+    for name, bad in dict(q=t(F32, (12, 8, 64)), table=t(I64, (3, 5)), out=t(BF16, (12, 8, 32)), lse=t(F32, (12, 7)),
+                          gate=t(BF16, (6, 15))).items():
+        assert entry(lib, **{name: bad}) == INV, name
+    assert entry(lib, q=None) == entry(lib, table=None) == entry(lib, out=None) == INV
+    assert entry(lib, table=t(I32, (2, 5))) == INV
+    assert entry(lib, table=t(I32, (3, 5), (10, 2))) == INV
+    assert entry(lib, q=t(BF16, (12, 8, 64), (1024, 128, 2))) == INV
+    assert entry(lib, lse=t(F32, (12, 8), (0, 1))) == INV
+    assert entry(lib, out=t(BF16, (12, 8, 64), (0, 64, 1))) == INV
+    assert entry(lib, scale=float("inf")) == INV
+    assert entry(lib, D=96) == UNS
+    assert entry(lib, ws=None) == WS
+    assert entry(lib, ws=(1 << 24) + 128) == WS
+    assert entry(lib, wsb=255) == WS
+    assert entry(lib, q=t(BF16, (12, 8, 64), addr=0)) == INV
+
+
+def test_paged_refusals(lib):
+    assert paged(lib, lens=t(F32, (3,))) == INV
+    assert paged(lib, lens=t(I32, (4,))) == INV                              # rows are not 4 requests'
+    assert paged(lib, lens=None) == INV
+    assert paged(lib, ql=0) == INV
+    assert paged(lib, H=33) == UNS                                           # more than 64 query rows
+    assert paged(lib, reqs=0) == OK
+
+
+def test_region_refusals(lib):
+    for name, bad in dict(ids=t(I64, (12, 4)), pos=t(I64, (12,)), act=t(I32, (12,))).items():
+        assert regions(lib, **{name: bad}) == INV, name
+    assert regions(lib, ids=None) == regions(lib, pos=None) == regions(lib, act=None) == INV
+    assert regions(lib, ids=t(I32, (11, 4))) == regions(lib, pos=t(I32, (11,))) == regions(lib, act=t(5, (11,))) == INV
+    assert regions(lib, ids=t(I32, (12, 4), (8, 2))) == INV
+    assert regions(lib, rt=-8) == INV
+    assert regions(lib, toks=5, ql=5, q=t(BF16, (11, 8, 64)), out=t(BF16, (11, 8, 64)), lse=None) == INV
+    assert regions(lib, H=17) == UNS
+    assert regions(lib, rt=12) == UNS                                        # gcd with pages of 16 is 4
+    assert regions(lib, rt=1 << 25) == UNS
+    assert regions(lib, R=1 << 17, rt=1 << 15) == UNS                        # more tokens than 31 bits count
+    assert regions(lib, R=(1 << 20) + 1) == UNS
+    assert regions(lib, toks=0) == OK
+    assert regions(lib, toks=0, rt=40) == regions(lib, toks=0, R=0) == OK    # gcd 8; nothing listed
+
+
 def host_calls(ws=None):
     bf, i32 = torch.bfloat16, torch.int32
     cache, scales = torch.zeros(3, 1, 16, 128, dtype=torch.int8), torch.zeros(3, 1, 2, 2)
     x, n, table = torch.zeros(4, 1, 64, dtype=bf), torch.ones(4, dtype=i32), torch.zeros(4, 2, dtype=i32)
     slots = torch.zeros(4, dtype=torch.int64)
-    return dict(append=lambda: sda.sparse_decode_quantised_append(x, x, slots, cache, scales, workspace=ws),
+    q, on = torch.zeros(4, 8, 64, dtype=bf), torch.ones(4, dtype=torch.bool)
+    return dict(paged=lambda: sda.sparse_decode_quantised_paged_attention(q, cache, scales, table, n, q.clone(), scale=0.1,
+                                                                          workspace=ws),
+                regions=lambda: sda.sparse_decode_quantised_attention(q, cache, scales, table, table, n, on, q.clone(), scale=0.1,
+                                                                      workspace=ws),
+                append=lambda: sda.sparse_decode_quantised_append(x, x, slots, cache, scales, workspace=ws),
                 read=lambda: sda.sparse_decode_quantised_read(cache, scales, table, n, x, x, workspace=ws))
 
 
