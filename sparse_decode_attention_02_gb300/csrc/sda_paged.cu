@@ -462,6 +462,7 @@ sda_status run_call(const Call &c)
         p.scales = static_cast<const float *>(c.scales->data);
         p.s_s0 = c.scales->stride[0], p.s_s1 = c.scales->stride[1], p.s_s2 = c.scales->stride[2];
         p.span_inv = inverse_of(static_cast<unsigned>(quantised.span));
+        p.one_scale = quantised.span % p.piece == 0;
     }
     p.output = static_cast<uint16_t *>(const_cast<void *>(output->data));
     p.o_s0 = output->stride[0];

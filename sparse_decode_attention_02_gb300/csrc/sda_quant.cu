@@ -25,6 +25,7 @@
 #include "sda_quant.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace {
 
@@ -33,7 +34,7 @@ using namespace sda;
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxChunk = 64;                   // rows that a CTA looks at for runs
-constexpr int kKept = 8;                        // 8-element pieces that a thread keeps between the passes
+constexpr int kKept = 7;                        // 8-element pieces that a thread keeps between the passes
 
 struct AppendParams {
     const uint16_t *key, *value;
@@ -44,8 +45,16 @@ struct AppendParams {
     float *scales;
     int64_t s_s0, s_s1, s_s2;
     unsigned int *flags;
-    int64_t cache_slots;                        // pages * block
+    uint32_t cache_slots;                       // pages * block
+    unsigned long long block_inv, span_inv, vecs_inv;       // inverse_of a page's places, a block's, 8-element pieces of a row
     int tokens, groups, dim, block, span, chunk;
+};
+
+// A run of rows in one block, of one head's keys or values.
+struct Run {
+    uint8_t *cache;                             // the block's first place
+    float *scale;
+    int row, place, length;                     // first row and place; (within the CTA's window of rows)
 };
 
 // Four fp32 values to E4M3 bytes, rounded to nearest even, saturated at 448.
@@ -102,13 +111,16 @@ __device__ __forceinline__ float least_scale(float largest)
     }
 }
 
-// The larger |x| of the bf16 pairs in a and b, half by half, as bits.
+// The larger |x| of the bf16 pairs in a and b, half by half and with any sign; not a
+// number if one is not.
 __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b)
 {
-    return __vmaxu2(a, b & 0x7FFF7FFFu);
+    uint32_t r;
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
 
-// The same over finite values only.
+// The same over finite values only, as bits.
 __device__ __forceinline__ uint32_t larger_finite(uint32_t a, uint32_t b)
 {
     b &= 0x7FFF7FFFu;
@@ -116,50 +128,141 @@ __device__ __forceinline__ uint32_t larger_finite(uint32_t a, uint32_t b)
     return __vmaxu2(a, b);
 }
 
-template <bool INT8>
+// Eight values over the scale, as elements.  `inverse`: the scale's reciprocal, in fp32.
+template <bool INT8, bool POWER_OF_TWO>
 __device__ __forceinline__ uint2 quantise(const uint4 &v, float scale, float inverse)
 {
-    // x / scale; where the scale is a power of two the product by its reciprocal is the same
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     float x[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 8; ++i)
         x[i] = __uint_as_float(i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
-        x[i] = inverse != 0.0f ? x[i] * inverse : __fdiv_rn(x[i], scale);
+    if constexpr (INT8) {
+        // The product by the reciprocal is off by 2^-23 of itself at most, the quotient in
+        // fp32 by 2^-24: away from a border by more than 2^-15 (of values up to 127) both
+        // round to the same integer.  1.5 * 2^23 added to it leaves it in the low bits.
+        constexpr float kInteger = 12582912.0f;
+        uint32_t bits[8];
+        bool clear = true;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float y = x[i] * inverse, z = y + kInteger;
+            clear = clear && fabsf(y - (z - kInteger)) < 0.5f - 0x1p-15f;       // not so if y is not finite
+            bits[i] = __float_as_uint(z);
+        }
+        if (clear)
+            return make_uint2(bytes_of<0x5410u>(bytes_of<0x0040u>(bits[0], bits[1]), bytes_of<0x0040u>(bits[2], bits[3])),
+                              bytes_of<0x5410u>(bytes_of<0x0040u>(bits[4], bits[5]), bytes_of<0x0040u>(bits[6], bits[7])));
+    }
+    if constexpr (!INT8 && POWER_OF_TWO) {             // the quotient, exactly (or next to 0, and less than E4M3 has)
+        const __nv_bfloat162 f = __bfloat162bfloat162(__float2bfloat16_rn(inverse));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]), f);
+            const uint32_t z = *reinterpret_cast<const uint32_t *>(&y);
+            x[2 * i] = __uint_as_float(z << 16);
+            x[2 * i + 1] = __uint_as_float(z & 0xFFFF0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            x[i] = __fdiv_rn(x[i], scale);
     }
     return make_uint2(to_elements<INT8>(x[0], x[1], x[2], x[3]), to_elements<INT8>(x[4], x[5], x[6], x[7]));
 }
 
+// A thread's 8-element pieces of a run.  WIDE, threads for a row or more: each keeps to
+// a place in the row, and those beyond whole rows have none.  Else a row's pieces by turns.
+template <class T, bool WIDE>
+struct Pieces {
+    T *at;
+    int row, vec;
+    int64_t step;                               // in elements: to the next piece
+    int rows, threads, vecs;                    // rows of all threads at a time; pieces of a row
+    int64_t wrap;                               // (not WIDE) more, where the next is the first of its row
+
+    __device__ __forceinline__ Pieces(T *base, int64_t stride, int tid, int threads, const AppendParams &p)
+        : threads(threads), vecs(p.dim / 8)
+    {
+        rows = static_cast<int>(quotient(threads, p.vecs_inv));
+        row = WIDE ? static_cast<int>(quotient(tid, p.vecs_inv)) : 0;
+        vec = tid - row * vecs;
+        at = base + row * stride + 8 * vec;
+        if (WIDE && row >= rows)
+            row = INT32_MAX / 2;
+        step = WIDE ? rows * stride : 8 * threads;
+        wrap = WIDE ? 0 : stride - 8 * ((vecs - vec + threads - 1) / threads) * threads;
+    }
+
+    __device__ __forceinline__ void next()
+    {
+        at += step;
+        if constexpr (WIDE) {
+            row += rows;
+        } else {
+            vec += threads;
+            if (vec >= vecs) {
+                vec %= threads;
+                at += wrap;
+                ++row;
+            }
+        }
+    }
+};
+
 template <bool INT8>
-__global__ void __launch_bounds__(kThreads) sda_quantised_append_kernel(const __grid_constant__ AppendParams p)
+__global__ void __launch_bounds__(kThreads, 4) sda_quantised_append_kernel(const __grid_constant__ AppendParams p)
 {
-    __shared__ int runs[kMaxChunk];             // first rows of the runs that begin in this chunk
+    __shared__ Run runs[kMaxChunk];             // that begin in this chunk
+    __shared__ uint32_t goes_on[kWarps];        // rows of the window that continue the one before, a bit each
     __shared__ int count;
     __shared__ uint32_t tops[2][kWarps];        // largest element of each warp, by turns
     pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int units = 2 * p.groups;
-    const int unit = static_cast<int>(blockIdx.x % static_cast<unsigned>(units));
-    const int row0 = static_cast<int>(blockIdx.x / static_cast<unsigned>(units)) * p.chunk;
+    const unsigned units = 2 * p.groups;
+    const int unit = static_cast<int>(blockIdx.x % units);
+    const int row0 = static_cast<int>(blockIdx.x / units) * p.chunk;
     const bool value = unit & 1;
     const int group = unit >> 1;
-    auto valid = [&](int64_t slot) { return slot >= 0 && slot < p.cache_slots; };
 
-    // ---- Runs: rows whose neighbour before them lies in another block.
+    // ---- Runs.  The window is a row a thread; a run begins where the row before lies in
+    // another block (or nowhere).
+    constexpr uint32_t kNone = ~0u;             // not a slot: there are fewer
+    auto slot_of = [&](int r) {
+        const int64_t slot = r >= 0 && r < p.tokens ? p.slots[r] : -1;
+        if (static_cast<uint64_t>(slot) < p.cache_slots)
+            return static_cast<uint32_t>(slot);
+        if (slot != -1 && p.flags)
+            atomicOr(p.flags, SDA_FLAG_BOUNDS);
+        return kNone;
+    };
     if (threadIdx.x == 0)
         count = 0;
+    const int r = row0 + static_cast<int>(threadIdx.x);         // < 2^29
+    const uint32_t slot = slot_of(r), before = slot_of(r - 1);
+    const bool joins = slot != kNone && before != kNone && quotient(slot, p.span_inv) == quotient(before, p.span_inv);
+    const unsigned on = __ballot_sync(~0u, joins && slot == before + 1);
+    if (lane == 0)
+        goes_on[warp] = on;
     __syncthreads();
-    if (static_cast<int>(threadIdx.x) < p.chunk && row0 + static_cast<int>(threadIdx.x) < p.tokens) {
-        const int r = row0 + threadIdx.x;
-        const int64_t slot = p.slots[r], before = r > 0 ? p.slots[r - 1] : -1;
-        if (valid(slot)) {
-            const bool joins = valid(before) && before / p.span == slot / p.span;
-            if (!joins)
-                runs[atomicAdd(&count, 1)] = r;
-            else if (slot != before + 1 && p.flags)             // the block's rows are not in order: left out
-                atomicOr(p.flags, SDA_FLAG_BOUNDS);
-        } else if (slot != -1 && p.flags) {
+    if (static_cast<int>(threadIdx.x) < p.chunk && slot != kNone) {
+        if (!joins) {
+            const uint32_t page = quotient(slot, p.block_inv), off = slot - page * p.block;
+            const uint32_t part = quotient(off, p.span_inv), place = off - part * p.span;
+            int length = 1, i = static_cast<int>(threadIdx.x) + 1;              // rows of the window from here that go on
+            while (i < kThreads) {
+                const uint32_t stops = ~goes_on[i >> 5] >> (i & 31);
+                const int some = stops ? __ffs(stops) - 1 : 32;
+                length += min(some, 32 - (i & 31));
+                if (stops && some < 32 - (i & 31))
+                    break;
+                i = (i | 31) + 1;
+            }
+            runs[atomicAdd(&count, 1)] = {p.cache + page * p.c_s0 + group * p.c_s1 + (value ? p.dim : 0) + (off - place) * p.c_s2,
+                                          p.scales + page * p.s_s0 + group * p.s_s1 + part * p.s_s2 + (value ? 1 : 0), r,
+                                          static_cast<int>(place), length};
+        } else if (slot != before + 1 && p.flags) {             // the block's rows are not in order: left out
             atomicOr(p.flags, SDA_FLAG_BOUNDS);
         }
     }
@@ -175,26 +278,25 @@ __global__ void __launch_bounds__(kThreads) sda_quantised_append_kernel(const __
             asm volatile("bar.sync %0, %1;" ::"r"(1 + mine), "r"(threads) : "memory");
     };
 
-    const int vecs = p.dim / 8;                 // 8-element pieces of a row
-    const int row_step = threads / vecs, vec_step = threads - row_step * vecs;
     const uint16_t *src = value ? p.value + group * p.v_s1 : p.key + group * p.k_s1;
     const int64_t src_row = value ? p.v_s0 : p.k_s0;
     int turn = 0;
-    for (int i = mine; i < n; i += teams, turn ^= 1) {
-        const int r0 = runs[i];
-        const int64_t slot = p.slots[r0];
-        const int64_t page = slot / p.block;
-        const int off = static_cast<int>(slot - page * p.block), part = off / p.span, place = off - part * p.span;
-        float *at = p.scales + page * p.s_s0 + group * p.s_s1 + part * p.s_s2 + (value ? 1 : 0);
+    auto run = [&](int i, auto wide) {
+        using In = Pieces<const uint16_t, decltype(wide)::value>;
+        using Out = Pieces<uint8_t, decltype(wide)::value>;
+        const Run &its = runs[i];
+        const int r0 = its.row, place = its.place;
+        float *at = its.scale;
         const float had = place > 0 ? *at : 0.0f;
-        // its length: rows with consecutive slots, up to the block's end
-        int length = min(p.span - place, p.tokens - r0);
-        for (int k = 0; k < length; k += 32) {
-            const bool goes_on = k + lane < length && p.slots[r0 + k + lane] == slot + k + lane;
-            const unsigned m = __ballot_sync(~0u, goes_on);
-            if (m != ~0u) {
-                length = min(length, k + __ffs(~m) - 1);
-                break;
+        int length = its.length;
+        if (r0 - row0 + length >= kThreads) {   // it goes on behind the window, up to the block's end
+            const int64_t first = p.slots[r0];
+            for (int most = min(p.span - place, p.tokens - r0); length < most;) {
+                const bool one = length + lane < most && p.slots[r0 + length + lane] == first + length + lane;
+                const unsigned m = __ballot_sync(~0u, one);
+                length += m == ~0u ? 32 : __ffs(~m) - 1;
+                if (m != ~0u)
+                    break;
             }
         }
 
@@ -202,40 +304,29 @@ __global__ void __launch_bounds__(kThreads) sda_quantised_append_kernel(const __
         const uint16_t *rows = src + r0 * src_row;
         uint4 kept[kKept];
         uint32_t top = 0;
-        int row = tid / vecs, vec = tid - row * vecs;
-        auto step = [&](int &row, int &vec) {
-            row += row_step;
-            vec += vec_step;
-            if (vec >= vecs) {
-                vec -= vecs;
-                ++row;
+        auto top_of = [](uint32_t top, const uint4 &v) { return larger(larger(larger(larger(top, v.x), v.y), v.z), v.w); };
+        {
+            In in(rows, src_row, tid, threads, p);
+#pragma unroll
+            for (int k = 0; k < kKept; ++k) {
+                kept[k] = in.row < length ? *reinterpret_cast<const uint4 *>(in.at) : make_uint4(0, 0, 0, 0);
+                in.next();
             }
-        };
-        const int row_first = row, vec_first = vec;
+            const bool rest = in.row < length;
 #pragma unroll
-        for (int k = 0; k < kKept; ++k) {
-            kept[k] = make_uint4(0, 0, 0, 0);
-            if (row < length)
-                kept[k] = *reinterpret_cast<const uint4 *>(rows + row * src_row + 8 * vec);
-            step(row, vec);
-        }
-        const int row_rest = row, vec_rest = vec;
-#pragma unroll
-        for (int k = 0; k < kKept; ++k)
-            top = larger(larger(larger(larger(top, kept[k].x), kept[k].y), kept[k].z), kept[k].w);
-        for (; row < length; step(row, vec)) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(rows + row * src_row + 8 * vec);
-            top = larger(larger(larger(larger(top, v.x), v.y), v.z), v.w);
+            for (int k = 0; k < kKept; ++k)
+                top = top_of(top, kept[k]);
+            if (rest)
+                for (; in.row < length; in.next())
+                    top = top_of(top, *reinterpret_cast<const uint4 *>(in.at));
         }
         auto over_team = [&](uint32_t x, int which) {
-            x = __reduce_max_sync(~0u, max(x & 0xFFFFu, x >> 16));
+            x = __reduce_max_sync(~0u, max(x & 0x7FFFu, (x >> 16) & 0x7FFFu));
             if (team > 1) {
                 if (lane == 0)
                     tops[which][warp] = x;
                 together();
-                x = 0;
-                for (int w = 0; w < team; ++w)
-                    x = max(x, tops[which][mine * team + w]);
+                x = __reduce_max_sync(~0u, lane < team ? tops[which][mine * team + lane] : 0u);
             }
             return x;
         };
@@ -245,10 +336,8 @@ __global__ void __launch_bounds__(kThreads) sda_quantised_append_kernel(const __
                 atomicOr(p.flags, SDA_FLAG_NONFINITE);
             together();                         // `tops` has been read
             top = 0;
-            row = row_first;
-            vec = vec_first;
-            for (; row < length; step(row, vec)) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(rows + row * src_row + 8 * vec);
+            for (In in(rows, src_row, tid, threads, p); in.row < length; in.next()) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(in.at);
                 top = larger_finite(larger_finite(larger_finite(larger_finite(top, v.x), v.y), v.z), v.w);
             }
             top = over_team(top, turn);
@@ -256,19 +345,18 @@ __global__ void __launch_bounds__(kThreads) sda_quantised_append_kernel(const __
         }
         const float need = least_scale<INT8>(__uint_as_float(top << 16));
         const float scale = fmaxf(had, need);
-        together();                             // every thread has read the scale that was there
+        if (team == 1)
+            __syncwarp();                       // every thread has read the scale that was there (else before the team's maximum)
         if (tid == 0 && (place == 0 || scale != had))
             *at = scale;
 
         // ---- Places before the rows, where the scale grew.
-        uint8_t *base = p.cache + page * p.c_s0 + group * p.c_s1 + (value ? p.dim : 0);
         if (place > 0 && scale > had) {
             const float factor = __fdiv_rn(had, scale);
             const int pieces = p.dim / 16;
-            uint8_t *first = base + static_cast<int64_t>(off - place) * p.c_s2;
             for (int k = tid; k < place * pieces; k += threads) {
                 const int row = k / pieces;
-                uint4 *v = reinterpret_cast<uint4 *>(first + row * p.c_s2 + 16 * (k - row * pieces));
+                uint4 *v = reinterpret_cast<uint4 *>(its.cache + row * p.c_s2 + 16 * (k - row * pieces));
                 const uint4 x = *v;
                 const uint32_t w[4] = {x.x, x.y, x.z, x.w};
                 uint32_t z[4];
@@ -282,24 +370,35 @@ __global__ void __launch_bounds__(kThreads) sda_quantised_append_kernel(const __
         }
 
         // ---- The rows.
-        const uint32_t bits = __float_as_uint(scale);
-        // 2^-k for 2^k; its exponent is in 1..252, so that the reciprocal is normal
-        const float inverse = (bits & 0x7FFFFFu) == 0 && (bits >> 23) < 253u ? __uint_as_float((254u << 23) - bits) : 0.0f;
-        uint8_t *out = base + off * p.c_s2;
-        row = row_first;
-        vec = vec_first;
+        auto write = [&](auto power_of_two) {
+            constexpr bool kPower = decltype(power_of_two)::value;
+            const float inverse = __frcp_rn(scale);
+            Out out(its.cache + place * p.c_s2, p.c_s2, tid, threads, p);
 #pragma unroll
-        for (int k = 0; k < kKept; ++k) {
-            if (row < length)
-                *reinterpret_cast<uint2 *>(out + row * p.c_s2 + 8 * vec) = quantise<INT8>(kept[k], scale, inverse);
-            step(row, vec);
-        }
-        row = row_rest;
-        vec = vec_rest;
-        for (; row < length; step(row, vec)) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(rows + row * src_row + 8 * vec);
-            *reinterpret_cast<uint2 *>(out + row * p.c_s2 + 8 * vec) = quantise<INT8>(v, scale, inverse);
-        }
+            for (int k = 0; k < kKept; ++k) {
+                if (out.row < length)
+                    *reinterpret_cast<uint2 *>(out.at) = quantise<INT8, kPower>(kept[k], scale, inverse);
+                out.next();
+            }
+            if (out.row < length) {
+                In in(rows, src_row, tid, threads, p);
+                for (int k = 0; k < kKept; ++k)
+                    in.next();
+                for (; out.row < length; in.next(), out.next())
+                    *reinterpret_cast<uint2 *>(out.at) =
+                        quantise<INT8, kPower>(*reinterpret_cast<const uint4 *>(in.at), scale, inverse);
+            }
+        };
+        if (!INT8 && (__float_as_uint(scale) & 0x7FFFFFu) == 0 && scale < 0x1p126f)
+            write(std::true_type{});
+        else
+            write(std::false_type{});
+    };
+    for (int i = mine; i < n; i += teams, turn ^= 1) {
+        if (threads >= p.dim / 8)
+            run(i, std::true_type{});
+        else
+            run(i, std::false_type{});
     }
 }
 
@@ -307,7 +406,7 @@ __global__ void __launch_bounds__(kThreads) sda_quantised_append_kernel(const __
 // Read
 // ---------------------------------------------------------------------------
 
-constexpr int kReadTurns = 8;                   // rows of a thread, at most
+constexpr int kReadTurns = 4;                   // rows of a thread, at most
 constexpr int kMaxReadRows = kThreads / 2 * kReadTurns;         // of a CTA (16 dims: two threads a row)
 
 struct ReadParams {
@@ -326,13 +425,14 @@ struct ReadParams {
     unsigned long long block_inv, span_inv;
     int rows, groups, dim, block, requests, width;
     int lanes, turns;                           // rows of a CTA at a time, and how often
+    int wide;                                   // rows on 32-byte boundaries
 };
 
 template <bool INT8>
-__global__ void __launch_bounds__(kThreads) sda_quantised_read_kernel(const __grid_constant__ ReadParams p)
+__global__ void __launch_bounds__(kThreads, 6) sda_quantised_read_kernel(const __grid_constant__ ReadParams p)
 {
     extern __shared__ int64_t where[];          // [rows of the CTA] x (place in the cache, -1: none; its scales')
-    __shared__ int owners[2];                   // requests of the CTA's first and last row
+    __shared__ int32_t starts_here[kThreads], first_here[kThreads];
     pdl_launch_dependents();
     pdl_wait();
     const int group = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.groups));
@@ -340,40 +440,55 @@ __global__ void __launch_bounds__(kThreads) sda_quantised_read_kernel(const __gr
     const int64_t row0 = static_cast<int64_t>(blockIdx.x / static_cast<unsigned>(p.groups)) * per;
     const int rows = static_cast<int>(min(static_cast<int64_t>(per), p.rows - row0));
 
-    // ---- The requests of the first and the last row, all threads' samples of the
-    // starts at a time: the last start at or before the row.
-#pragma unroll 1
-    for (int which = 0; which < 2; ++which) {
-        const int64_t r = row0 + (which ? rows - 1 : 0);
-        int lo = 0, size = p.requests + 1;
-        while (size > 1) {
-            const int step = (size + blockDim.x - 1) / blockDim.x, at = static_cast<int>(threadIdx.x) * step;
-            const int before = __syncthreads_count(at < size && p.starts[lo + at] <= r);
-            if (before == 0) {
-                lo = -1;
-                break;
-            }
-            lo += (before - 1) * step;
-            size = min(step, size - (before - 1) * step);
+    // ---- The rows' requests: the last start at or before the row.  Few requests' starts
+    // (and where they are read from) are looked at here once, at the same time; of many
+    // a sample by all threads at a time, for the first and for the last row.
+    const bool few = p.requests < kThreads;
+    int q0, q1;
+    if (few) {
+        for (int i = threadIdx.x; i <= p.requests; i += blockDim.x) {
+            starts_here[i] = p.starts[i];
+            first_here[i] = p.first && i < p.requests ? p.first[i * p.first_s] : 0;
         }
-        if (threadIdx.x == 0)
-            owners[which] = lo;
+        q0 = 0;
+        q1 = p.requests - 1;
+    } else {
+#pragma unroll 1
+        for (int which = 0; which < 2; ++which) {
+            const int64_t r = row0 + (which ? rows - 1 : 0);
+            int lo = 0, size = p.requests + 1;
+            while (size > 1) {
+                const int step = (size + blockDim.x - 1) / blockDim.x, at = static_cast<int>(threadIdx.x) * step;
+                const int before = __syncthreads_count(at < size && p.starts[lo + at] <= r);
+                if (before == 0) {
+                    lo = -1;
+                    break;
+                }
+                lo += (before - 1) * step;
+                size = min(step, size - (before - 1) * step);
+            }
+            if (which)
+                q1 = min(lo, p.requests - 1);
+            else
+                q0 = max(lo, 0);
+        }
     }
     __syncthreads();
-    const int q0 = max(owners[0], 0), q1 = min(owners[1], p.requests - 1);
+    const int32_t *starts = few ? starts_here : p.starts;
     for (int i = threadIdx.x; i < rows; i += blockDim.x) {
         const int r = static_cast<int>(row0) + i;
         int lo = q0, hi = q1;
-        while (lo < hi) {                       // the last request that begins at or before the row
+        while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (p.starts[mid] <= r)
+            if (starts[mid] <= r)
                 lo = mid;
             else
                 hi = mid - 1;
         }
         int64_t place = -1, scale = 0;
-        if (lo <= hi && r >= p.starts[lo] && r < p.starts[lo + 1]) {
-            const int64_t token = static_cast<int64_t>(r) - p.starts[lo] + (p.first ? p.first[lo * p.first_s] : 0);
+        if (lo <= hi && r >= starts[lo] && r < starts[lo + 1]) {
+            const int first = few ? first_here[lo] : p.first ? p.first[lo * p.first_s] : 0;
+            const int64_t token = static_cast<int64_t>(r) - starts[lo] + first;
             const bool inside = token >= 0 && token <= INT32_MAX;
             const int col = inside ? static_cast<int>(quotient(static_cast<uint32_t>(token), p.block_inv)) : p.width;
             const int page = col < p.width ? p.table[lo * p.t_s0 + col] : -1;
@@ -428,9 +543,15 @@ __global__ void __launch_bounds__(kThreads) sda_quantised_read_kernel(const __gr
             z[2 * j] = pack_bf16(v.x * s[k], v.y * s[k]);
             z[2 * j + 1] = pack_bf16(v.z * s[k], v.w * s[k]);
         }
-        uint4 *dst = reinterpret_cast<uint4 *>(out + (row0 + i) * out_row);
-        dst[0] = make_uint4(z[0], z[1], z[2], z[3]);
-        dst[1] = make_uint4(z[4], z[5], z[6], z[7]);
+        uint16_t *dst = out + (row0 + i) * out_row;
+        if (p.wide) {
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(z[0]), "r"(z[1]), "r"(z[2]),
+                         "r"(z[3]), "r"(z[4]), "r"(z[5]), "r"(z[6]), "r"(z[7])
+                         : "memory");
+        } else {
+            reinterpret_cast<uint4 *>(dst)[0] = make_uint4(z[0], z[1], z[2], z[3]);
+            reinterpret_cast<uint4 *>(dst)[1] = make_uint4(z[4], z[5], z[6], z[7]);
+        }
     }
 }
 
@@ -476,6 +597,8 @@ extern "C" sda_status sparse_decode_quantised_append(const sda_tensor *key, cons
         return st;
     if (q.groups != groups)
         return SDA_ERR_INVALID;
+    if (q.pages * q.block >= UINT32_MAX)
+        return SDA_ERR_UNSUPPORTED;
     st = check_workspace(workspace, workspace_bytes);
     if (st != SDA_OK || tokens == 0)
         return st;
@@ -494,7 +617,10 @@ extern "C" sda_status sparse_decode_quantised_append(const sda_tensor *key, cons
     p.scales = static_cast<float *>(const_cast<void *>(scales->data));
     p.s_s0 = scales->stride[0], p.s_s1 = scales->stride[1], p.s_s2 = scales->stride[2];
     p.flags = static_cast<unsigned int *>(workspace);
-    p.cache_slots = q.pages * q.block;
+    p.cache_slots = static_cast<uint32_t>(q.pages * q.block);
+    p.block_inv = inverse_of(static_cast<unsigned>(q.block));
+    p.span_inv = inverse_of(static_cast<unsigned>(q.span));
+    p.vecs_inv = inverse_of(static_cast<unsigned>(dim / 8));
     p.tokens = static_cast<int>(tokens);
     p.groups = static_cast<int>(groups);
     p.dim = static_cast<int>(dim);
@@ -590,6 +716,10 @@ extern "C" sda_status sparse_decode_quantised_read(const sda_tensor *cache, cons
     const int sms = sm_count();
     if (sms < 1)
         return SDA_ERR_CUDA;
+    p.wide = 1;
+    for (const sda_tensor *t : {key, value})
+        if (t && (!aligned(t->data, 32) || (rows > 1 && t->stride[0] % 16 != 0) || (groups > 1 && t->stride[1] % 16 != 0)))
+            p.wide = 0;
     const int cols = static_cast<int>(dim) / 8;
     p.lanes = kThreads / cols;
     // As many rows to a thread as leave each SM two CTAs.
