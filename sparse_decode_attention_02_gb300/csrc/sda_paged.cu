@@ -406,8 +406,8 @@ sda_status run_call(const Call &c)
         widest = widest_with(false);
     p.whole_units = !p.cta_units && widest <= kWholeTiles;
     // Few tiles: a worker on each of as many SMs first.
-    const int64_t want = p.whole_units || p.cta_units ? units
-                                                      : (units * (widest + kUnitCost) - 1) / (kMinTiles + kUnitCost) + 1;
+    const int cost = unit_cost(c.scales != nullptr);
+    const int64_t want = p.whole_units || p.cta_units ? units : (units * (widest + cost) - 1) / (kMinTiles + cost) + 1;
     p.ctas = static_cast<int>(p.cta_units ? units : std::min<int64_t>(most, std::max<int64_t>(1, want)));
     p.workers = p.ctas * per_cta;
 
@@ -446,6 +446,7 @@ sda_status run_call(const Call &c)
         p.active = static_cast<const uint8_t *>(c.active->data);
         p.act_s = c.active->stride[0];
         p.region_tokens = static_cast<int>(region);
+        p.block_inv = inverse_of(static_cast<unsigned>(block));
         p.per_region = static_cast<int>(region / p.piece);
         p.per_region_inv = inverse_of(static_cast<unsigned>(p.per_region));
         p.region_groups = static_cast<int>(groups);

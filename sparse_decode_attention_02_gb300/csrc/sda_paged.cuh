@@ -58,8 +58,13 @@ constexpr int kMaxRegionHeads = 16;             // of a row that attends over re
 constexpr int kSms = 152;
 constexpr int kMaxWorkers = kSms * 2 * kWarps;  // two CTAs of them on each SM (or three of two)
 // Tiles that a unit's end is worth on the line (188 requests of up to 2500 tokens, then
-// at 59 us with four: none 76, eight 61).
-constexpr int kUnitCost = 4;
+// at 59 us with four: none 76, eight 61).  Of a quantised cache two: its tiles take
+// longer, and few are cut finer (six rows of 2048 selected tokens, integers: 21.1 us
+// with four, 16.4; 188 requests of up to 2500 77.2, 75.1).
+constexpr int unit_cost(bool scaled)
+{
+    return scaled ? 2 : 4;
+}
 // A worker takes at least this many tiles before the line is cut finer (one request
 // of 1198 tokens x 4 groups: 14.5 us, with two 14.9).
 constexpr int kMinTiles = 1;
@@ -120,7 +125,7 @@ struct Params {
     int ctas, workers, whole_units, cta_units;   // cta_units: ALONE
     unsigned long long per_block_inv, tile_inv, workers_inv;    // inverse_of the pieces of a page, tile, workers
     int q_vec, o_vec;                           // 8-byte loads of q and stores of the output
-    unsigned long long span_inv, per_region_inv, region_groups_inv, request_rows_inv;
+    unsigned long long span_inv, block_inv, per_region_inv, region_groups_inv, request_rows_inv;
     int per_region, region_tokens;              // pieces and tokens of a region
     int region_groups, request_rows;            // KV groups (0: no regions), rows that share a line of the table
     int clear_inactive, one_scale;              // one_scale: a piece's tokens have one pair of scales
@@ -168,6 +173,7 @@ template <int KIND, int D, int MT, bool FULL, bool ALONE = false, bool REGIONS =
 struct Shape {
     static constexpr bool kFull = FULL, kAlone = ALONE, kRegions = REGIONS, kScaled = KIND >= kScaledE4m3;
     static constexpr bool FP8 = KIND != kBf16;
+    static constexpr int kUnitCost = unit_cost(kScaled);
     static constexpr int kElt = FP8 ? 1 : 2;
     static constexpr int kRowBytes = 2 * D * kElt;
     static constexpr int kBands = kRowBytes / 128;
@@ -210,7 +216,7 @@ struct Segment {
     int request, group, first, last, tiles, len;   // tiles [first, last) of the unit's `tiles`
 };
 
-template <bool REGIONS>
+template <bool REGIONS, int COST>
 struct Walk {
     long long left;                             // line from the unit's start to the part's end
     int request, group, tile;                   // (whole_units: units still to take)
@@ -241,11 +247,11 @@ struct Walk {
             s.len = len;
             // a unit's cost comes before its tiles
             s.last = p.whole_units ? tiles
-                                   : static_cast<int>(max(min(left - kUnitCost, static_cast<long long>(tiles)),
+                                   : static_cast<int>(max(min(left - COST, static_cast<long long>(tiles)),
                                                           static_cast<long long>(tile)));
             const bool some = s.last > s.first;
             if (s.last == tiles) {
-                left -= p.whole_units ? 1 : tiles > 0 ? tiles + kUnitCost : 0;
+                left -= p.whole_units ? 1 : tiles > 0 ? tiles + COST : 0;
                 tile = 0;
                 if (++group == p.groups || (tiles == 0 && !p.whole_units)) {
                     group = 0;
@@ -522,7 +528,7 @@ __device__ __forceinline__ long long boundary(const Params &p, long long total, 
 // w * CTAs + CTA, which spreads them over the SMs.  Every thread of the block
 // calls it; a worker's warps look for its part together.
 // `sums`: kThreads + kWarps values of shared memory.
-template <int WORKERS, bool REGIONS>
+template <int WORKERS, class Line, int COST>
 __device__ __forceinline__ Part find_part(const Params &p, long long *sums, int w, long long &total, int &used, int &v)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -541,8 +547,8 @@ __device__ __forceinline__ Part find_part(const Params &p, long long *sums, int 
     const int per = (p.requests + kThreads - 1) / kThreads;
     const int q0 = min(p.requests, static_cast<int>(threadIdx.x) * per), q1 = min(p.requests, q0 + per);
     auto span = [&](int q) -> long long {
-        const int tiles = Walk<REGIONS>::tiles_of(p, Walk<REGIONS>::length(p, q));
-        return tiles > 0 ? tiles + kUnitCost : 0;
+        const int tiles = Line::tiles_of(p, Line::length(p, q));
+        return tiles > 0 ? tiles + COST : 0;
     };
     auto scan = [&](long long x) {              // inclusive, over the warp
 #pragma unroll
@@ -572,7 +578,7 @@ __device__ __forceinline__ Part find_part(const Params &p, long long *sums, int 
         }
     }
     total = all * p.groups;
-    constexpr int least = kMinTiles + kUnitCost;
+    constexpr int least = kMinTiles + COST;
     used = total >= static_cast<long long>(p.workers) * least ? p.workers
                                                                : (static_cast<int>(total) + least - 1) / least;
     v = used == p.workers ? static_cast<int>(blockIdx.x) * WORKERS + w : spread;
@@ -621,21 +627,21 @@ __device__ __forceinline__ Part find_part(const Params &p, long long *sums, int 
     const unsigned long long in = x - at;
     const int g = static_cast<int>(in >> 32 || len >> 32 ? in / len : static_cast<unsigned>(in) / static_cast<unsigned>(len));
     const long long u0 = at + g * len;
-    return {x1 - u0, u0, q, g, static_cast<int>(max(x - u0 - kUnitCost, 0ll))};
+    return {x1 - u0, u0, q, g, static_cast<int>(max(x - u0 - COST, 0ll))};
 }
 
 // Where a warp is on the line.  It lies in shared memory (all lanes write the
 // same): between units it is not needed, and registers are short.
-template <bool REGIONS>
+template <class Line>
 struct Place {
-    Walk<REGIONS> walk;
+    Line walk;
     Segment seg;
     long long unit;                             // where the segment's unit begins on the line
 
     // The next segment into seg; a copy of it in `s`.
     __device__ __forceinline__ bool next(const Params &p, long long part_end, Segment &s)
     {
-        Walk<REGIONS> w = walk;
+        Line w = walk;
         __syncwarp();                           // every lane has read it
         unit = part_end - w.left;
         const bool some = w.next(p, s);
@@ -646,14 +652,14 @@ struct Place {
     }
 };
 
-template <bool REGIONS>
+template <class Line>
 struct WarpState {
-    Place<REGIONS> here, ahead;                          // of the warp's products and of its feed
+    Place<Line> here, ahead;                          // of the warp's products and of its feed
     long long part_end, total;                  // on the line; the line's length
     int used, number;                           // workers with a part; this one's number
 };
 
-static_assert(sizeof(WarpState<false>) == kStateBytes && sizeof(WarpState<true>) == kStateBytes, "shared memory of a warp");
+static_assert(sizeof(WarpState<Walk<false, 0>>) == kStateBytes, "shared memory of a warp");
 
 // A worker's ring of stages: their places, barriers, headers (the slots that
 // hold tokens) and how often each was issued.
@@ -668,13 +674,18 @@ struct Ring {
 // in one segment.
 template <class S>
 struct Feed {
-    Place<S::kRegions> *at_line;                // of the next segment to look up
+    Place<Walk<S::kRegions, S::kUnitCost>> *at_line;                // of the next segment to look up
     bool more;
     int tile;                                   // of the segment, the next to look up
     int per_stage, batch, lane_stage, lane_piece;   // pieces of a stage, stages of a batch; the lane's place in one
     int at, n, group, page, off, left;          // the batch: next stage to issue, stages, ...
     int n2, group2, page2, off2, left2;         // the one after
-    const float *scales;                        // quantised caches: of the lane's piece of the batch
+    // Quantised caches: the scales of the lane's piece of the batch and, of the stage that
+    // begins at the lane, the slots that will hold tokens and the bytes to come.
+    const float *scales;
+    uint64_t bits;
+    uint32_t bytes;
+    int id3, pos3;                              // regions: of the batch after that, id and position, on their way
 
     __device__ __forceinline__ void look_up(const Params &p)
     {
@@ -686,9 +697,9 @@ struct Feed {
         at = 0;
         n2 = 0;
         // here, once for a batch, and not at each stage, where the products wait for it
-        // (16 documents of 64K to 128K tokens, E4M3, 192 dims: 450 us there, 405 here)
+        // (16 documents of 64K to 128K tokens, E4M3, 192 dims: 450 us there, 402 here)
         if constexpr (S::kScaled)
-            scales = p.scales + page * p.s_s0 + group * p.s_s1 + quotient(off, p.span_inv) * p.s_s2;
+            prepare(p);
         if (!more)
             return;
         const int P = p.piece;
@@ -697,7 +708,7 @@ struct Feed {
         group2 = seg.group;
         const int f = (tile + lane_stage) * per_stage + lane_piece;
         if constexpr (S::kRegions) {
-            region_piece(p, seg, f);
+            region_piece(p, seg.request, f);
         } else {
             const int col = static_cast<int>(quotient(f, p.per_block_inv));
             off2 = f * P - col * p.block;
@@ -712,10 +723,12 @@ struct Feed {
                 more = at_line->next(p, 0, seg);
             tile = seg.first;
         }
+        if constexpr (S::kRegions)
+            region_ids(p, seg);
     }
 
     // The feed's place is where the worker's part begins.
-    __device__ __forceinline__ void start(const Params &p, Place<S::kRegions> *place, int lane)
+    __device__ __forceinline__ void start(const Params &p, Place<Walk<S::kRegions, S::kUnitCost>> *place, int lane)
     {
         at_line = place;
         per_stage = S::kFull ? 1 : p.tile / p.piece;
@@ -730,7 +743,10 @@ struct Feed {
             more = at_line->next(p, 0, seg);
         }
         tile = seg.first;
-        n2 = 0;
+        n2 = group2 = off2 = left2 = 0;         // no batch yet
+        page2 = -1;
+        if constexpr (S::kRegions)
+            region_ids(p, seg);
         look_up(p);                             // the first batch's table entries are on their way
     }
 
@@ -762,27 +778,54 @@ struct Feed {
     }
 
 private:
-    // Piece f of a row's regions: its request's table line, the row's group, and how
-    // many of its tokens the row sees.
-    __device__ __forceinline__ void region_piece(const Params &p, const Segment &seg, int f)
+    // The next batch's region ids, and its row's position, a batch before they are
+    // needed: the table entries are looked up by them.
+    __device__ __forceinline__ void region_ids(const Params &p, const Segment &seg)
     {
-        const unsigned row = static_cast<unsigned>(seg.request);
-        const unsigned of = quotient(f, p.per_region_inv);
-        const bool some = lane_stage < n2 && f * p.piece < seg.len;
-        const int id = some ? p.regions[row * p.reg_s0 + of] : -1;
+        const int f = (tile + lane_stage) * per_stage + lane_piece;
+        const bool some = more && tile + lane_stage < seg.last && lane_stage < batch && f * p.piece < seg.len;
+        const int64_t row = seg.request;
+        id3 = some ? p.regions[row * p.reg_s0 + quotient(f, p.per_region_inv)] : -1;
+        pos3 = some ? p.positions[row * p.pos_s] : -1;
+    }
+
+    // Piece f of a row's regions, of region id3: its request's table line, the row's group,
+    // and how many of its tokens the row sees.
+    __device__ __forceinline__ void region_piece(const Params &p, int request, int f)
+    {
+        const unsigned row = static_cast<unsigned>(request);
+        const int in_region = f - static_cast<int>(quotient(f, p.per_region_inv)) * p.per_region;
         group2 = static_cast<int>(row - quotient(row, p.region_groups_inv) * p.region_groups);
-        const int64_t token = static_cast<int64_t>(id) * p.region_tokens + (f - static_cast<int>(of) * p.per_region) * p.piece;
-        const int64_t seen = id >= 0 ? p.positions[row * p.pos_s] + 1 - token : 0;
+        const int64_t token = static_cast<int64_t>(id3) * p.region_tokens + in_region * p.piece;
+        const int64_t seen = id3 >= 0 ? static_cast<int64_t>(pos3) + 1 - token : 0;
         left2 = static_cast<int>(max(min(seen, static_cast<int64_t>(p.piece)), static_cast<int64_t>(0)));
         page2 = -1;
-        if (id < -1)
+        if (id3 < -1)
             atomicOr(p.flags, SDA_FLAG_BOUNDS);
         if (left2 > 0) {                        // token <= position: 31 bits
-            const int col = static_cast<int>(static_cast<unsigned>(token) / static_cast<unsigned>(p.block));
+            const int col = static_cast<int>(quotient(static_cast<uint32_t>(token), p.block_inv));
             off2 = static_cast<int>(token) - col * p.block;
             if (col < p.table_cols)
                 page2 = p.block_table[static_cast<int64_t>(quotient(row, p.request_rows_inv)) * p.bt_s0 + col];
         }
+    }
+
+    __device__ __forceinline__ void prepare(const Params &p)
+    {
+        const bool some = lane_stage < n && left > 0;
+        const bool copy = some && page >= 0 && page < p.pages;
+        if (some && !copy)
+            atomicOr(p.flags, SDA_FLAG_BOUNDS);
+        page = copy ? page : -1;
+        scales = p.scales + page * p.s_s0 + group * p.s_s1 + quotient(off, p.span_inv) * p.s_s2;
+        const uint64_t own = copy ? low_bits(min(p.piece, left)) << (lane_piece * p.piece) : 0;
+        bits = own;
+        int pieces = copy;
+        for (int k = 1; k < per_stage; ++k) {                   // of use to a stage's first lane
+            bits |= __shfl_down_sync(~0u, own, k);
+            pieces += __shfl_down_sync(~0u, static_cast<int>(copy), k);
+        }
+        bytes = static_cast<uint32_t>(pieces * p.piece) * S::kRowBytes;
     }
 
     // Stages at .. at + count - 1 of the batch into places slot, slot + 1, ...:
@@ -792,33 +835,38 @@ private:
     {
         const uint32_t piece_bytes = static_cast<uint32_t>(p.piece) * S::kRowBytes;
         const int mine = lane_stage - at;
-        const bool wanted = mine >= 0 && mine < count && left > 0;
-        const bool copy = wanted && page >= 0 && page < p.pages;
-        if (wanted && !copy)
-            atomicOr(p.flags, SDA_FLAG_BOUNDS);
-        const unsigned copies = __ballot_sync(~0u, copy);
         const int place = slot + mine;
         const uint32_t full = r.full + 8 * place;
         const bool leads = mine >= 0 && mine < count && lane_piece == 0;
-        uint64_t bits = 0;
-        if constexpr (S::kRegions) {            // each piece has tokens of its own
-            const uint64_t own = copy ? low_bits(left) << (lane_piece * p.piece) : 0;
-            for (int k = 0; k < per_stage; ++k)
-                bits |= __shfl_down_sync(~0u, own, k);          // of use to a stage's first lane
-        }
-        if (leads) {
-            const unsigned of_stage = copies >> lane;           // this lane is the stage's first
-            int pieces = 0;
-            for (int k = 0; k < per_stage; ++k)
-                if ((of_stage >> k) & 1u) {
-                    ++pieces;
-                    if constexpr (!S::kRegions)
+        bool copy;
+        if constexpr (S::kScaled) {
+            copy = mine >= 0 && mine < count && page >= 0;
+            if (leads) {
+                r.hdr[place] = bits;
+                r.issued[place] += 1;
+                if (bytes > 0)
+                    mbar_expect_tx(full, bytes);
+            }
+        } else {
+            const bool wanted = mine >= 0 && mine < count && left > 0;
+            copy = wanted && page >= 0 && page < p.pages;
+            if (wanted && !copy)
+                atomicOr(p.flags, SDA_FLAG_BOUNDS);
+            const unsigned copies = __ballot_sync(~0u, copy);
+            if (leads) {
+                uint64_t bits = 0;
+                const unsigned of_stage = copies >> lane;       // this lane is the stage's first
+                int pieces = 0;
+                for (int k = 0; k < per_stage; ++k)
+                    if ((of_stage >> k) & 1u) {
+                        ++pieces;
                         bits |= low_bits(min(p.piece, left - k * p.piece)) << (k * p.piece);
-                }
-            r.hdr[place] = bits;
-            r.issued[place] += 1;
-            if (pieces > 0)
-                mbar_expect_tx(full, pieces * piece_bytes);
+                    }
+                r.hdr[place] = bits;
+                r.issued[place] += 1;
+                if (pieces > 0)
+                    mbar_expect_tx(full, pieces * piece_bytes);
+            }
         }
         __syncwarp();
         if (copy)
@@ -847,7 +895,8 @@ __global__ void __launch_bounds__(kThreads, Shape<KIND, D, MT, FULL, ALONE, REGI
     sda_paged_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_constant__ Params p)
 {
     using S = Shape<KIND, D, MT, FULL, ALONE, REGIONS>;
-    using Line = Walk<REGIONS>;
+    constexpr int kUnitCost = S::kUnitCost;
+    using Line = Walk<REGIONS, kUnitCost>;
     constexpr bool FP8 = S::FP8, SCALED = S::kScaled;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -877,7 +926,7 @@ __global__ void __launch_bounds__(kThreads, Shape<KIND, D, MT, FULL, ALONE, REGI
     pdl_wait();
 
     // What is needed between units only: this warp's place, its feed's, the line.
-    WarpState<REGIONS> *state = reinterpret_cast<WarpState<REGIONS> *>(smem + S::kStateOff) + warp;
+    WarpState<Line> *state = reinterpret_cast<WarpState<Line> *>(smem + S::kStateOff) + warp;
     if constexpr (ALONE) {
         Segment &seg = state->here.seg;
         seg.request = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.groups));
@@ -889,7 +938,7 @@ __global__ void __launch_bounds__(kThreads, Shape<KIND, D, MT, FULL, ALONE, REGI
     } else {
         long long total;
         int used, v;
-        const Part part = find_part<S::kWorkers, REGIONS>(p, sums, worker, total, used, v);
+        const Part part = find_part<S::kWorkers, Line, kUnitCost>(p, sums, worker, total, used, v);
         state->here.walk = state->ahead.walk = {part.left, part.request, part.group, part.tile};
         state->part_end = part.start + part.left;
         state->total = total;
@@ -1305,7 +1354,7 @@ __global__ void __launch_bounds__(kThreads, Shape<KIND, D, MT, FULL, ALONE, REGI
         // ---- The unit's result, or its piece's.
         const volatile Segment &at = state->here.seg;
         const Segment seg = {at.request, at.group, at.first, at.last, at.tiles, at.len};
-        const int v = static_cast<const volatile WarpState<REGIONS> *>(state)->number;
+        const int v = static_cast<const volatile WarpState<Line> *>(state)->number;
         const int64_t out_row0 = static_cast<int64_t>(seg.request) * p.query_len * p.groups + seg.group;
         auto row_of = [&](int r) { return out_row0 + static_cast<int64_t>(token_of(r)) * p.groups; };
         auto gate_of = [&](int r, int h) {      // of query row r, head h

@@ -382,3 +382,32 @@ def test_nothing_to_do():
     p.rt, p.regions = 8, torch.zeros(0, 5, dtype=torch.int32, device="cuda")
     p.positions, p.active = torch.zeros(0, dtype=torch.int32, device="cuda"), torch.zeros(0, dtype=torch.bool, device="cuda")
     p.run(regions=True)
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("peak", [0.0, 3.0])
+def test_long_contexts_keep_their_mean(int8, peak):
+    """Rows that weigh 100,000 tokens nearly alike, each unit one worker's from its first tile to its last: the mean of
+    values without one is small beside them, and so is its error (in steps of the elements: 2^-11 of each weight, without
+    a sign, and 2^-20 for sums in fp32)."""
+    G, D, B, n, requests = 8, 64, 128, 100000, 200
+    width = -(-n // B)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    # one request's pages for all of them: every unit has the same tokens
+    raw = torch.randint(-100, 101, (width, 1, B, 2 * D), generator=gen, device="cuda")
+    cache = (raw.to(torch.int8) if int8 else raw.float().to(torch.float8_e4m3fn).view(torch.uint8)).expand(width, G, B, 2 * D).contiguous()
+    scales = torch.ones(width, G, 1, 2, device="cuda")
+    table = torch.arange(width, dtype=torch.int32, device="cuda").expand(requests, width)
+    query = torch.zeros(requests * G, 1, D, dtype=torch.bfloat16, device="cuda")
+    query[:, :, 0] = peak
+    out = torch.empty_like(query)
+    lse = torch.empty(requests * G, 1, device="cuda")
+    sda.sparse_decode_quantised_paged_attention(query, cache, scales, table, torch.full((requests,), n, dtype=torch.int32, device="cuda"),
+                                                out, scale=0.01, lse=lse)
+    x = (cache if int8 else cache.view(torch.float8_e4m3fn).float())[:, 0].double().reshape(-1, 2 * D)[:n]
+    w = torch.softmax(x[:, 0] * peak * float(np.float32(0.01)), 0)
+    want = w @ x[:, D:]
+    far = (out[:, 0].double() - want).abs().amax(0)
+    # weights' roundings have no sign of their own: 2^-11 / sqrt(tokens that count) of the values' size, six times over
+    spread = torch.sqrt((w * w) @ (x[:, D:] ** 2))
+    assert (far <= want.abs() * 2.0 ** -8 + 6 * spread * 2.0 ** -11 + 100 * 2.0 ** -15).all(), far.max().item()
