@@ -467,9 +467,9 @@ sda_status sparse_decode_paged_attention(const sda_tensor *query, const sda_tens
  * the first that does not on, a block's rows are left out with SDA_FLAG_BOUNDS.  So
  * is a slot outside the cache.  Rows of one block in two places of `slots` make its
  * contents a mix of the two.
- * D is a multiple of 16 up to 512.  stride[2] == 1 (cache: stride[3] == 1); bases
- * and the other byte strides of key, value and cache are multiples of 16, those of
- * scales of 8, else SDA_ERR_UNSUPPORTED.  Returns SDA_ERR_INVALID for shapes,
+ * D is a multiple of 16 up to 512, pages * B below 2^32 - 1.  stride[2] == 1 (cache:
+ * stride[3] == 1); bases and the other byte strides of key, value and cache are
+ * multiples of 16, those of scales of 8, else SDA_ERR_UNSUPPORTED.  Returns SDA_ERR_INVALID for shapes,
  * dtypes or strides outside this contract, SDA_ERR_WORKSPACE for a bad workspace,
  * SDA_ERR_CUDA if the launch failed; T == 0 returns SDA_OK with no launch.
  */
@@ -509,7 +509,8 @@ sda_status sparse_decode_quantised_read(const sda_tensor *cache, const sda_tenso
  *   stream         as in sparse_decode_paged_attention (the workspace of
  *                  sparse_decode_paged_workspace_bytes).
  * The scales enter in fp32: a block's key scale multiplies its logits, its value
- * scale its weights.  Weights times value scales have 11 bits down to 2^-27 of the
+ * scale its weights.  (Integer keys are multiplied with 128 added, which the sums
+ * take out again: their logits round by the size of 255 |q| * key scale.)  Weights times value scales have 11 bits down to 2^-27 of the
  * product of the row's largest weight and the largest value scale that is met, and
  * below that are off by 2^-38 of it at most.  Scales of blocks that no visible token
  * lies in may hold anything.

@@ -362,16 +362,43 @@ __device__ __forceinline__ void split_bf16(float lo, float hi, uint32_t &most, u
     rest = pack_bf16(lo - __uint_as_float(a & 0xFFFF0000u), hi - __uint_as_float(b & 0xFFFF0000u));
 }
 
+// Keys of integers go into the products as fp16 numbers below the normal ones: the byte
+// of x + 128 by itself stands for (x + 128) 2^-24, exactly.  Scores begin at -128 times
+// the row's sum of q instead of 0, so that they round by the size of 255 |q|, not of
+// |q k|: far below half a step of k.  (To take the 128 off each element takes two more
+// instructions a word: 16 documents of 64K to 128K tokens 444 us, so 414.  Values have
+// it taken off: where a token of nearly all weight is 0, outputs are as small as the
+// rest of them, and would be off by the bias's rounding.)
+constexpr float kKeyUnit = 0x1p-24f, kKeyBias = 128.0f;
+
 // The four elements of a word of keys: two pairs of fp16 values, in order.
 template <int KIND>
 __device__ __forceinline__ uint2 key_pairs(uint32_t w)
 {
     if constexpr (KIND == kScaledInt8) {
         const uint32_t x = w ^ 0x80808080u;
-        return make_uint2(int8x2_to_f16x2<0, 1>(x), int8x2_to_f16x2<2, 3>(x));
+        return make_uint2(bytes_of<0x4140u>(x, 0u), bytes_of<0x4342u>(x, 0u));
     } else {
         return make_uint2(e4m3x2_to_f16x2(w), e4m3x2_to_f16x2(w >> 16));
     }
+}
+
+// The four elements of a word as fp32 values.
+template <int KIND>
+__device__ __forceinline__ float4 word_values(uint32_t w)
+{
+    uint32_t a, b;
+    if constexpr (KIND == kScaledInt8) {
+        const uint32_t x = w ^ 0x80808080u;
+        a = int8x2_to_f16x2<0, 1>(x);
+        b = int8x2_to_f16x2<2, 3>(x);
+    } else {
+        a = e4m3x2_to_f16x2(w);
+        b = e4m3x2_to_f16x2(w >> 16);
+    }
+    const float2 u = __half22float2(*reinterpret_cast<const __half2 *>(&a));
+    const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&b));
+    return make_float4(u.x, u.y, v.x, v.y);
 }
 
 // A word of two tokens' values (two dims of one, two of the other): the pairs of the
@@ -897,7 +924,7 @@ __global__ void __launch_bounds__(kThreads, Shape<KIND, D, MT, FULL, ALONE, REGI
     using S = Shape<KIND, D, MT, FULL, ALONE, REGIONS>;
     constexpr int kUnitCost = S::kUnitCost;
     using Line = Walk<REGIONS, kUnitCost>;
-    constexpr bool FP8 = S::FP8, SCALED = S::kScaled;
+    constexpr bool FP8 = S::FP8, SCALED = S::kScaled, INT8 = KIND == kScaledInt8;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
@@ -1043,6 +1070,7 @@ __global__ void __launch_bounds__(kThreads, Shape<KIND, D, MT, FULL, ALONE, REGI
             }
         }
         float sl[2] = {p.scale * kLog2e * ks, p.scale * kLog2e * ks};   // logit scales in log2 units
+        float from[2] = {0.0f, 0.0f};           // what the rows' scores begin at
         if constexpr (FP8) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
@@ -1059,9 +1087,20 @@ __global__ void __launch_bounds__(kThreads, Shape<KIND, D, MT, FULL, ALONE, REGI
 #pragma unroll
                 for (int kk = 0; kk < S::kSteps; ++kk)
 #pragma unroll
-                    for (int i = k; i < 4; i += 2)
+                    for (int i = k; i < 4; i += 2) {
                         qf[kk][i] = pack_f16(__uint_as_float(qf[kk][i] << 16) * up,
                                              __uint_as_float(qf[kk][i] & 0xFFFF0000u) * up);
+                        if constexpr (INT8) {   // as the products take it
+                            const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&qf[kk][i]));
+                            from[k] += x.x + x.y;
+                        }
+                    }
+                if constexpr (INT8) {
+                    from[k] += __shfl_xor_sync(~0u, from[k], 1);
+                    from[k] += __shfl_xor_sync(~0u, from[k], 2);
+                    from[k] *= -kKeyBias * kKeyUnit;
+                    sl[k] *= 1.0f / kKeyUnit;
+                }
             }
         }
 
@@ -1102,8 +1141,10 @@ __global__ void __launch_bounds__(kThreads, Shape<KIND, D, MT, FULL, ALONE, REGI
                 // ---- S = Q K^T: tile i, column g is slot 8i + slot_of(g).
                 float sc[NT][4];
 #pragma unroll
-                for (int i = 0; i < NT; ++i)
-                    sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.0f;
+                for (int i = 0; i < NT; ++i) {
+                    sc[i][0] = sc[i][1] = INT8 ? from[0] : 0.0f;
+                    sc[i][2] = sc[i][3] = INT8 ? from[1] : 0.0f;
+                }
                 const uint32_t krow = sb + ksw * 128u;
                 constexpr int kGroup = NT < 4 ? NT : 4;         // tiles, independent chains, at a time
 #pragma unroll
@@ -1294,20 +1335,18 @@ __global__ void __launch_bounds__(kThreads, Shape<KIND, D, MT, FULL, ALONE, REGI
                             const int idx = kFirst + c;
                             const uint32_t w = lds32(vrow + (idx >> 3) * bstride + (((idx & 7) ^ (s & 7)) << 4));
                             if constexpr (FP8) {
-                                const uint2 x = key_pairs<KIND>(w);
-                                const float2 va = __half22float2(*reinterpret_cast<const __half2 *>(&x.x));
-                                const float2 vb = __half22float2(*reinterpret_cast<const __half2 *>(&x.y));
+                                const float4 x = word_values<KIND>(w);
                                 if (see0) {
-                                    o[2 * c][0] += p0 * va.x;
-                                    o[2 * c + 1][0] += p0 * va.y;
-                                    o[2 * c][1] += p0 * vb.x;
-                                    o[2 * c + 1][1] += p0 * vb.y;
+                                    o[2 * c][0] += p0 * x.x;
+                                    o[2 * c + 1][0] += p0 * x.y;
+                                    o[2 * c][1] += p0 * x.z;
+                                    o[2 * c + 1][1] += p0 * x.w;
                                 }
                                 if (see1) {
-                                    o[2 * c][2] += p1 * va.x;
-                                    o[2 * c + 1][2] += p1 * va.y;
-                                    o[2 * c][3] += p1 * vb.x;
-                                    o[2 * c + 1][3] += p1 * vb.y;
+                                    o[2 * c][2] += p1 * x.x;
+                                    o[2 * c + 1][2] += p1 * x.y;
+                                    o[2 * c][3] += p1 * x.z;
+                                    o[2 * c + 1][3] += p1 * x.w;
                                 }
                             } else {
                                 const float va = __uint_as_float(w << 16), vb = __uint_as_float(w & 0xFFFF0000u);
