@@ -540,7 +540,8 @@ sda_status sparse_decode_quantised_paged_attention(const sda_tensor *query, cons
  *                  aligned, its header zeroed once before first use.  Calls that
  *                  overlap on the GPU must not share one.
  * The regions of all active rows are dealt out evenly over the GPU on the device;
- * there is no split count.  An active row that sees no token is +0.0.  Equal inputs
+ * there is no split count.  A region that a row lists twice counts twice.  An active
+ * row that sees no token is +0.0.  Equal inputs
  * give equal bits.  A region id below -1, a table column past the width or an entry
  * outside the cache leaves its tokens out with SDA_FLAG_BOUNDS.  rows must be tokens
  * * G; requests = ceil(rows / (G * query_len)).

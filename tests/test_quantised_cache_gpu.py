@@ -308,3 +308,32 @@ def test_captured_and_on_another_stream():
     for x in (c, d):
         assert torch.equal(x.store, eager.store) and torch.equal(x.scale_store, eager.scale_store)
     assert all(torch.equal(a, b) for pair in outs[1:] for a, b in zip(pair, outs[0]))
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("D,G,S,rows", [(64, 4, 16, 6000), (64, 4, 64, 6000), (16, 2, 512, 1500), (16, 8, 512, 3000)])
+def test_long_prompts(D, G, S, rows, int8):
+    """Rows enough for CTAs of 64 each, and blocks longer than the window that a CTA looks at."""
+    c = Cache(pages=rows // S + 3, G=G, B=S, S=S, D=D, int8=int8)
+    gen = torch.Generator().manual_seed(rows + D)
+    pages = list(range(c.cache.shape[0]))
+    random.Random(1).shuffle(pages)
+    c.append(*c.rows(rows, gen), slots_of(pages, 3, rows, S))
+    c.append(*c.rows(5, gen), slots_of(pages, 3 + rows, 5, S))
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("D", [272, 416, 512])
+def test_wide_heads_of_many_requests(D, int8):
+    """A warp for each of many runs, fewer threads than a row has pieces."""
+    c = Cache(pages=60, G=2, B=16, S=16, D=D, int8=int8)
+    filled(c, [[2] * 40, [1] * 40, [5 if q % 3 else 0 for q in range(40)]], torch.Generator().manual_seed(D))
+
+
+def test_a_block_of_two_lists_of_rows():
+    """A long run that stops inside the window and one that stops behind it, each followed by rows that are left out."""
+    c = Cache(pages=4, G=1, B=512, S=512, D=16)
+    gen = torch.Generator().manual_seed(3)
+    for stop in (100, 255, 256, 257, 300, 479):
+        slots = list(range(512, 512 + stop)) + list(range(512 + stop + 1, 1024)) + [0, 1]
+        c.append(*c.rows(len(slots), gen), slots, flags=sda.FLAG_BOUNDS)
