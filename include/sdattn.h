@@ -524,6 +524,13 @@ sda_status sparse_decode_quantised_paged_attention(const sda_tensor *query, cons
                                                    size_t workspace_bytes, void *stream);
 
 /*
+ * Bytes of workspace sparse_decode_quantised_attention needs for `rows` rows of
+ * `heads` heads and head size `head_dim`: what sparse_decode_paged_attention takes
+ * for query_len 1, and four bytes a row.  Returns 0 for arguments out of range.
+ */
+size_t sparse_decode_quantised_workspace_bytes(int64_t rows, int heads, int head_dim);
+
+/*
  * sparse_decode_attention over a quantised cache, for the head sizes of
  * sparse_decode_paged_attention.
  *
@@ -536,15 +543,17 @@ sda_status sparse_decode_quantised_paged_attention(const sda_tensor *query, cons
  *   lse            NULL, or [rows, H] fp32 (written): natural log-sum-exp of the
  *                  row's scaled logits; -inf for a row that sees nothing, as it was
  *                  where the output is left as it was.
- *   workspace      >= sparse_decode_paged_workspace_bytes(H, 1, D) bytes, 256-byte
- *                  aligned, its header zeroed once before first use.  Calls that
- *                  overlap on the GPU must not share one.
- * The regions of all active rows are dealt out evenly over the GPU on the device;
- * there is no split count.  A region that a row lists twice counts twice.  An active
- * row that sees no token is +0.0.  Equal inputs
- * give equal bits.  A region id below -1, a table column past the width or an entry
- * outside the cache leaves its tokens out with SDA_FLAG_BOUNDS.  rows must be tokens
- * * G; requests = ceil(rows / (G * query_len)).
+ *   workspace      >= sparse_decode_quantised_workspace_bytes(rows, H, D) bytes,
+ *                  256-byte aligned, its header zeroed once before first use.  Calls
+ *                  that overlap on the GPU must not share one.
+ * The regions of all active rows, up to the last that a row sees, are dealt out evenly
+ * over the GPU on the device; there is no split count, and lists that end in -1 cost
+ * no more than shorter ones.  A region that a row lists twice counts twice.  An active
+ * row that sees no token is +0.0.  Equal inputs give equal bits.  A region id below
+ * -1, a table column past the width or an entry outside the cache leaves its tokens
+ * out with SDA_FLAG_BOUNDS.  rows must be tokens * G; requests = ceil(rows / (G *
+ * query_len)); rows below 2^25 - 1, R at most 2^20 and R * region_tokens below 2^31 -
+ * 4096, else SDA_ERR_UNSUPPORTED.
  */
 sda_status sparse_decode_quantised_attention(const sda_tensor *query, const sda_tensor *cache,
                                              const sda_tensor *scales, const sda_tensor *regions,

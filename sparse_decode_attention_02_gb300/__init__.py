@@ -16,6 +16,7 @@ from ._binding import (  # noqa: F401
     load,
     no_alloc_read_errors,
     paged_workspace_bytes,
+    quantised_workspace_bytes,
     read_errors,
     set_wait_limit_ns,
     sparse_decode_attention,

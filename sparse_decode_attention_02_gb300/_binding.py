@@ -93,6 +93,8 @@ def _declare(lib):
     lib.sparse_decode_quantised_read.restype = I
     lib.sparse_decode_quantised_paged_attention.argtypes = 7 * [V] + [F, I, V, V, Z, V]
     lib.sparse_decode_quantised_paged_attention.restype = I
+    lib.sparse_decode_quantised_workspace_bytes.argtypes = [ctypes.c_int64, I, I]
+    lib.sparse_decode_quantised_workspace_bytes.restype = Z
     lib.sparse_decode_quantised_attention.argtypes = 9 * [V] + [F, I, V, I, I, V, Z, V]
     lib.sparse_decode_quantised_attention.restype = I
     lib.sparse_decode_read_errors.argtypes = [ctypes.c_void_p, ctypes.POINTER(ctypes.c_uint32),
@@ -625,6 +627,10 @@ def sparse_decode_quantised_paged_attention(query, cache, scales, block_table, s
         raise SdaError(rc, lib.sparse_decode_status_string(rc).decode())
 
 
+def quantised_workspace_bytes(rows: int, heads: int, head_dim: int = 192) -> int:
+    return load().sparse_decode_quantised_workspace_bytes(operator.index(rows), _int32(heads), _int32(head_dim))
+
+
 def sparse_decode_quantised_attention(query, cache, scales, regions, block_table, positions, active, output, *,
                                       scale: float, query_len: int = 1, clear_inactive: bool = True, gate=None,
                                       lse=None, region_tokens: int = 0, workspace: torch.Tensor | None = None,
@@ -633,7 +639,9 @@ def sparse_decode_quantised_attention(query, cache, scales, regions, block_table
     for head sizes 64, 128, 192 and 256, and the rows' log-sum-exps into `lse` if given; see
     include/sdattn.h for the contract."""
     lib = _lib or load()
-    need = _paged_need(query, 1) if workspace is None else 0
+    need = 0
+    if workspace is None:                       # the header at least, where the call is refused
+        need = quantised_workspace_bytes(query.shape[0], query.shape[1], query.shape[-1]) or 256
     tensors = query, cache, scales, regions, block_table, positions, active, output, lse, gate
     rc = None
     if stream is None:

@@ -196,6 +196,50 @@ __global__ void __launch_bounds__(kJoinThreads) sda_paged_join_kernel(const __gr
 }
 
 // ---------------------------------------------------------------------------
+// Extent kernel: how far a row's list of regions has one that the row sees.  Lists end in
+// -1 where a context has fewer regions than are selected; dealt out by their room alone
+// such rows would leave most workers idle.  A warp a row, from the end on: of a full list
+// the last ids are all that it reads.  3 to 5 us, most of it the launch.
+// ---------------------------------------------------------------------------
+
+constexpr int kExtentWarps = 4, kExtentIds = 4;                 // ids of a lane at a time
+
+__global__ void __launch_bounds__(kExtentWarps * 32) sda_region_extent_kernel(const __grid_constant__ Params p)
+{
+    pdl_launch_dependents();
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * kExtentWarps + (threadIdx.x >> 5);
+    if (row >= p.requests)
+        return;
+    int last = -1;
+    const bool active = p.active[row * p.act_s] != 0;
+    if (active) {
+        const int pos = p.positions[row * p.pos_s];
+        const int most = pos >= 0 ? pos / p.region_tokens : -1;               // the last region that it sees
+        const int32_t *ids = p.regions + row * p.reg_s0;
+        for (int end = p.listed; end > 0 && last < 0; end -= 32 * kExtentIds) {
+            int id[kExtentIds];
+#pragma unroll
+            for (int k = 0; k < kExtentIds; ++k) {
+                const int i = end - 1 - 32 * k - lane;
+                id[k] = i >= 0 ? ids[i] : -1;
+            }
+#pragma unroll
+            for (int k = 0; k < kExtentIds; ++k) {
+                if (id[k] < -1)
+                    atomicOr(p.flags, SDA_FLAG_BOUNDS);
+                const unsigned live = __ballot_sync(~0u, id[k] >= 0 && id[k] <= most);
+                if (last < 0 && live)
+                    last = end - 1 - 32 * k - (__ffs(live) - 1);
+            }
+        }
+    }
+    if (lane == 0)
+        p.extents[row] = active ? (last + 1) * p.region_tokens : p.clear_inactive ? 0 : -1;
+}
+
+// ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
 
@@ -243,6 +287,11 @@ size_t align256(size_t n)
 //     in one round: 7.4, 5.8).
 constexpr int kWholeTiles = 8, kAloneTiles = 12;
 constexpr int kRounds = 4;
+// Rows' lists are looked at for their extents where a worker has at least this many tiles of their
+// room (1024 slots, E4M3, 192 dims, 2 groups; not looked at, looked at: 256 requests of 1K to 2K tokens
+// 196 us, 100, of 16K to 32K 296, 301; 16 requests of 1K to 3K 33.2, 28.5, of 16K to 20K 39.5, 42.7;
+// four of either, which have fewer tiles, 19.6 and 20.9, and 25.6 and 23.5).
+constexpr int kExtentTiles = 8;
 
 // CTAs of a launch, at most.
 int ctas_of(int64_t dim, int64_t rows)
@@ -257,6 +306,12 @@ int workers_of(int64_t rows)
 }
 
 }  // namespace
+
+extern "C" size_t sparse_decode_quantised_workspace_bytes(int64_t rows, int heads, int head_dim)
+{
+    const size_t bytes = heads <= kMaxRegionHeads ? sparse_decode_paged_workspace_bytes(heads, 1, head_dim) : 0;
+    return bytes && rows >= 0 && rows <= INT32_MAX ? bytes + align256(static_cast<size_t>(rows) * sizeof(int32_t)) : 0;
+}
 
 extern "C" size_t sparse_decode_paged_workspace_bytes(int heads, int query_len, int head_dim)
 {
@@ -368,7 +423,8 @@ sda_status run_call(const Call &c)
                       c.regions->shape[1] * region > INT32_MAX - 4096))
         return SDA_ERR_UNSUPPORTED;
     const int64_t held = by_region ? c.regions->shape[1] * region : block_table->shape[1] * block;
-    const size_t need = sparse_decode_paged_workspace_bytes(static_cast<int>(heads), query_len, static_cast<int>(dim));
+    const size_t need = by_region ? sparse_decode_quantised_workspace_bytes(rows, static_cast<int>(heads), static_cast<int>(dim))
+                                  : sparse_decode_paged_workspace_bytes(static_cast<int>(heads), query_len, static_cast<int>(dim));
     if (!c.workspace || !aligned(c.workspace, 256) || c.workspace_bytes < need)
         return SDA_ERR_WORKSPACE;
     if (rows == 0)
@@ -446,6 +502,7 @@ sda_status run_call(const Call &c)
         p.active = static_cast<const uint8_t *>(c.active->data);
         p.act_s = c.active->stride[0];
         p.region_tokens = static_cast<int>(region);
+        p.listed = static_cast<int>(c.regions->shape[1]);
         p.block_inv = inverse_of(static_cast<unsigned>(block));
         p.per_region = static_cast<int>(region / p.piece);
         p.per_region_inv = inverse_of(static_cast<unsigned>(p.per_region));
@@ -517,6 +574,14 @@ sda_status run_call(const Call &c)
     Launch *launch = kLaunches[kind][dim / 64 - 1];
     // The split kernel leaves its list and pieces in the workspace, the join empties it.
     const std::lock_guard<std::mutex> together(sda_launch_mutex(c.workspace));
+    if (by_region && !p.whole_units && !p.cta_units && units * widest >= kExtentTiles * static_cast<int64_t>(p.workers)) {
+        p.extents = reinterpret_cast<int32_t *>(
+            ws + sparse_decode_paged_workspace_bytes(static_cast<int>(heads), query_len, static_cast<int>(dim)));
+        const dim3 blocks(static_cast<unsigned>((rows + kExtentWarps - 1) / kExtentWarps));
+        const sda_status looked = launch_pdl(sda_region_extent_kernel, blocks, dim3(kExtentWarps * 32), 0, c.stream, p);
+        if (looked != SDA_OK)
+            return looked;
+    }
     const sda_status st = launch(tmap, p, c.stream);
     if (st != SDA_OK || p.whole_units || p.cta_units)
         return st;

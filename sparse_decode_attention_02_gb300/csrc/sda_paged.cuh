@@ -47,7 +47,7 @@
 // and of those a row's selected regions can be walked instead of a request's tokens.
 // 16 documents of 64K to 128K tokens (192 dims, 4 groups): E4M3 377 to 379 us, 6.6 TB/s
 // (one scale for all: 370 to 376), integers 414, 6.1 TB/s, bound by their conversions; 512 rows of
-// 1024 regions of 8 tokens (E4M3, 192 dims) 282 us, 5.7 TB/s, in TMA boxes of 3 KB.
+// 1024 regions of 8 tokens (E4M3, 192 dims) 285 to 289 us, 5.7 TB/s, in TMA boxes of 3 KB.
 #pragma once
 
 #include "sda_quant.cuh"
@@ -118,6 +118,7 @@ struct Params {
     int64_t pos_s;
     const uint8_t *active;
     int64_t act_s;
+    int32_t *extents;                           // NULL or, written by the extent kernel, Walk::length of each row
     unsigned int *flags;
     JoinItem *items;
     float *partial;                             // [worker][continued here / goes on][rows][D]
@@ -135,6 +136,7 @@ struct Params {
     unsigned long long span_inv, block_inv, per_region_inv, region_groups_inv, request_rows_inv;
     int per_region, region_tokens;              // pieces and tokens of a region
     int region_groups, request_rows;            // KV groups (0: no regions), rows that share a line of the table
+    int listed;                                 // regions of a row's list
     int clear_inactive, one_scale;              // one_scale: a piece's tokens have one pair of scales
 };
 
@@ -228,12 +230,13 @@ struct Walk {
     long long left;                             // line from the unit's start to the part's end
     int request, group, tile;                   // (whole_units: units still to take)
 
-    // Tokens of a unit; of an active row all that its list has room for.  0: a row
-    // of zeros, < 0: left as it was.
+    // Tokens of a unit; of an active row those of its list, up to the last region that it
+    // sees or (without extents) all that there is room for.  0: a row of zeros, < 0: left
+    // as it was.
     static __device__ __forceinline__ int length(const Params &p, int q)
     {
         if constexpr (REGIONS)
-            return p.active[q * p.act_s] ? p.cap : p.clear_inactive ? 0 : -1;
+            return p.extents ? p.extents[q] : p.active[q * p.act_s] ? p.cap : p.clear_inactive ? 0 : -1;
         else
             return min(p.seq_lens[q * p.len_s], p.cap);
     }

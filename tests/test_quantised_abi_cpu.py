@@ -125,7 +125,7 @@ def regions(lib, toks=6, ql=2, G=2, H=8, D=64, R=4, W=5, rt=0, scale=0.1, ws=1 <
                                                     act=t(5, (rows,)), out=t(BF16, (rows, H, D)), lse=t(F32, (rows, H)),
                                                     gate=None) | change
     a = [ref(x) for x in d.values()]
-    need = lib.sparse_decode_paged_workspace_bytes(H, 1, D)
+    need = lib.sparse_decode_quantised_workspace_bytes(rows, H, D)
     return lib.sparse_decode_quantised_attention(*a[:9], scale, ql, a[9], 1, rt, ws, need if wsb is None else wsb, None)
 
 
@@ -179,6 +179,14 @@ def test_region_refusals(lib):
     assert regions(lib, R=(1 << 20) + 1) == UNS
     assert regions(lib, toks=0) == OK
     assert regions(lib, toks=0, rt=40) == regions(lib, toks=0, R=0) == OK    # gcd 8; nothing listed
+
+
+def test_region_workspace_bytes(lib):
+    f = sda.quantised_workspace_bytes
+    assert f(10, 0) == f(10, 17) == f(10, 8, 96) == f(-1, 8) == f(1 << 40, 8) == 0
+    for rows in (0, 1, 63, 64, 65, 1000):
+        assert f(rows, 8, 128) == sda.paged_workspace_bytes(8, 1, 128) + -(-rows * 4 // 256) * 256
+    assert regions(lib, wsb=f(12, 8, 64) - 1) == WS
 
 
 def host_calls(ws=None):

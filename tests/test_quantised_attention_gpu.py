@@ -75,7 +75,8 @@ class Problem:
         self.active = torch.tensor([p >= 0 and r.random() < 0.9 for p in pos], device="cuda")
 
     def workspace(self):
-        need = max(sda.paged_workspace_bytes(self.H, k, self.D) for k in (1, self.ql))
+        need = sda.paged_workspace_bytes(self.H, self.ql, self.D)
+        need = max(need, sda.quantised_workspace_bytes(self.query.shape[0], self.H, self.D))
         return torch.zeros(need, dtype=torch.uint8, device="cuda")
 
     def run(self, *, regions=False, out=None, lse=None, workspace=None, flags=0, **kw):
@@ -283,6 +284,34 @@ def test_many_rows():
     r = random.Random(2)
     check([r.randint(1, 600) for _ in range(300)], G=2, H=4, D=64, block=16, regions=(20, 8))
     check([r.randint(1, 600) for _ in range(150)], G=2, H=8, D=192, block=16, ql=2, int8=True, regions=(40, 16))
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_long_lists_of_short_contexts(int8):
+    """Rows enough for their lists to be looked at first: most of a list is -1, at its end, at its beginning, between,
+    or past the row's position; some rows are full, some empty, some inactive."""
+    r = random.Random(7)
+    p = Problem([r.choice((1, 30, 200, 900, 1500)) for _ in range(120)], G=2, H=4, D=64, block=16, int8=int8, ql=2, regions=(12, 8))
+    ids = torch.full((480, 1100), -1, dtype=torch.int32, device="cuda")
+    for k in range(480):
+        at = (0, 1088, 500 + k, 128 * (k % 8) + k % 3)[k % 4]
+        ids[k, at:at + 12] = p.regions[k]
+    ids[5::40, 1099] = 10 ** 8                                          # past any position
+    p.regions = ids
+    p.active[::7] = False
+    p.check(*p.run(regions=True), regions=True)
+    left = p.query.clone() * 3, torch.full(p.query.shape[:2], 5.0, device="cuda")
+    out, lse = p.run(regions=True, out=left[0].clone(), lse=left[1].clone(), clear_inactive=False)
+    p.check(out, lse, regions=True, left=left)
+    p.regions = ids.clone()
+    p.regions[3, 1090] = -2
+    p.active[3] = True
+    out, lse = p.run(regions=True, flags=sda.FLAG_BOUNDS)
+    p.regions[3, 1090] = -1
+    p.check(out, lse, regions=True)
+    p.regions[:] = -1
+    out, lse = p.run(regions=True)
+    assert (out.view(torch.int16) == 0).all() and (lse == -float("inf")).all()
 
 
 def test_rows_that_see_nothing():

@@ -31,7 +31,8 @@ class Server:
         self.plain_scales = self.scales.cpu().numpy().copy()
         self.inv = (10000.0 ** (-torch.arange(D // 2).double() / (D // 2))).float().cuda()
         self.plain = dict(context=[0] * slots, ring=order.tolist(), state=[0, pages], table=np.full((slots, width), -1))
-        self.ws = torch.zeros(max(sda.paged_workspace_bytes(H, k, D) for k in (1, 3)), dtype=torch.uint8, device="cuda")
+        need = max(sda.paged_workspace_bytes(H, 3, D), sda.paged_workspace_bytes(H, 1, D), sda.quantised_workspace_bytes(3 * G * slots, H, D))
+        self.ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
 
     def step(self, new, rows, per_request, gen):
         """Plans, turns and appends; returns the turned queries after checking the cache."""
