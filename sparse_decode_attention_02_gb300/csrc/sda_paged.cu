@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kJoinThreads) sda_paged_join_kernel(const __gr
 // Extent kernel: how far a row's list of regions has one that the row sees.  Lists end in
 // -1 where a context has fewer regions than are selected; dealt out by their room alone
 // such rows would leave most workers idle.  A warp a row, from the end on: of a full list
-// the last ids are all that it reads.  3 to 5 us, most of it the launch.
+// the last ids are all that it reads.  2 to 3 us, most of it the launch.
 // ---------------------------------------------------------------------------
 
 constexpr int kExtentWarps = 4, kExtentIds = 4;                 // ids of a lane at a time
@@ -212,19 +212,24 @@ __global__ void __launch_bounds__(kExtentWarps * 32) sda_region_extent_kernel(co
     const int64_t row = static_cast<int64_t>(blockIdx.x) * kExtentWarps + (threadIdx.x >> 5);
     if (row >= p.requests)
         return;
-    int last = -1;
-    const bool active = p.active[row * p.act_s] != 0;
-    if (active) {
-        const int pos = p.positions[row * p.pos_s];
-        const int most = pos >= 0 ? pos / p.region_tokens : -1;               // the last region that it sees
-        const int32_t *ids = p.regions + row * p.reg_s0;
-        for (int end = p.listed; end > 0 && last < 0; end -= 32 * kExtentIds) {
-            int id[kExtentIds];
+    const int32_t *ids = p.regions + row * p.reg_s0;
+    int id[kExtentIds];                         // the list's last ones, beside the row's position and flag: one latency
+    auto load = [&](int end) {
 #pragma unroll
-            for (int k = 0; k < kExtentIds; ++k) {
-                const int i = end - 1 - 32 * k - lane;
-                id[k] = i >= 0 ? ids[i] : -1;
-            }
+        for (int k = 0; k < kExtentIds; ++k) {
+            const int i = end - 1 - 32 * k - lane;
+            id[k] = i >= 0 ? ids[i] : -1;
+        }
+    };
+    load(p.listed);
+    const int pos = p.positions[row * p.pos_s];
+    const bool active = p.active[row * p.act_s] != 0;
+    int last = -1;
+    if (active) {
+        const int most = pos >= 0 ? pos / p.region_tokens : -1;               // the last region that it sees
+        for (int end = p.listed; end > 0 && last < 0; end -= 32 * kExtentIds) {
+            if (end < p.listed)
+                load(end);
 #pragma unroll
             for (int k = 0; k < kExtentIds; ++k) {
                 if (id[k] < -1)
@@ -289,8 +294,8 @@ constexpr int kWholeTiles = 8, kAloneTiles = 12;
 constexpr int kRounds = 4;
 // Rows' lists are looked at for their extents where a worker has at least this many tiles of their
 // room (1024 slots, E4M3, 192 dims, 2 groups; not looked at, looked at: 256 requests of 1K to 2K tokens
-// 196 us, 100, of 16K to 32K 296, 301; 16 requests of 1K to 3K 33.2, 28.5, of 16K to 20K 39.5, 42.7;
-// four of either, which have fewer tiles, 19.6 and 20.9, and 25.6 and 23.5).
+// 192 us, 90, of 16K to 32K 284, 292; 16 requests of 1K to 3K 32.4, 26.6, of 16K to 20K 38.4, 40.0;
+// four of either, which have fewer tiles, 19.3 and 20.6, and 24.1 and 22.6).
 constexpr int kExtentTiles = 8;
 
 // CTAs of a launch, at most.

@@ -47,7 +47,7 @@
 // and of those a row's selected regions can be walked instead of a request's tokens.
 // 16 documents of 64K to 128K tokens (192 dims, 4 groups): E4M3 377 to 379 us, 6.6 TB/s
 // (one scale for all: 370 to 376), integers 414, 6.1 TB/s, bound by their conversions; 512 rows of
-// 1024 regions of 8 tokens (E4M3, 192 dims) 285 to 289 us, 5.7 TB/s, in TMA boxes of 3 KB.
+// 1024 regions of 8 tokens (E4M3, 192 dims) 291 us, 5.6 TB/s, in TMA boxes of 3 KB.
 #pragma once
 
 #include "sda_quant.cuh"
@@ -88,6 +88,11 @@ constexpr float kLn2 = 0.6931471805599453f;
 // E4M3 or integers with scales of their own for each block of tokens and head.  All
 // one-byte kinds are multiplied in fp16, which holds them exactly.
 enum Kind { kBf16, kE4m3, kScaledE4m3, kScaledInt8 };
+
+// What a unit's tiles are: a request's tokens, or a row's selected regions, as many as
+// its list has room for or as the extent kernel found (a run-time choice of the two in
+// one kernel: 512 rows of 1024 regions 300 us, so 292).
+enum Walked { kTokens, kRegions, kExtents };
 
 struct JoinItem {
     int pieces, request, group, first;          // the unit, and the worker with its first piece
@@ -178,9 +183,10 @@ constexpr int kStateBytes = 136;                // WarpState
 // requests of 16K tokens (most with 32 and 64 query rows), 1 to 12 % for 60 of up to
 // 500, at 64, 192 and 256 dims.  ALONE: each CTA has one unit, its workers a share of
 // the unit's tiles each.
-template <int KIND, int D, int MT, bool FULL, bool ALONE = false, bool REGIONS = false>
+template <int KIND, int D, int MT, bool FULL, bool ALONE = false, int WALKED = kTokens>
 struct Shape {
-    static constexpr bool kFull = FULL, kAlone = ALONE, kRegions = REGIONS, kScaled = KIND >= kScaledE4m3;
+    static constexpr int kWalked = WALKED;
+    static constexpr bool kFull = FULL, kAlone = ALONE, kRegions = WALKED != kTokens, kScaled = KIND >= kScaledE4m3;
     static constexpr bool FP8 = KIND != kBf16;
     static constexpr int kUnitCost = unit_cost(kScaled);
     static constexpr int kElt = FP8 ? 1 : 2;
@@ -225,7 +231,7 @@ struct Segment {
     int request, group, first, last, tiles, len;   // tiles [first, last) of the unit's `tiles`
 };
 
-template <bool REGIONS, int COST>
+template <int WALKED, int COST>
 struct Walk {
     long long left;                             // line from the unit's start to the part's end
     int request, group, tile;                   // (whole_units: units still to take)
@@ -235,8 +241,10 @@ struct Walk {
     // as it was.
     static __device__ __forceinline__ int length(const Params &p, int q)
     {
-        if constexpr (REGIONS)
-            return p.extents ? p.extents[q] : p.active[q * p.act_s] ? p.cap : p.clear_inactive ? 0 : -1;
+        if constexpr (WALKED == kExtents)
+            return p.extents[q];
+        else if constexpr (WALKED == kRegions)
+            return p.active[q * p.act_s] ? p.cap : p.clear_inactive ? 0 : -1;
         else
             return min(p.seq_lens[q * p.len_s], p.cap);
     }
@@ -696,7 +704,7 @@ struct WarpState {
     int used, number;                           // workers with a part; this one's number
 };
 
-static_assert(sizeof(WarpState<Walk<false, 0>>) == kStateBytes, "shared memory of a warp");
+static_assert(sizeof(WarpState<Walk<kTokens, 0>>) == kStateBytes, "shared memory of a warp");
 
 // A worker's ring of stages: their places, barriers, headers (the slots that
 // hold tokens) and how often each was issued.
@@ -711,7 +719,7 @@ struct Ring {
 // in one segment.
 template <class S>
 struct Feed {
-    Place<Walk<S::kRegions, S::kUnitCost>> *at_line;                // of the next segment to look up
+    Place<Walk<S::kWalked, S::kUnitCost>> *at_line;                // of the next segment to look up
     bool more;
     int tile;                                   // of the segment, the next to look up
     int per_stage, batch, lane_stage, lane_piece;   // pieces of a stage, stages of a batch; the lane's place in one
@@ -765,7 +773,7 @@ struct Feed {
     }
 
     // The feed's place is where the worker's part begins.
-    __device__ __forceinline__ void start(const Params &p, Place<Walk<S::kRegions, S::kUnitCost>> *place, int lane)
+    __device__ __forceinline__ void start(const Params &p, Place<Walk<S::kWalked, S::kUnitCost>> *place, int lane)
     {
         at_line = place;
         per_stage = S::kFull ? 1 : p.tile / p.piece;
@@ -927,13 +935,14 @@ private:
     }
 };
 
-template <int KIND, int D, int MT, bool FULL, bool ALONE, bool REGIONS>
-__global__ void __launch_bounds__(kThreads, Shape<KIND, D, MT, FULL, ALONE, REGIONS>::kPerSm)
+template <int KIND, int D, int MT, bool FULL, bool ALONE, int WALKED>
+__global__ void __launch_bounds__(kThreads, Shape<KIND, D, MT, FULL, ALONE, WALKED>::kPerSm)
     sda_paged_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_constant__ Params p)
 {
-    using S = Shape<KIND, D, MT, FULL, ALONE, REGIONS>;
+    using S = Shape<KIND, D, MT, FULL, ALONE, WALKED>;
     constexpr int kUnitCost = S::kUnitCost;
-    using Line = Walk<REGIONS, kUnitCost>;
+    constexpr bool REGIONS = S::kRegions;
+    using Line = Walk<WALKED, kUnitCost>;
     constexpr bool FP8 = S::FP8, SCALED = S::kScaled, INT8 = KIND == kScaledInt8;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -1643,41 +1652,47 @@ __global__ void __launch_bounds__(kThreads, Shape<KIND, D, MT, FULL, ALONE, REGI
     }
 }
 
-template <int KIND, int D, int MT, bool FULL, bool ALONE, bool REGIONS>
+template <int KIND, int D, int MT, bool FULL, bool ALONE, int WALKED>
 sda_status launch_shape(const CUtensorMap &tmap, const Params &p, void *stream)
 {
-    using S = Shape<KIND, D, MT, FULL, ALONE, REGIONS>;
+    using S = Shape<KIND, D, MT, FULL, ALONE, WALKED>;
     static size_t raised[64] = {};
-    if (!raise_smem(sda_paged_kernel<KIND, D, MT, FULL, ALONE, REGIONS>, S::kBytes, raised))
+    if (!raise_smem(sda_paged_kernel<KIND, D, MT, FULL, ALONE, WALKED>, S::kBytes, raised))
         return SDA_ERR_CUDA;
-    return launch_pdl(sda_paged_kernel<KIND, D, MT, FULL, ALONE, REGIONS>, dim3(static_cast<unsigned>(p.ctas)), dim3(kThreads),
+    return launch_pdl(sda_paged_kernel<KIND, D, MT, FULL, ALONE, WALKED>, dim3(static_cast<unsigned>(p.ctas)), dim3(kThreads),
                       S::kBytes, stream, tmap, p);
 }
 
-template <int KIND, int D, int MT, bool REGIONS>
+template <int KIND, int D, int MT, int WALKED>
+sda_status launch_line(const CUtensorMap &tmap, const Params &p, void *stream)
+{
+    return p.piece == Shape<KIND, D, MT, true>::kSlots ? launch_shape<KIND, D, MT, true, false, WALKED>(tmap, p, stream)
+                                                       : launch_shape<KIND, D, MT, false, false, WALKED>(tmap, p, stream);
+}
+
+template <int KIND, int D, int MT, int WALKED>
 sda_status launch_tiles(const CUtensorMap &tmap, const Params &p, void *stream)
 {
     if (p.cta_units)
-        return p.piece == Shape<KIND, D, MT, true, true>::kSlots ? launch_shape<KIND, D, MT, true, true, REGIONS>(tmap, p, stream)
-                                                                 : launch_shape<KIND, D, MT, false, true, REGIONS>(tmap, p, stream);
-    return p.piece == Shape<KIND, D, MT, true>::kSlots ? launch_shape<KIND, D, MT, true, false, REGIONS>(tmap, p, stream)
-                                                       : launch_shape<KIND, D, MT, false, false, REGIONS>(tmap, p, stream);
+        return p.piece == Shape<KIND, D, MT, true, true>::kSlots ? launch_shape<KIND, D, MT, true, true, WALKED>(tmap, p, stream)
+                                                                 : launch_shape<KIND, D, MT, false, true, WALKED>(tmap, p, stream);
+    return launch_line<KIND, D, MT, WALKED>(tmap, p, stream);
 }
 
 template <int KIND, int D>
 sda_status launch_dim(const CUtensorMap &tmap, const Params &p, void *stream)
 {
     const int tiles = tiles_of_rows(p.rows);
-    return tiles == 1   ? launch_tiles<KIND, D, 1, false>(tmap, p, stream)
-           : tiles == 2 ? launch_tiles<KIND, D, 2, false>(tmap, p, stream)
-                        : launch_tiles<KIND, D, 4, false>(tmap, p, stream);
+    return tiles == 1   ? launch_tiles<KIND, D, 1, kTokens>(tmap, p, stream)
+           : tiles == 2 ? launch_tiles<KIND, D, 2, kTokens>(tmap, p, stream)
+                        : launch_tiles<KIND, D, 4, kTokens>(tmap, p, stream);
 }
 
 // Regions: a row of at most 16 heads is one tile.
 template <int KIND, int D>
 sda_status launch_regions(const CUtensorMap &tmap, const Params &p, void *stream)
 {
-    return launch_tiles<KIND, D, 1, true>(tmap, p, stream);
+    return p.extents ? launch_line<KIND, D, 1, kExtents>(tmap, p, stream) : launch_tiles<KIND, D, 1, kRegions>(tmap, p, stream);
 }
 
 // One translation unit per head size and cache type.
