@@ -640,8 +640,8 @@ def sparse_decode_quantised_attention(query, cache, scales, regions, block_table
     include/sdattn.h for the contract."""
     lib = _lib or load()
     need = 0
-    if workspace is None:                       # the header at least, where the call is refused
-        need = quantised_workspace_bytes(query.shape[0], query.shape[1], query.shape[-1]) or 256
+    if workspace is None:                       # quantised_workspace_bytes, without a call for it
+        need = _paged_need(query, 1) + (4 * query.shape[0] + 255) // 256 * 256
     tensors = query, cache, scales, regions, block_table, positions, active, output, lse, gate
     rc = None
     if stream is None:

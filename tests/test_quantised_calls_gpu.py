@@ -13,20 +13,33 @@ pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda", 0)
 
 
-@pytest.mark.parametrize("regions", [None, (2500, 8)])
-@pytest.mark.parametrize("ql", [1, 2])
-def test_a_wait_that_runs_out_is_flagged_and_recoverable(regions, ql):
+@pytest.mark.parametrize("regions,ql,D,int8", [(None, 1, 192, False), (None, 2, 192, True), ((2500, 8), 1, 192, False), ((1200, 64), 2, 64, True)])
+def test_a_wait_that_runs_out_is_flagged_and_recoverable(regions, ql, D, int8):
     """Stages and their scales are still on their way when every wait gives up at once: the flag is raised, the
-    copies land before the blocks end, and the next call is right."""
-    # (many stages a worker: the first few are there by the time that its queries are)
-    p = Problem([20000, 30000, 9000] * 4, G=4, H=16, D=192, block=64, span=32, ql=ql, int8=ql == 2, regions=regions)
+    copies land before the blocks end, and the next call is right.  (Whether a stage is late is a matter of time:
+    more calls where none was.)"""
+    p = Problem([20000, 30000, 9000] * 4, G=4, H=16, D=D, block=64, span=32, ql=ql, int8=int8, regions=regions)
     by = regions is not None
     ws = p.workspace()
+    out, lse, other = torch.empty_like(p.query), torch.empty(p.query.shape[:2], device="cuda"), torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    kw = dict(scale=p.scale, query_len=p.ql, lse=lse, workspace=ws)
+    flags = 0
     sda.set_wait_limit_ns(0)
     try:
-        p.run(regions=by, workspace=ws, flags=sda.FLAG_TIMEOUT)
+        for _ in range(50):
+            other.fill_(1)                      # nothing of the cache lies in L2
+            if by:
+                sda.sparse_decode_quantised_attention(p.query, p.cache, p.scales, p.regions, p.table, p.positions, p.active, out,
+                                                      region_tokens=p.rt, **kw)
+            else:
+                sda.sparse_decode_quantised_paged_attention(p.query, p.cache, p.scales, p.table, p.seq_lens, out, **kw)
+            torch.cuda.synchronize()
+            flags |= sda.read_errors(ws, clear=True)
+            if flags:
+                break
     finally:
         sda.set_wait_limit_ns(10 ** 9)
+    assert flags == sda.FLAG_TIMEOUT
     p.check(*p.run(regions=by, workspace=ws), regions=by)
 
 
