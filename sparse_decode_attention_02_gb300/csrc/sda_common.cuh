@@ -193,6 +193,27 @@ inline sda_status launch_pdl(void (*kernel)(Params...), dim3 grid, dim3 block, s
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args &&>(args)...) == cudaSuccess ? SDA_OK : SDA_ERR_CUDA;
 }
 
+// The same in clusters of `size` CTAs (1: none).
+template <typename... Params, typename... Args>
+inline sda_status launch_pdl_clusters(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, int size, void *stream,
+                                      Args &&...args)
+{
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(size);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cfg.attrs = attr;
+    cfg.numAttrs = size > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args &&>(args)...) == cudaSuccess ? SDA_OK : SDA_ERR_CUDA;
+}
+
 // Raises a kernel's dynamic shared memory limit once per device.
 template <typename Kernel>
 inline bool raise_smem(Kernel kernel, size_t bytes, size_t (&raised)[64])

@@ -94,6 +94,12 @@ enum Kind { kBf16, kE4m3, kScaledE4m3, kScaledInt8 };
 // one kernel: 512 rows of 1024 regions 300 us, so 292).
 enum Walked { kTokens, kRegions, kExtents };
 
+// Who takes a unit: workers of the line, their pieces joined by another kernel (4 to 6 us of a
+// small call); a CTA alone; or a cluster of CTAs, which merge through one another's shared
+// memory in the same kernel.
+enum Takers { kOnLine, kCta, kCluster };
+constexpr int kMaxCluster = 8;
+
 struct JoinItem {
     int pieces, request, group, first;          // the unit, and the worker with its first piece
     int row, rows, spare[2];                    // query rows of the item
@@ -136,6 +142,7 @@ struct Params {
     int table_cols, block, cap;                 // cap: tokens the table's width can hold
     int piece, tile;                            // tokens of a TMA box and of a stage
     int ctas, workers, whole_units, cta_units;   // cta_units: ALONE
+    int cluster;                                // CTAs of a unit: 1 or, a power of two, of a cluster
     unsigned long long per_block_inv, tile_inv, workers_inv;    // inverse_of the pieces of a page, tile, workers
     int q_vec, o_vec;                           // 8-byte loads of q and stores of the output
     unsigned long long span_inv, block_inv, per_region_inv, region_groups_inv, request_rows_inv;
@@ -183,16 +190,16 @@ constexpr int kStateBytes = 136;                // WarpState
 // requests of 16K tokens (most with 32 and 64 query rows), 1 to 12 % for 60 of up to
 // 500, at 64, 192 and 256 dims.  ALONE: each CTA has one unit, its workers a share of
 // the unit's tiles each.
-template <int KIND, int D, int MT, bool FULL, bool ALONE = false, int WALKED = kTokens>
+template <int KIND, int D, int MT, bool FULL, int ALONE = kOnLine, int WALKED = kTokens>
 struct Shape {
     static constexpr int kWalked = WALKED;
-    static constexpr bool kFull = FULL, kAlone = ALONE, kRegions = WALKED != kTokens, kScaled = KIND >= kScaledE4m3;
+    static constexpr bool kFull = FULL, kAlone = ALONE != kOnLine, kRegions = WALKED != kTokens, kScaled = KIND >= kScaledE4m3;
     static constexpr bool FP8 = KIND != kBf16;
     static constexpr int kUnitCost = unit_cost(kScaled);
     static constexpr int kElt = FP8 ? 1 : 2;
     static constexpr int kRowBytes = 2 * D * kElt;
     static constexpr int kBands = kRowBytes / 128;
-    static constexpr int kSlots = stage_slots(kRowBytes, MT, ALONE);
+    static constexpr int kSlots = stage_slots(kRowBytes, MT, kAlone);
     static constexpr int kStageBytes = kSlots * kRowBytes;
     static constexpr int kSteps = D / 16;                       // QK k-steps
     // Log2 units that the running maximum may lag behind the true one, and that the
@@ -935,11 +942,50 @@ private:
     }
 };
 
-template <int KIND, int D, int MT, bool FULL, bool ALONE, int WALKED>
-__global__ void __launch_bounds__(kThreads, Shape<KIND, D, MT, FULL, ALONE, WALKED>::kPerSm)
+// All threads of the cluster's CTAs: what they wrote before is seen by all after.
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+__device__ __forceinline__ int cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return static_cast<int>(r);
+}
+
+// The address of `addr` of this CTA's shared memory in that of CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t peer(uint32_t addr, int rank)
+{
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+    return a;
+}
+
+__device__ __forceinline__ float peer_f32(uint32_t at)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float4 peer_f32x4(uint32_t at)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(at)
+                 : "memory");
+    return v;
+}
+
+template <int KIND, int D, int MT, bool FULL, int TAKERS, int WALKED>
+__global__ void __launch_bounds__(kThreads, Shape<KIND, D, MT, FULL, TAKERS, WALKED>::kPerSm)
     sda_paged_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_constant__ Params p)
 {
-    using S = Shape<KIND, D, MT, FULL, ALONE, WALKED>;
+    using S = Shape<KIND, D, MT, FULL, TAKERS, WALKED>;
+    constexpr bool ALONE = S::kAlone, CLUSTER = TAKERS == kCluster;     // CLUSTER: together with others
     constexpr int kUnitCost = S::kUnitCost;
     constexpr bool REGIONS = S::kRegions;
     using Line = Walk<WALKED, kUnitCost>;
@@ -975,12 +1021,16 @@ __global__ void __launch_bounds__(kThreads, Shape<KIND, D, MT, FULL, ALONE, WALK
     WarpState<Line> *state = reinterpret_cast<WarpState<Line> *>(smem + S::kStateOff) + warp;
     if constexpr (ALONE) {
         Segment &seg = state->here.seg;
-        seg.request = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.groups));
-        seg.group = static_cast<int>(blockIdx.x) - seg.request * p.groups;
+        const unsigned of_cluster = CLUSTER ? p.cluster : 1;
+        const unsigned unit = blockIdx.x / of_cluster;
+        const int mine = static_cast<int>(blockIdx.x - unit * of_cluster) * S::kWorkers + worker;
+        const int all = static_cast<int>(of_cluster) * S::kWorkers;
+        seg.request = static_cast<int>(unit / static_cast<unsigned>(p.groups));
+        seg.group = static_cast<int>(unit) - seg.request * p.groups;
         seg.len = Line::length(p, seg.request);
         seg.tiles = Line::tiles_of(p, seg.len);
-        seg.first = seg.tiles * worker / S::kWorkers;
-        seg.last = seg.tiles * (worker + 1) / S::kWorkers;
+        seg.first = seg.tiles * mine / all;
+        seg.last = seg.tiles * (mine + 1) / all;
     } else {
         long long total;
         int used, v;
@@ -1480,6 +1530,71 @@ __global__ void __launch_bounds__(kThreads, Shape<KIND, D, MT, FULL, ALONE, WALK
                     }
                 }
             }
+            if constexpr (CLUSTER) {
+                // ---- A CTA's share of the rows, from the pieces of all workers of the cluster:
+                // a lane looks at a piece's maximum, sum and unit, then all lanes add the outputs up.
+                cluster_sync();
+                const int lg_c = __ffs(p.cluster) - 1, pieces = p.cluster * S::kWorkers;
+                const int lg = (MT == 1 ? 3 : 2) + (R <= 8 * MT ? 1 : 0) + lg_c;       // threads of a row
+                const int r = static_cast<int>(threadIdx.x >> lg) * p.cluster + cluster_rank();
+                const int rr = r < R ? r : 0, c0 = static_cast<int>(threadIdx.x) & ((1 << lg) - 1);
+                const int among = min(32, 1 << lg), k = lane & (among - 1), lane0 = lane - k;   // pieces <= among
+                const uint32_t stats_at = smem_u32(stats), outs_at = smem_u32(outs), units_at = smem_u32(units);
+                float m = -INFINITY, l = 0.0f, u = 1.0f;
+                if (k < pieces) {
+                    const int cta = k / S::kWorkers, w = k - cta * S::kWorkers;
+                    m = peer_f32(peer(stats_at + (w * kRows + rr) * 8, cta));
+                    l = peer_f32(peer(stats_at + (w * kRows + rr) * 8 + 4, cta));
+                    if constexpr (SCALED)
+                        u = peer_f32(peer(units_at + w * 4, cta));
+                }
+                float M = m;
+                for (int i = among / 2; i; i >>= 1)
+                    M = fmaxf(M, __shfl_xor_sync(~0u, M, i));
+                float of = m == -INFINITY ? 1.0f : fast_exp2(m - M);    // all of a worker that saw nothing is 0 (or not a number)
+                float L = l * of;
+                for (int i = among / 2; i; i >>= 1)
+                    L += __shfl_xor_sync(~0u, L, i);
+                const bool empty = M == -INFINITY && L == 0.0f;
+                of *= (empty ? 0.0f : 1.0f / L) * u;
+                const int h = rr - token_of(rr) * H;
+                float f = 1.0f;
+                if (p.gate)
+                    f = gate_of(rr, h);
+                uint16_t *out = p.output + row_of(rr) * p.o_s0 + h * p.o_s1;
+                for (int d0 = 0; d0 < D; d0 += 4 << lg) {       // as many turns for every lane
+                    const int d = d0 + 4 * c0;
+                    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    // sixteen loads from other SMs on their way at a time (four: 2 us more)
+#pragma unroll 16
+                    for (int i = 0; i < pieces; ++i) {
+                        const float g = __shfl_sync(~0u, of, lane0 + i);
+                        if (d < D) {
+                            const int cta = i / S::kWorkers, w = i - cta * S::kWorkers;
+                            const float4 y = peer_f32x4(peer(outs_at + (w * kOut + rr * kStride + d) * 4, cta));
+                            x.x += g * y.x;
+                            x.y += g * y.y;
+                            x.z += g * y.z;
+                            x.w += g * y.w;
+                        }
+                    }
+                    if (d < D && r < R) {
+                        const uint2 w = make_uint2(pack_bf16(x.x * f, x.y * f), pack_bf16(x.z * f, x.w * f));
+                        if (p.o_vec) {
+                            *reinterpret_cast<uint2 *>(out + d) = w;
+                        } else {
+                            out[d] = static_cast<uint16_t>(w.x);
+                            out[d + 1] = static_cast<uint16_t>(w.x >> 16);
+                            out[d + 2] = static_cast<uint16_t>(w.y);
+                            out[d + 3] = static_cast<uint16_t>(w.y >> 16);
+                        }
+                    }
+                }
+                if (c0 == 0 && r < R && p.lse)
+                    p.lse[row_of(r) * p.l_s0 + h * p.l_s1] = (empty ? -INFINITY : M + log2f(L)) * kLn2;
+                cluster_sync();                 // the others have read this CTA's pieces
+                break;                          // the unit is done
+            }
             __syncthreads();
             const int64_t first = static_cast<int64_t>(v - worker) * 2 + (from_start ? 1 : 0);
             // As many threads for a row as there are for 16, or 8, of each tile.
@@ -1623,7 +1738,9 @@ __global__ void __launch_bounds__(kThreads, Shape<KIND, D, MT, FULL, ALONE, WALK
     }
 
     // Requests without tokens: zeros.  A CTA alone with a unit knows its own.
-    for (int q = blockIdx.x; q < (ALONE ? p.requests * p.groups : p.requests); q += gridDim.x) {
+    for (int q = blockIdx.x; q < (CLUSTER ? gridDim.x : ALONE ? p.requests * p.groups : p.requests); q += gridDim.x) {
+        if (CLUSTER && cluster_rank() > 0)
+            break;
         const int request = ALONE ? state->here.seg.request : q, g0 = ALONE ? state->here.seg.group : 0;
         const int len = ALONE ? state->here.seg.len : Line::length(p, q);
         if (!REGIONS && threadIdx.x == 0 && (!ALONE || len == p.cap) && p.seq_lens[request * p.len_s] > p.cap)
@@ -1652,31 +1769,33 @@ __global__ void __launch_bounds__(kThreads, Shape<KIND, D, MT, FULL, ALONE, WALK
     }
 }
 
-template <int KIND, int D, int MT, bool FULL, bool ALONE, int WALKED>
+template <int KIND, int D, int MT, bool FULL, int TAKERS, int WALKED>
 sda_status launch_shape(const CUtensorMap &tmap, const Params &p, void *stream)
 {
-    using S = Shape<KIND, D, MT, FULL, ALONE, WALKED>;
+    using S = Shape<KIND, D, MT, FULL, TAKERS, WALKED>;
     static size_t raised[64] = {};
-    if (!raise_smem(sda_paged_kernel<KIND, D, MT, FULL, ALONE, WALKED>, S::kBytes, raised))
+    if (!raise_smem(sda_paged_kernel<KIND, D, MT, FULL, TAKERS, WALKED>, S::kBytes, raised))
         return SDA_ERR_CUDA;
-    return launch_pdl(sda_paged_kernel<KIND, D, MT, FULL, ALONE, WALKED>, dim3(static_cast<unsigned>(p.ctas)), dim3(kThreads),
-                      S::kBytes, stream, tmap, p);
+    return launch_pdl_clusters(sda_paged_kernel<KIND, D, MT, FULL, TAKERS, WALKED>, dim3(static_cast<unsigned>(p.ctas)),
+                               dim3(kThreads), S::kBytes, TAKERS == kCluster ? p.cluster : 1, stream, tmap, p);
 }
 
-template <int KIND, int D, int MT, int WALKED>
-sda_status launch_line(const CUtensorMap &tmap, const Params &p, void *stream)
+template <int KIND, int D, int MT, int TAKERS, int WALKED>
+sda_status launch_pieces(const CUtensorMap &tmap, const Params &p, void *stream)
 {
-    return p.piece == Shape<KIND, D, MT, true>::kSlots ? launch_shape<KIND, D, MT, true, false, WALKED>(tmap, p, stream)
-                                                       : launch_shape<KIND, D, MT, false, false, WALKED>(tmap, p, stream);
+    return p.piece == Shape<KIND, D, MT, true, TAKERS>::kSlots ? launch_shape<KIND, D, MT, true, TAKERS, WALKED>(tmap, p, stream)
+                                                               : launch_shape<KIND, D, MT, false, TAKERS, WALKED>(tmap, p, stream);
 }
 
 template <int KIND, int D, int MT, int WALKED>
 sda_status launch_tiles(const CUtensorMap &tmap, const Params &p, void *stream)
 {
-    if (p.cta_units)
-        return p.piece == Shape<KIND, D, MT, true, true>::kSlots ? launch_shape<KIND, D, MT, true, true, WALKED>(tmap, p, stream)
-                                                                 : launch_shape<KIND, D, MT, false, true, WALKED>(tmap, p, stream);
-    return launch_line<KIND, D, MT, WALKED>(tmap, p, stream);
+    // clusters: where the host chooses them
+    if constexpr (Shape<KIND, D, MT, true>::kScaled && MT <= 2)
+        if (p.cluster > 1)
+            return launch_pieces<KIND, D, MT, kCluster, WALKED>(tmap, p, stream);
+    return p.cta_units ? launch_pieces<KIND, D, MT, kCta, WALKED>(tmap, p, stream)
+                       : launch_pieces<KIND, D, MT, kOnLine, WALKED>(tmap, p, stream);
 }
 
 template <int KIND, int D>
@@ -1692,7 +1811,8 @@ sda_status launch_dim(const CUtensorMap &tmap, const Params &p, void *stream)
 template <int KIND, int D>
 sda_status launch_regions(const CUtensorMap &tmap, const Params &p, void *stream)
 {
-    return p.extents ? launch_line<KIND, D, 1, kExtents>(tmap, p, stream) : launch_tiles<KIND, D, 1, kRegions>(tmap, p, stream);
+    return p.extents ? launch_pieces<KIND, D, 1, kOnLine, kExtents>(tmap, p, stream)
+                     : launch_tiles<KIND, D, 1, kRegions>(tmap, p, stream);
 }
 
 // One translation unit per head size and cache type.

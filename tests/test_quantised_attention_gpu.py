@@ -440,3 +440,28 @@ def test_long_contexts_keep_their_mean(int8, peak):
     # weights' roundings have no sign of their own: 2^-11 / sqrt(tokens that count) of the values' size, six times over
     spread = torch.sqrt((w * w) @ (x[:, D:] ** 2))
     assert (far <= want.abs() * 2.0 ** -8 + 6 * spread * 2.0 ** -11 + 100 * 2.0 ** -15).all(), far.max().item()
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("D,H,ql", [(64, 16, 1), (128, 5, 1), (192, 16, 2), (192, 8, 1), (256, 3, 4), (256, 16, 2), (64, 1, 1)])
+@pytest.mark.parametrize("lens,G", [([1200], 4), ([4000, 0, 3000, 7], 4), ([700, -1, 650], 12), ([2000], 1), ([257, 33], 38), ([9000, 0], 2)])
+def test_few_units_by_clusters(lens, G, D, H, ql, int8):
+    """From two to eight CTAs a unit, some of them or all of their workers without a tile; lengths of 0 and below."""
+    check(lens, G=G, H=H, ql=ql, D=D, int8=int8, block=32, span=16, gate=D == 192, scale_std=1.0)
+    check(lens, G=G, H=H, ql=ql, D=D, int8=int8, block=24, span=8, spare=5)
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("D,H", [(64, 16), (128, 5), (192, 16), (256, 1)])
+def test_few_rows_of_regions_by_clusters(D, H, int8):
+    for count, rt in ((40, 64), (33, 8), (150, 16), (9, 128)):
+        check([3000, 500, 9], G=2, H=H, D=D, int8=int8, block=32, span=16, regions=(count, rt), gate=True)
+    p = check([5000], G=1, H=H, D=D, int8=int8, block=64, span=64, regions=(64, 64))
+    left = p.query.clone() * 3, torch.full(p.query.shape[:2], 5.0, device="cuda")
+    for on in (False, True):
+        p.active[:] = on
+        out, lse = p.run(regions=True, out=left[0].clone(), lse=left[1].clone(), clear_inactive=False)
+        p.check(out, lse, regions=True, left=left)
+    p.regions[:] = -1
+    out, lse = p.run(regions=True)
+    assert (out.view(torch.int16) == 0).all() and (lse == -float("inf")).all()

@@ -13,12 +13,17 @@ pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda", 0)
 
 
-@pytest.mark.parametrize("regions,ql,D,int8", [(None, 1, 192, False), (None, 2, 192, True), ((2500, 8), 1, 192, False), ((1200, 64), 2, 64, True)])
-def test_a_wait_that_runs_out_is_flagged_and_recoverable(regions, ql, D, int8):
+LONG = [20000, 30000, 9000] * 4
+
+
+@pytest.mark.parametrize("lens,regions,ql,D,int8", [(LONG, None, 1, 192, False), (LONG, None, 2, 192, True), (LONG, (2500, 8), 1, 192, False),
+                                                    (LONG, (1200, 64), 2, 64, True), ([6000, 300], None, 1, 192, False),
+                                                    ([7000], (80, 64), 1, 256, True)])
+def test_a_wait_that_runs_out_is_flagged_and_recoverable(lens, regions, ql, D, int8):
     """Stages and their scales are still on their way when every wait gives up at once: the flag is raised, the
     copies land before the blocks end, and the next call is right.  (Whether a stage is late is a matter of time:
     more calls where none was.)"""
-    p = Problem([20000, 30000, 9000] * 4, G=4, H=16, D=D, block=64, span=32, ql=ql, int8=int8, regions=regions)
+    p = Problem(lens, G=4, H=16, D=D, block=64, span=32, ql=ql, int8=int8, regions=regions)
     by = regions is not None
     ws = p.workspace()
     out, lse, other = torch.empty_like(p.query), torch.empty(p.query.shape[:2], device="cuda"), torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
