@@ -1085,7 +1085,9 @@ __global__ void __launch_bounds__(kThreads, Shape<KIND, D, MT, FULL, TAKERS, WAL
             Segment seg;
             if constexpr (ALONE) {
                 seg = state->here.seg;
-                if (seg.tiles == 0)
+                // A cluster's CTAs all come to its barriers, whatever each has read (lengths that
+                // change meanwhile must not leave some of them waiting).
+                if (!CLUSTER && seg.tiles == 0)
                     break;
             } else {
                 if (!state->here.next(p, state->part_end, seg))
@@ -1578,7 +1580,7 @@ __global__ void __launch_bounds__(kThreads, Shape<KIND, D, MT, FULL, TAKERS, WAL
                             x.w += g * y.w;
                         }
                     }
-                    if (d < D && r < R) {
+                    if (d < D && r < R && seg.len >= 0) {       // below 0: left as it was
                         const uint2 w = make_uint2(pack_bf16(x.x * f, x.y * f), pack_bf16(x.z * f, x.w * f));
                         if (p.o_vec) {
                             *reinterpret_cast<uint2 *>(out + d) = w;
@@ -1590,7 +1592,7 @@ __global__ void __launch_bounds__(kThreads, Shape<KIND, D, MT, FULL, TAKERS, WAL
                         }
                     }
                 }
-                if (c0 == 0 && r < R && p.lse)
+                if (c0 == 0 && r < R && seg.len >= 0 && p.lse)
                     p.lse[row_of(r) * p.l_s0 + h * p.l_s1] = (empty ? -INFINITY : M + log2f(L)) * kLn2;
                 cluster_sync();                 // the others have read this CTA's pieces
                 break;                          // the unit is done
@@ -1745,7 +1747,7 @@ __global__ void __launch_bounds__(kThreads, Shape<KIND, D, MT, FULL, TAKERS, WAL
         const int len = ALONE ? state->here.seg.len : Line::length(p, q);
         if (!REGIONS && threadIdx.x == 0 && (!ALONE || len == p.cap) && p.seq_lens[request * p.len_s] > p.cap)
             atomicOr(p.flags, SDA_FLAG_BOUNDS);
-        if (len != 0)
+        if (len != 0 || CLUSTER)                // a cluster has merged nothing to zeros
             continue;
         for (int gr = warp + g0 * H; gr < (ALONE ? (g0 + 1) * H : p.groups * H); gr += kWarps)          // [group][head]
             for (int j = 0; j < p.query_len; ++j) {
