@@ -465,3 +465,55 @@ def test_few_rows_of_regions_by_clusters(D, H, int8):
     p.regions[:] = -1
     out, lse = p.run(regions=True)
     assert (out.view(torch.int16) == 0).all() and (lse == -float("inf")).all()
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("lens,G", [([160, 90], 1), ([1600, 200], 2), ([40000, 3000], 2)])
+def test_tables_too_narrow_and_bad_pages(lens, G, int8):
+    """A length past the table counts as what the table holds, and a page outside the cache is left out, with a flag: by a
+    CTA alone, a cluster and the line."""
+    p = Problem(lens, G=G, H=8, D=128, block=16, span=8, int8=int8)
+    whole = p.table
+    p.table = whole[:, :-2]
+    out, lse = p.run(flags=sda.FLAG_BOUNDS)
+    held = 16 * p.table.shape[1]
+    narrow = p.lens
+    p.lens = [min(n, held) for n in narrow]
+    p.check(out, lse)
+    p.lens, p.table = narrow, whole.clone()
+    p.check(*p.run())
+    p.table[0, 0], p.table[1, 1] = -1, 10 ** 7
+    out, lse = p.run(flags=sda.FLAG_BOUNDS)
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    # the same requests without those pages' tokens
+    p.host_cache, p.host_scales = p.cache.cpu(), p.scales.cpu()
+    for r, gone in ((0, range(0, 16)), (G, range(16, 32))):
+        k, v, top = p.row(r, False)
+        keep = torch.tensor([t not in gone for t in range(len(k))])
+        x = p.query[r].cpu().double()
+        o, _, spread, slack = quant_util.attend(x, k[keep], v[keep], float(np.float32(p.scale)))
+        bound = quant_util.attention_bound(o, spread, slack, top * (127 if int8 else 448), len(k))
+        assert ((out[r].cpu().double() - o).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_pages_past_32_bits(int8):
+    """Pages whose bytes lie more than 2^32 behind the first, whole and by regions."""
+    G, B, D, pages, n = 8, 128, 256, 9000, 300                          # 4.7 GB
+    cache = torch.zeros(pages, G, B, 2 * D, dtype=torch.int8 if int8 else torch.uint8, device="cuda")
+    scales = torch.zeros(pages, G, B // 64, 2, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    ids = [8999, 8400, 8998]
+    cache[ids] = torch.randint(0, 0x7E, (3, G, B, 2 * D), generator=gen, device="cuda").to(cache.dtype)
+    scales[ids] = torch.rand(3, G, B // 64, 2, generator=gen, device="cuda") * 0.02 + 0.01
+    near_cache, near_scales = cache[ids].contiguous(), scales[ids].contiguous()
+    query = torch.randn(G, 4, D, generator=gen, device="cuda").bfloat16()
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    outs = []
+    for c, s, table in ((cache, scales, i32([ids])), (near_cache, near_scales, i32([[0, 1, 2]]))):
+        outs.append([torch.zeros_like(query) for _ in range(2)])
+        sda.sparse_decode_quantised_paged_attention(query, c, s, table, i32([n]), outs[-1][0], scale=0.06)
+        sda.sparse_decode_quantised_attention(query, c, s, i32([[4, 0, 2]] * G), table, i32([n - 1] * G),
+                                              torch.ones(G, dtype=torch.bool, device="cuda"), outs[-1][1], scale=0.06, region_tokens=64)
+    for a, b in zip(*outs):
+        assert torch.equal(a, b) and a.abs().sum() > 0
