@@ -1170,7 +1170,6 @@ __global__ void __launch_bounds__(kThreads, Shape<KIND, D, MT, FULL, TAKERS, WAL
                     from[k] += __shfl_xor_sync(~0u, from[k], 1);
                     from[k] += __shfl_xor_sync(~0u, from[k], 2);
                     from[k] *= -kKeyBias * kKeyUnit;
-                    sl[k] *= 1.0f / kKeyUnit;
                 }
             }
         }
@@ -1274,6 +1273,10 @@ __global__ void __launch_bounds__(kThreads, Shape<KIND, D, MT, FULL, TAKERS, WAL
                         const float2 tile_scales = lds64(scale_base + ring * S::kStageScales + i * tile_scale_step);
                         sl0 *= tile_scales.x;
                         sl1 *= tile_scales.x;
+                        if constexpr (INT8) {   // not before the key scale: next to a large query it would overflow
+                            sl0 *= 1.0f / kKeyUnit;
+                            sl1 *= 1.0f / kKeyUnit;
+                        }
                         // where nothing was loaded it may be anything
                         of_value[i] = kPlain || ((loaded >> (8 * i)) & 0xFFull) ? tile_scales.y : 0.0f;
                         top_scale = fmaxf(top_scale, of_value[i]);
