@@ -465,8 +465,9 @@ sda_status sparse_decode_paged_attention(const sda_tensor *query, const sda_tens
  * The rows of a block stand next to each other, in the order of their places and
  * with no place between them left out, as sparse_decode_plan_step gives them: from
  * the first that does not on, a block's rows are left out with SDA_FLAG_BOUNDS.  So
- * is a slot outside the cache.  Rows of one block in two places of `slots` make its
- * contents a mix of the two.
+ * is a slot outside the cache.  Rows of one block must not stand in two places of
+ * `slots`, rows of others or padding between them: its contents would be a mix of the
+ * two.  Of calls of up to 2^16 rows SDA_FLAG_BOUNDS tells of it.
  * D is a multiple of 16 up to 512, pages * B below 2^32 - 1.  stride[2] == 1 (cache:
  * stride[3] == 1); bases and the other byte strides of key, value and cache are
  * multiples of 16, those of scales of 8, else SDA_ERR_UNSUPPORTED.  Returns SDA_ERR_INVALID for shapes,

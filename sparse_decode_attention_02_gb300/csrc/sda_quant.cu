@@ -20,6 +20,8 @@
 // the second pass.  16,363 tokens of 4 heads of 192 dims: 20 us in E4M3, 25 in integers
 // (75.5 MB, floor 11; 15.7 from L2: bound by the start and by the chain slots, run, rows,
 // maximum, stores of 3.4 waves of CTAs); a decode batch of 256 4.0 us, one token 3.4.
+// The first CTAs write nothing: they look for a block whose rows stand in two places, which
+// would be two runs that race for its scale and its places.
 //
 // Read.  One pass, bound by memory: a byte in and two out an element.  A thread keeps
 // to 16 elements of a head's row and walks over tokens, whose places are looked up
@@ -38,6 +40,10 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 // Rows that a CTA lists runs of: a prompt's blocks of 64 tokens one each (20 us; with 32 rows 25, with 128 27).
 constexpr int kMaxChunk = 64;
+// A CTA that looks for blocks in two places takes those that begin in kLookRows rows and compares
+// them with as many rows behind as kLookParts such parts have (10 us): each of the T / kLookRows
+// parts with all behind it, which of more rows than kMaxLooked would be the whole call.
+constexpr int kLookBits = 11, kLookRows = 1 << kLookBits, kLookParts = 8, kMaxLooked = 1 << 16;
 // 8-element pieces that a thread keeps between the passes, the rest is loaded again: what
 // four CTAs an SM have registers for, and 64 tokens of 192 dims need (six 22.6 us, three CTAs with eight 22.4).
 constexpr int kKept = 7;
@@ -54,6 +60,7 @@ struct AppendParams {
     uint32_t cache_slots;                       // pages * block
     unsigned long long block_inv, span_inv, vecs_inv;       // inverse_of a page's places, a block's, 8-element pieces of a row
     int tokens, groups, dim, block, span, chunk;
+    int lookers, look_parts;                    // CTAs ahead of the others that look for blocks in two places; parts
 };
 
 // A run of rows in one block, of one head's keys or values.
@@ -216,6 +223,70 @@ struct Pieces {
     }
 };
 
+constexpr uint32_t kNone = ~0u;                 // not a slot, nor a block: there are fewer
+
+// Row r's slot; kNone for padding, with `outside` where it is not in the cache, and past the rows.
+__device__ __forceinline__ uint32_t slot_of(const AppendParams &p, int r, bool &outside)
+{
+    const int64_t slot = r >= 0 && r < p.tokens ? p.slots[r] : -1;
+    if (static_cast<uint64_t>(slot) < p.cache_slots)
+        return static_cast<uint32_t>(slot);
+    outside = outside || slot != -1;
+    return kNone;
+}
+
+// Whether a block of which rows begin (behind a row of another, or of none) in a part of the rows has
+// others that begin there too, or in the parts behind that are this looker's.  `blocks`: a hash
+// table with room for twice a part.
+__device__ __forceinline__ bool block_in_two_places(const AppendParams &p, uint32_t (&blocks)[2 * kLookRows], int looker)
+{
+    const int part = looker % p.look_parts, tid = static_cast<int>(threadIdx.x);
+    const int row0 = part * kLookRows, first = row0 + looker / p.look_parts * (kLookParts * kLookRows);
+    const int last = min(p.tokens, first + (kLookParts + 1) * kLookRows);       // in steps from `first`, the part itself left out
+    if (first >= p.tokens)
+        return false;
+    auto home = [](uint32_t b) { return (b * 2654435769u) >> (31 - kLookBits); };        // 2^32 / golden ratio
+    auto after = [](uint32_t at) { return (at + 1) % (2 * kLookRows); };
+    bool outside = false, twice = false;
+    // the block that row r begins, or kNone
+    auto begun = [&](int r) {
+        const uint32_t slot = slot_of(p, r, outside), before = slot_of(p, r - 1, outside);
+        const uint32_t block = quotient(slot, p.span_inv);
+        return slot != kNone && (before == kNone || quotient(before, p.span_inv) != block) ? block : kNone;
+    };
+    constexpr int kEach = kLookRows / kThreads;
+    uint32_t b[kEach];
+    auto load = [&](int from) {
+#pragma unroll
+        for (int k = 0; k < kEach; ++k)
+            b[k] = begun(from + k * kThreads + tid);
+    };
+    for (int i = tid; i < 2 * kLookRows; i += kThreads)
+        blocks[i] = kNone;
+    load(row0);
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kEach; ++k)
+        if (b[k] != kNone)
+            for (uint32_t at = home(b[k]), was;; at = after(at)) {
+                was = atomicCAS(&blocks[at], kNone, b[k]);
+                if (was == kNone || was == b[k]) {
+                    twice = twice || was == b[k];
+                    break;
+                }
+            }
+    __syncthreads();
+    for (int from = first + kLookRows; from < last; from += kLookRows) {
+        load(from);
+#pragma unroll
+        for (int k = 0; k < kEach; ++k)
+            if (b[k] != kNone)
+                for (uint32_t at = home(b[k]); blocks[at] != kNone; at = after(at))
+                    twice = twice || blocks[at] == b[k];
+    }
+    return twice;
+}
+
 template <bool INT8>
 __global__ void __launch_bounds__(kThreads, 4) sda_quantised_append_kernel(const __grid_constant__ AppendParams p)
 {
@@ -223,30 +294,30 @@ __global__ void __launch_bounds__(kThreads, 4) sda_quantised_append_kernel(const
     __shared__ uint32_t goes_on[kWarps];        // rows of the window that continue the one before, a bit each
     __shared__ int count;
     __shared__ uint32_t tops[2][kWarps];        // largest element of each warp, by turns
+    __shared__ uint32_t looked[2 * kLookRows];
     pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const unsigned units = 2 * p.groups;
-    const int unit = static_cast<int>(blockIdx.x % units);
-    const int row0 = static_cast<int>(blockIdx.x / units) * p.chunk;
+    if (static_cast<int>(blockIdx.x) < p.lookers) {
+        if (block_in_two_places(p, looked, static_cast<int>(blockIdx.x)))
+            atomicOr(p.flags, SDA_FLAG_BOUNDS);
+        return;
+    }
+    const unsigned units = 2 * p.groups, cta = blockIdx.x - p.lookers;
+    const int unit = static_cast<int>(cta % units);
+    const int row0 = static_cast<int>(cta / units) * p.chunk;
     const bool value = unit & 1;
     const int group = unit >> 1;
 
     // ---- Runs.  The window is a row a thread; a run begins where the row before lies in
     // another block (or nowhere).
-    constexpr uint32_t kNone = ~0u;             // not a slot: there are fewer
-    auto slot_of = [&](int r) {
-        const int64_t slot = r >= 0 && r < p.tokens ? p.slots[r] : -1;
-        if (static_cast<uint64_t>(slot) < p.cache_slots)
-            return static_cast<uint32_t>(slot);
-        if (slot != -1 && p.flags)
-            atomicOr(p.flags, SDA_FLAG_BOUNDS);
-        return kNone;
-    };
     if (threadIdx.x == 0)
         count = 0;
     const int r = row0 + static_cast<int>(threadIdx.x);         // < 2^29
-    const uint32_t slot = slot_of(r), before = slot_of(r - 1);
+    bool outside = false;
+    const uint32_t slot = slot_of(p, r, outside), before = slot_of(p, r - 1, outside);
+    if (outside && p.flags)
+        atomicOr(p.flags, SDA_FLAG_BOUNDS);
     const bool joins = slot != kNone && before != kNone && quotient(slot, p.span_inv) == quotient(before, p.span_inv);
     const unsigned on = __ballot_sync(~0u, joins && slot == before + 1);
     if (lane == 0)
@@ -641,7 +712,11 @@ extern "C" sda_status sparse_decode_quantised_append(const sda_tensor *key, cons
     p.chunk = kMaxChunk;
     while (p.chunk > kWarps && (tokens + p.chunk - 1) / p.chunk * 2 * groups < 2 * sms)
         p.chunk /= 2;
-    const int64_t ctas = (tokens + p.chunk - 1) / p.chunk * 2 * groups;
+    if (p.flags && tokens > 1 && tokens <= kMaxLooked) {
+        p.look_parts = static_cast<int>((tokens + kLookRows - 1) / kLookRows);
+        p.lookers = p.look_parts * ((p.look_parts + kLookParts - 1) / kLookParts);
+    }
+    const int64_t ctas = (tokens + p.chunk - 1) / p.chunk * 2 * groups + p.lookers;
     if (ctas > INT32_MAX)
         return SDA_ERR_UNSUPPORTED;
     auto kernel = q.int8 ? sda_quantised_append_kernel<true> : sda_quantised_append_kernel<false>;
