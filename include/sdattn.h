@@ -468,11 +468,13 @@ sda_status sparse_decode_paged_attention(const sda_tensor *query, const sda_tens
  * is a slot outside the cache.  Rows of one block must not stand in two places of
  * `slots`, rows of others or padding between them: its contents would be a mix of the
  * two.  Of calls of up to 2^16 rows SDA_FLAG_BOUNDS tells of it.
- * D is a multiple of 16 up to 512, pages * B below 2^32 - 1.  stride[2] == 1 (cache:
- * stride[3] == 1); bases and the other byte strides of key, value and cache are
- * multiples of 16, those of scales of 8, else SDA_ERR_UNSUPPORTED.  Returns SDA_ERR_INVALID for shapes,
- * dtypes or strides outside this contract, SDA_ERR_WORKSPACE for a bad workspace,
- * SDA_ERR_CUDA if the launch failed; T == 0 returns SDA_OK with no launch.
+ * T is at most 2^28, D a multiple of 16 up to 512, G at most 2^16, B at most 2^24, pages
+ * below 2^31 and pages * B below 2^32 - 1; stride[2] == 1 (cache: stride[3] == 1); bases
+ * and the other byte strides of key, value and cache are multiples of 16, those of
+ * scales of 8; the strides of cache and scales are not 0: else SDA_ERR_UNSUPPORTED (for
+ * the innermost stride SDA_ERR_INVALID).  Returns SDA_ERR_INVALID for other shapes, dtypes
+ * or strides outside this contract, SDA_ERR_WORKSPACE for a bad workspace, SDA_ERR_CUDA if
+ * the launch failed; T == 0 returns SDA_OK with no launch.
  */
 sda_status sparse_decode_quantised_append(const sda_tensor *key, const sda_tensor *value,
                                           const sda_tensor *slots, const sda_tensor *cache,
@@ -493,8 +495,9 @@ sda_status sparse_decode_quantised_append(const sda_tensor *key, const sda_tenso
  *                  first_tokens[q] + i.  Other rows are left as they were.
  *   workspace      as in sparse_decode_quantised_append.
  * A token whose table column is past the width or whose page is outside the cache
- * leaves its row as it was, with SDA_FLAG_BOUNDS.  Limits and errors as for
- * sparse_decode_quantised_append.
+ * leaves its row as it was, with SDA_FLAG_BOUNDS.  T and Q are at most 2^30 and W is
+ * below 2^31, else SDA_ERR_UNSUPPORTED; other limits and errors as for
+ * sparse_decode_quantised_append, but pages * B has none.
  */
 sda_status sparse_decode_quantised_read(const sda_tensor *cache, const sda_tensor *scales,
                                         const sda_tensor *block_table, const sda_tensor *token_starts,
@@ -508,7 +511,9 @@ sda_status sparse_decode_quantised_read(const sda_tensor *cache, const sda_tenso
  *   cache, scales  as in sparse_decode_quantised_append; finite scales >= 0.
  *   query, block_table, seq_lens, output, lse, scale, query_len, gate, workspace,
  *   stream         as in sparse_decode_paged_attention (the workspace of
- *                  sparse_decode_paged_workspace_bytes).
+ *                  sparse_decode_paged_workspace_bytes), as are limits and errors.  G is
+ *                  at most 2^16, B at most 2^24, pages and W are below 2^31, rows at most
+ *                  2^25 - 1, else SDA_ERR_UNSUPPORTED.
  * The scales enter in fp32: a block's key scale multiplies its logits, its value
  * scale its weights.  (Integer keys are multiplied with 128 added, which the sums
  * take out again: their logits round by the size of 255 |q| * key scale.)  Weights times value scales have 11 bits down to 2^-27 of the
@@ -558,8 +563,9 @@ size_t sparse_decode_quantised_workspace_bytes(int64_t rows, int heads, int head
  * row that sees no token is +0.0.  Equal inputs give equal bits.  A region id below
  * -1, a table column past the width or an entry outside the cache leaves its tokens
  * out with SDA_FLAG_BOUNDS.  rows must be tokens * G; requests = ceil(rows / (G *
- * query_len)); rows below 2^25 - 1, R at most 2^20 and R * region_tokens below 2^31 -
- * 4096, else SDA_ERR_UNSUPPORTED.
+ * query_len)); rows at most 2^25 - 1, R at most 2^20, region_tokens at most 2^24 and
+ * R * region_tokens below 2^31 - 4096, else SDA_ERR_UNSUPPORTED.  Other limits and errors
+ * as for sparse_decode_quantised_paged_attention.
  */
 sda_status sparse_decode_quantised_attention(const sda_tensor *query, const sda_tensor *cache,
                                              const sda_tensor *scales, const sda_tensor *regions,
