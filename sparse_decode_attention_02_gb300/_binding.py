@@ -628,7 +628,10 @@ def sparse_decode_quantised_paged_attention(query, cache, scales, block_table, s
 
 
 def quantised_workspace_bytes(rows: int, heads: int, head_dim: int = 192) -> int:
-    return load().sparse_decode_quantised_workspace_bytes(operator.index(rows), _int32(heads), _int32(head_dim))
+    rows = operator.index(rows)
+    if not -2 ** 63 <= rows < 2 ** 63:
+        raise OverflowError("an argument does not fit 64 bits")
+    return load().sparse_decode_quantised_workspace_bytes(rows, _int32(heads), _int32(head_dim))
 
 
 def sparse_decode_quantised_attention(query, cache, scales, regions, block_table, positions, active, output, *,

@@ -1,8 +1,9 @@
 """The sizes up to which the quantised cache's entry points go: one past each is refused, the last one is not (it gets
-as far as a workspace that is refused, or has no rows; descriptors with made-up addresses, nothing is launched)."""
+as far as a workspace that is refused; descriptors with made-up addresses, nothing is launched)."""
 import pytest
 
-from test_quantised_abi_cpu import BF16, F32, I32, I64, OK, U8, UNS, WS, append, lib, paged, read, regions, t  # noqa: F401
+import sparse_decode_attention_02_gb300 as sda
+from test_quantised_abi_cpu import F32, U8, UNS, WS, append, lib, paged, read, regions, t  # noqa: F401
 
 BAD = dict(ws=1 << 24, wsb=128)                # a workspace that is too small, looked at after the sizes
 
@@ -77,3 +78,10 @@ def test_strides_of_nothing(lib, entry):  # noqa: F811
         cache[at] = scales[at] = 0
         assert entry(lib, **(both() | dict(cache=t(U8, (5, 2, 16, 128), tuple(cache))))) == UNS
         assert entry(lib, **(both() | dict(scales=t(F32, (5, 2, 2, 2), tuple(scales))))) == UNS
+
+
+def test_workspace_bytes_of_rows_past_64_bits(lib):  # noqa: F811
+    for rows in (1 << 63, 1 << 64, (1 << 64) + 5, -(1 << 63) - 1):
+        with pytest.raises(OverflowError):
+            sda.quantised_workspace_bytes(rows, 8)
+    assert sda.quantised_workspace_bytes((1 << 63) - 1, 8) == sda.quantised_workspace_bytes(-(1 << 63), 8) == 0
