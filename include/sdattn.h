@@ -508,7 +508,8 @@ sda_status sparse_decode_quantised_read(const sda_tensor *cache, const sda_tenso
 /*
  * sparse_decode_paged_attention over a quantised cache.
  *
- *   cache, scales  as in sparse_decode_quantised_append; finite scales >= 0.
+ *   cache, scales  as in sparse_decode_quantised_append; scales from 0 to 2^126 (what
+ *                  is quantised from bf16 needs no more than 2^121).
  *   query, block_table, seq_lens, output, lse, scale, query_len, gate, workspace,
  *   stream         as in sparse_decode_paged_attention (the workspace of
  *                  sparse_decode_paged_workspace_bytes), as are limits and errors.  G is
@@ -516,7 +517,9 @@ sda_status sparse_decode_quantised_read(const sda_tensor *cache, const sda_tenso
  *                  2^25 - 1, else SDA_ERR_UNSUPPORTED.
  * The scales enter in fp32: a block's key scale multiplies its logits, its value
  * scale its weights.  (Integer keys are multiplied with 128 added, which the sums
- * take out again: their logits round by the size of 255 |q| * key scale.)  Weights times value scales have 11 bits down to 2^-27 of the
+ * take out again: their logits round by the size of 255 |q| * key scale.)  Any finite
+ * query will do as long as scale * q.k fits in fp32 and scale * |q| is below 2^140 and,
+ * times a key scale, below 2^116.  Weights times value scales have 11 bits down to 2^-27 of the
  * product of the row's largest weight and the largest value scale that is met, and
  * below that are off by 2^-38 of it at most.  Scales of blocks that no visible token
  * lies in may hold anything.
@@ -541,7 +544,8 @@ size_t sparse_decode_quantised_workspace_bytes(int64_t rows, int heads, int head
  * sparse_decode_paged_attention.
  *
  *   query          [rows, H, D] bf16, H in 1..16, D in {64, 128, 192, 256}.
- *   cache, scales  as in sparse_decode_quantised_append; finite scales >= 0.
+ *   cache, scales  as in sparse_decode_quantised_append; scales from 0 to 2^126 (what
+ *                  is quantised from bf16 needs no more than 2^121).
  *   regions, block_table, positions, active, output, scale, query_len, gate,
  *   clear_inactive, region_tokens, stream  as in sparse_decode_attention, but that
  *                  any region_tokens and B will do whose greatest common divisor is a
