@@ -17,16 +17,20 @@
 // first is written.  A CTA lists the runs that begin in some rows, once for all of its
 // warps, and a team of them takes each: all eight where there is one (a prompt's block), a
 // warp where there are many (a decode batch).  A run's first loads stay in registers for
-// the second pass.  16,363 tokens of 4 heads of 192 dims: 20 us in E4M3, 25 in integers
+// the second pass.  16,363 tokens of 4 heads of 192 dims: 18 to 19 us in E4M3, 24 in integers
 // (75.5 MB, floor 11; 15.7 from L2: bound by the start and by the chain slots, run, rows,
-// maximum, stores of 3.4 waves of CTAs); a decode batch of 256 4.0 us, one token 3.4.
+// maximum, stores of 3.4 waves of CTAs); a decode batch of 256 3.7 to 4.2 us, one token 2.3.
+// Those batches are steps in which no scale grows.  One in which every block's does, with 15
+// places before the row to round again on average, takes 14.5 us, integers 16.3 (4.9 and 5.1
+// without, from as many caches in turn): a warp does a head's keys or values alone.
 // The first CTAs write nothing: they look for a block whose rows stand in two places, which
 // would be two runs that race for its scale and its places.
 //
 // Read.  One pass, bound by memory: a byte in and two out an element.  A thread keeps
 // to 16 elements of a head's row and walks over tokens, whose places are looked up
 // once for a CTA.  131,003 tokens of the same heads 92 us, 6.5 TB/s; twelve contexts of 2K to
-// 8K (integers, 2 heads of 128 dims) 17 us, where the look-ups before the first store are a third.
+// 8K (integers, 2 heads of 128 dims) 17 us (13 where the reads' 25 MB lie in L2), where the
+// look-ups before the first store are a third.
 #include "sda_quant.cuh"
 
 #include <algorithm>
@@ -484,7 +488,8 @@ __global__ void __launch_bounds__(kThreads, 4) sda_quantised_append_kernel(const
 // ---------------------------------------------------------------------------
 
 // Rows of a thread, at most: six CTAs an SM with four loads each in flight (twelve contexts
-// 17.3 us; eight rows at four CTAs 22.6, at three 21.3).
+// 17.3 us; eight rows at four CTAs 22.6, at three 21.3), which leave a thread 40 registers and
+// spill 12 bytes of it beside E4M3, 4 beside integers.
 constexpr int kReadTurns = 4;
 constexpr int kMaxReadRows = kThreads / 2 * kReadTurns;         // of a CTA (16 dims: two threads a row)
 

@@ -28,8 +28,10 @@ __device__ __forceinline__ uint32_t bytes_of(uint32_t a, uint32_t b)
 }
 
 // 8-bit integers to fp16, exactly: byte + 128 in the low bits of 1024 is 1152 more
-// than the integer.  `biased`: the word with each byte's top bit flipped; A, B: which
-// of its bytes go to the low and the high half.
+// than the integer (a conversion by byte permutes as in Kim et al., "Who Says Elephants
+// Can't Run: Bringing Large Scale MoE Models into Cloud Scale Production", 2022).
+// `biased`: the word with each byte's top bit flipped; A, B: which of its bytes go to
+// the low and the high half.
 template <int A, int B>
 __device__ __forceinline__ uint32_t int8x2_to_f16x2(uint32_t biased)
 {
