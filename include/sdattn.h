@@ -467,7 +467,7 @@ sda_status sparse_decode_paged_attention(const sda_tensor *query, const sda_tens
  * the first that does not on, a block's rows are left out with SDA_FLAG_BOUNDS.  So
  * is a slot outside the cache.  Rows of one block must not stand in two places of
  * `slots`, rows of others or padding between them: its contents would be a mix of the
- * two.  Of calls of up to 2^16 rows SDA_FLAG_BOUNDS tells of it.
+ * two.  Of calls of up to 2^14 rows SDA_FLAG_BOUNDS tells of it.
  * T is at most 2^28, D a multiple of 16 up to 512, G at most 2^16, B at most 2^24, pages
  * below 2^31 and pages * B below 2^32 - 1; stride[2] == 1 (cache: stride[3] == 1); bases
  * and the other byte strides of key, value and cache are multiples of 16, those of

@@ -74,11 +74,12 @@ def test_without_a_workspace_nothing_is_looked_for():
     assert torch.equal(c.scales.view(-1, 2, 2, 2)[1:], before.view(-1, 2, 2, 2)[1:])
 
 
-@pytest.mark.parametrize("at", [(5, 39000), (2100, 18431), (2047, 2048 + 16384), (20000, 36864), (39997, 39999), None])
-def test_rows_far_apart(at):
-    """More rows than one CTA compares with a part of them."""
+@pytest.mark.parametrize("rows,at", [(16384, (5, 16000)), (16384, (2046, 2048)), (16384, (2100, 14336)), (16384, (14335, 16383)),
+                                     (12289, (4097, 12288)), (16384, None), (40000, None)])
+def test_rows_far_apart(rows, at):
+    """As many rows as are looked at, in any two of their parts; in order, and more of them."""
     c = Cache(pages=85, G=1, B=512, S=512, D=16)
-    slots = slots_of(list(range(80)), 5, 40000, 512)
+    slots = slots_of(list(range(80)), 5, rows, 512)
     gen = torch.Generator().manual_seed(7)
     if at is None:
         c.append(*c.rows(len(slots), gen), slots, flags=0)
