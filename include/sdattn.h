@@ -519,9 +519,11 @@ sda_status sparse_decode_quantised_read(const sda_tensor *cache, const sda_tenso
  * scale its weights.  (Integer keys are multiplied with 128 added, which the sums
  * take out again: their logits round by the size of 255 |q| * key scale.)  Any finite
  * query will do as long as scale * q.k fits in fp32 and scale * |q| is below 2^140 and,
- * times a key scale, below 2^116.  Weights times value scales have 11 bits down to 2^-27 of the
- * product of the row's largest weight and the largest value scale that is met, and
- * below that are off by 2^-38 of it at most.  Scales of blocks that no visible token
+ * times a key scale, below 2^116.  Weights times value scales have 11 bits down to 2^-26 of
+ * the product of the row's largest weight and the largest value scale of a token that
+ * all query tokens of the request see, and below that are off by 2^-37 of it at most;
+ * tokens that only the later ones see are weighed in fp32.  Scales of tokens that a row
+ * does not see, up to 2^100 times those of tokens that it does, change nothing of it.  Scales of blocks that no visible token
  * lies in may hold anything.
  */
 sda_status sparse_decode_quantised_paged_attention(const sda_tensor *query, const sda_tensor *cache,

@@ -183,6 +183,10 @@ constexpr int tiles_of_rows(int rows)
     return rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
 }
 
+// Value scales of up to 2^90 units, times weights below 2^15 and elements below 2^9, leave
+// outputs room in fp32.
+constexpr float kFarBelow = 0x1p-90f;
+
 constexpr int kStateBytes = 136;                // WarpState
 
 // FULL: a piece fills a stage (pages of at least a stage's tokens, in whole
@@ -470,6 +474,12 @@ __device__ __forceinline__ float fast_exp2(float x)
 __device__ __forceinline__ float reciprocal_of_power(float x)
 {
     return __uint_as_float((254u << 23) - __float_as_uint(x));
+}
+
+// The least power of two from x on, at most 2^126 (x > 0).
+__device__ __forceinline__ float power_from(float x)
+{
+    return __uint_as_float(min((__float_as_uint(x) + 0x7FFFFFu) & 0x7F800000u, 253u << 23));
 }
 
 // The headwise gate: sigmoid in fp32, rounded to bf16.
@@ -1188,8 +1198,9 @@ __global__ void __launch_bounds__(kThreads, Shape<KIND, D, MT, FULL, TAKERS, WAL
         for (int n = 0; n < D / 8; ++n)
             o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
         float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.0f, 0.0f};
-        // Outputs of a quantised cache are in units of a power of two that is at least
-        // the largest value scale so far, so that weights times scales fit fp16.
+        // Outputs of a quantised cache are in units of a power of two that is at least the
+        // largest value scale so far of tokens that all rows see, so that weights times
+        // scales fit fp16.
         float unit = kSmallestScale;
 
         for (; left > 0; --left, common -= FULL ? S::kSlots : p.tile) {
@@ -1264,7 +1275,9 @@ __global__ void __launch_bounds__(kThreads, Shape<KIND, D, MT, FULL, TAKERS, WAL
                 float mx0 = -INFINITY, mx1 = -INFINITY;
                 const uint64_t s0 = kPlain ? kAll : loaded & low_bits(common + j0);
                 const uint64_t s1 = kPlain ? kAll : loaded & low_bits(common + j1);
-                // The value scales of the tiles, then what their weights are multiplied by.
+                const uint64_t seen = kPlain ? kAll : loaded & low_bits(common);       // by all rows
+                // The value scales of the tiles that all rows see, then what their weights are
+                // multiplied by.
                 float of_value[SCALED ? NT : 1], top_scale = 0.0f;
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
@@ -1278,7 +1291,7 @@ __global__ void __launch_bounds__(kThreads, Shape<KIND, D, MT, FULL, TAKERS, WAL
                             sl1 *= 1.0f / kKeyUnit;
                         }
                         // where nothing was loaded it may be anything
-                        of_value[i] = kPlain || ((loaded >> (8 * i)) & 0xFFull) ? tile_scales.y : 0.0f;
+                        of_value[i] = kPlain || ((seen >> (8 * i)) & 0xFFull) ? tile_scales.y : 0.0f;
                         top_scale = fmaxf(top_scale, of_value[i]);
                     }
 #pragma unroll
@@ -1306,8 +1319,8 @@ __global__ void __launch_bounds__(kThreads, Shape<KIND, D, MT, FULL, TAKERS, WAL
                     m_run[1] = n1;
                     l_run[0] *= a0;
                     l_run[1] *= a1;
-                    if (SCALED && top_scale > unit) {           // the next power of two, at most 2^126
-                        const float more = __uint_as_float(min((__float_as_uint(top_scale) + 0x7FFFFFu) & 0x7F800000u, 253u << 23));
+                    if (SCALED && top_scale > unit) {
+                        const float more = power_from(top_scale);
                         const float less = unit * reciprocal_of_power(more);
                         unit = more;
                         a0 *= less;
@@ -1341,7 +1354,6 @@ __global__ void __launch_bounds__(kThreads, Shape<KIND, D, MT, FULL, TAKERS, WAL
 
                 // ---- O += P V.  P in 11 bits (fp16, next to E4M3 values' 4), or in
                 // two bf16 parts.  Tokens that only some rows see come below.
-                const uint64_t seen = kPlain ? kAll : loaded & low_bits(common);
                 auto both = [&](uint32_t km, int s) {           // V words of slots s, s + 4
                     return (((km >> s) & 1u) ? 0x0000FFFFu : 0u) | (((km >> (s + 4)) & 1u) ? 0xFFFF0000u : 0u);
                 };
@@ -1382,8 +1394,9 @@ __global__ void __launch_bounds__(kThreads, Shape<KIND, D, MT, FULL, TAKERS, WAL
                 }
                 // ---- The newest query_len - 1 tokens, which only some rows see:
                 // one at a time in fp32, so that a value that is not a number
-                // reaches the rows that see it alone.
-                if constexpr (!kPlain) {
+                // reaches the rows that see it alone, and a larger value scale
+                // costs no row that does not see it bits of its weights.
+                if constexpr (!kPlain && !REGIONS) {
                     for (uint64_t rest = loaded & ~seen & low_bits(common + p.query_len - 1); rest; rest &= rest - 1) {
                         const int s = __ffsll(static_cast<long long>(rest)) - 1;
                         float p0 = 0.0f, p1 = 0.0f;
@@ -1393,14 +1406,26 @@ __global__ void __launch_bounds__(kThreads, Shape<KIND, D, MT, FULL, TAKERS, WAL
                             if ((s >> 3) == i) {
                                 p0 = (s & 4) ? sc[i][1] : sc[i][0];
                                 p1 = (s & 4) ? sc[i][3] : sc[i][2];
-                                if constexpr (SCALED) {
-                                    p0 *= of_value[i];
-                                    p1 *= of_value[i];
-                                }
                                 off = tile_off[i];
                             }
                         p0 = __shfl_sync(~0u, p0, (lane & ~3) | (s & 3));
                         p1 = __shfl_sync(~0u, p1, (lane & ~3) | (s & 3));
+                        if constexpr (SCALED) {
+                            const float of = lds64(scale_base + ring * S::kStageScales + (s >> 3) * tile_scale_step).y;
+                            if (of * kFarBelow > unit) {        // the outputs so far keep their bits, down to fp32's least
+                                const float more = power_from(of), less = unit * reciprocal_of_power(more);
+                                unit = more;
+#pragma unroll
+                                for (int n = 0; n < D / 8; ++n) {
+                                    o[n][0] *= less;
+                                    o[n][1] *= less;
+                                    o[n][2] *= less;
+                                    o[n][3] *= less;
+                                }
+                            }
+                            p0 *= of * reciprocal_of_power(unit);
+                            p1 *= of * reciprocal_of_power(unit);
+                        }
                         const bool see0 = s < common + j0, see1 = s < common + j1;
                         const uint32_t vrow = sb + off + (s & 7) * 128u + 4 * t;
                         constexpr int kFirst = D * S::kElt / 16;
