@@ -45,9 +45,9 @@
 // Two more kinds of cache have elements of a byte and a scale for each block of tokens and
 // head, one for keys, which multiplies logits, one for values, which multiplies weights;
 // and of those a row's selected regions can be walked instead of a request's tokens.
-// 16 documents of 64K to 128K tokens (192 dims, 4 groups): E4M3 377 to 379 us, 6.6 TB/s
+// 16 documents of 64K to 128K tokens (192 dims, 4 groups): E4M3 377 to 380 us, 6.6 TB/s
 // (one scale for all: 370 to 376), integers 414, 6.1 TB/s, bound by their conversions; 512 rows of
-// 1024 regions of 8 tokens (E4M3, 192 dims) 291 us, 5.6 TB/s, in TMA boxes of 3 KB.
+// 1024 regions of 8 tokens (E4M3, 192 dims) 284 us, 5.7 TB/s, in TMA boxes of 3 KB.
 #pragma once
 
 #include "sda_quant.cuh"
